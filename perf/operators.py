@@ -217,10 +217,10 @@ def _plain_quant(x, pow2: bool):
     x = torch.nn.functional.pad(x.float(), (0, _blocks(K) * BLK - K)).view(M, _blocks(K), BLK)
     a = x.abs().amax(2)
     sc = a / torch.full_like(a, E4M3_MAX)  # (by a tensor: by a number it would be a product with 1 / 448)
+    sc = torch.clamp(sc, min=MIN_SCALE)
     if pow2:
         m, e = torch.frexp(sc)
         sc = torch.ldexp(torch.ones_like(sc), torch.where(m == 0.5, e - 1, e))
-    sc = torch.clamp(sc, min=MIN_SCALE)
     sc = torch.where(torch.isfinite(a), sc, math.nan)
     q = torch.where(torch.isfinite(sc)[:, :, None], x / sc[:, :, None], 0.0)
     return [q.view(M, -1)[:, :K].to(torch.float8_e4m3fn), sc.t().contiguous()]
