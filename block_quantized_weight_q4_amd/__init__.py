@@ -1,7 +1,8 @@
-"""Block-quantized (ggml Q4_0 / Q4_K / Q6_K) weight products on MI355X.
+"""Block-quantized weight products on MI355X: ggml Q4_0 / Q4_K / Q5_K / Q6_K, and
+e4m3 with a scale for each 128 x 128 block (``gq_f8_*``).
 
 The compute lives in ``libgq.so`` (HIP kernels for gfx950 behind the C ABI of
-``include/gq.h``); :mod:`._binding` is a thin ctypes layer with the same entry
+``include/gq.h`` and ``include/gq_f8.h``); :mod:`._binding` is a thin ctypes layer with the same entry
 point names that marshals torch tensors (device memory, streams) into it.
 
 The binding is loaded on first use, so ``block_quantized_weight_q4_amd.synth``
@@ -10,7 +11,9 @@ The binding is loaded on first use, so ``block_quantized_weight_q4_amd.synth``
 __all__ = [
     "gq_abi_version", "gq_block_info", "gq_dequant", "gq_matvec", "gq_matvec_id",
     "gq_matvec_id_workspace", "gq_matvec_id_check", "gq_matmul", "gq_route_topk", "gq_matvec_glu",
-    "gq_matvec_id_glu", "gq_matvec_id_noalloc", "gq_route_topk_plan", "gq_route_matvec_id_glu", "GqError", "TYPES", "lib_path",
+    "gq_matvec_id_glu", "gq_matvec_id_noalloc", "gq_route_topk_plan", "gq_route_matvec_id_glu",
+    "gq_f8_quant", "gq_f8_glu_quant", "gq_f8_matvec", "gq_f8_matmul", "gq_f8_matmul_id", "gq_f8_matmul_id_workspace",
+    "gq_f8_matmul_id_check", "gq_route_scored", "GqError", "TYPES", "lib_path",
 ]
 
 

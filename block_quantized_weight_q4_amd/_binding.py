@@ -51,10 +51,25 @@ if hasattr(_lib, "gq_route_matvec_id_glu"):
 _lib.gq_matvec_glu.argtypes = [ctypes.c_int, P, P, I64, I64, P, ctypes.c_int, I32, ctypes.c_int, P, ctypes.c_int, P]
 _lib.gq_matvec_id_glu.argtypes = [ctypes.c_int, P, P, I32, I64, I64, P, I32, I32, P, ctypes.c_int, ctypes.c_int, P,
                                   ctypes.c_int, P, SZ, P]
+if hasattr(_lib, "gq_f8_quant"):  # gq_f8.h
+    _lib.gq_f8_quant.argtypes = [P, ctypes.c_int, I64, I64, I64, I32, P, I64, P, I64, P]
+    _lib.gq_f8_glu_quant.argtypes = [P, P, ctypes.c_int, I64, I64, I64, I64, ctypes.c_int, I32, P, I64, P, I64, P]
+    _lib.gq_f8_matvec.argtypes = [P, P, I64, I64, P, ctypes.c_int, I32, P, ctypes.c_int, P]
+    _lib.gq_f8_matmul.argtypes = [P, P, I64, I64, P, P, I64, I64, I64, P, ctypes.c_int, I64, P]
+    _lib.gq_f8_matmul_id_workspace.argtypes = [I32, I32, I32, I64, ctypes.c_int, I32, ctypes.POINTER(SZ)]
+    _lib.gq_f8_matmul_id.argtypes = [P, P, I32, I64, I64, P, I32, I32, P, P, I64, I64, I32, P, P, ctypes.c_int, P, SZ,
+                                     P]
+    _lib.gq_f8_matmul_id_check.argtypes = [P, P, ctypes.POINTER(I32)]
+    _lib.gq_route_scored.argtypes = [P, ctypes.c_int, I32, I32, I32, ctypes.c_int, P, I32, I32, ctypes.c_int, I32,
+                                     ctypes.c_float, P, P, P]
 ACTS = {"silu": 0, "gelu_tanh": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_RANKS = {"max": 0, "top2": 1}
 for _f in ("gq_block_info", "gq_dequant", "gq_matvec", "gq_matvec_id_workspace", "gq_matvec_id", "gq_matvec_id_noalloc",
            "gq_matvec_id_check", "gq_matmul", "gq_route_topk", "gq_route_topk_plan", "gq_matvec_glu",
-           "gq_matvec_id_glu", "gq_route_matvec_id_glu"):
+           "gq_matvec_id_glu", "gq_route_matvec_id_glu", "gq_f8_quant", "gq_f8_glu_quant", "gq_f8_matvec",
+           "gq_f8_matmul", "gq_f8_matmul_id_workspace", "gq_f8_matmul_id", "gq_f8_matmul_id_check",
+           "gq_route_scored"):
     if hasattr(_lib, _f):
         getattr(_lib, _f).restype = ctypes.c_int
 
@@ -407,6 +422,237 @@ def gq_route_matvec_id_glu(t, experts_gate: torch.Tensor, experts_up: torch.Tens
                                        _ptr(h), _DTYPES[h.dtype], _ptr(ws), ws.numel() * ws.element_size(),
                                        _stream(stream)))
     return h
+
+
+# --- block-scaled 8-bit products and the router with scores (gq_f8.h) --------
+# These take the sizes from the tensors' shapes, rows may have a stride of
+# their own, and the work goes to the current stream of the tensors' device,
+# whichever device is current.
+
+_F8 = (torch.float8_e4m3fn, torch.uint8)
+_HALF_OR_F32 = (torch.float32, torch.bfloat16, torch.float16)
+
+
+def _f8_blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Elements from one row to the next (of a single row: its length)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _f8_rows(name: str, t: torch.Tensor) -> None:
+    """_rows, but an empty tensor's strides say nothing."""
+    _need(t.dim() == 2, "%s must be 2-D" % name)
+    if t.numel():
+        _rows(name, t)
+
+
+def _shape(name: str, t: torch.Tensor, *shape) -> None:
+    _need(tuple(t.shape) == shape, "%s must be %s, not %s" % (name, list(shape), list(t.shape)))
+
+
+def _launch(fn: str, stream, device, *args) -> None:
+    """Calls the C entry point with the device current and its stream last."""
+    f = getattr(_lib, fn)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    else:
+        _need(stream.device == device, "stream belongs to %s, the tensors to %s" % (stream.device, device))
+    if device.index == torch.cuda.current_device():
+        _check(fn, f(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn, f(*args, stream.cuda_stream))
+
+
+def _one_device(**tensors) -> torch.device:
+    _on_gpu(**tensors)
+    device = None
+    for name, t in tensors.items():
+        if t is not None:
+            _need(device is None or t.device == device, "%s is on %s, other tensors on %s" % (name, t.device, device))
+            device = t.device
+    return device
+
+
+def _f8_scales(name: str, s: torch.Tensor, *shape) -> None:
+    _tensor(name, s, _F32)
+    _shape(name, s, *shape)
+
+
+def _quantised(q: torch.Tensor, scales: torch.Tensor, M: int, K: int) -> None:
+    _tensor("q", q, _F8)
+    _f8_rows("q", q)
+    _shape("q", q, M, K)
+    _f8_scales("scales", scales, _f8_blocks(K), M)
+    _f8_rows("scales", scales)
+
+
+def gq_f8_quant(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, pow2: bool = False,
+                stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """q, scales of x [M][K] (fp32 / bf16 / fp16): e4m3 bytes [M][K] and one
+    fp32 scale for 128 inputs of a row, [ceil(K / 128)][M]."""
+    _tensor("x", x, _HALF_OR_F32)
+    _f8_rows("x", x)
+    M, K = x.shape
+    _quantised(q, scales, M, K)
+    dev = _one_device(x=x, q=q, scales=scales)
+    _launch("gq_f8_quant", stream, dev, _ptr(x), _DTYPES[x.dtype], M, K, _ld(x), 1 if pow2 else 0, _ptr(q), _ld(q),
+            _ptr(scales), _ld(scales))
+    return q, scales
+
+
+def gq_f8_glu_quant(g: torch.Tensor, u: torch.Tensor, act: str, q: torch.Tensor, scales: torch.Tensor,
+                    pow2: bool = False, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """gq_f8_quant of act(g) * u; g, u [M][K] of one type (fp32 / bf16 / fp16)."""
+    _tensor("g", g, _HALF_OR_F32)
+    _tensor("u", u, (g.dtype,))
+    _f8_rows("g", g)
+    _f8_rows("u", u)
+    _need(act in ACTS, "act must be one of %s" % sorted(ACTS))
+    M, K = g.shape
+    _shape("u", u, M, K)
+    _quantised(q, scales, M, K)
+    dev = _one_device(g=g, u=u, q=q, scales=scales)
+    _launch("gq_f8_glu_quant", stream, dev, _ptr(g), _ptr(u), _DTYPES[g.dtype], M, K, _ld(g), _ld(u), ACTS[act],
+            1 if pow2 else 0, _ptr(q), _ld(q), _ptr(scales), _ld(scales))
+    return q, scales
+
+
+def _f8_weights(W: torch.Tensor, wscales: torch.Tensor, dims: int) -> tuple:
+    _tensor("W", W, _F8)
+    _need(W.dim() == dims, "W must be %d-D" % dims)
+    _contig("W", W)
+    *lead, N, K = W.shape
+    _f8_scales("wscales", wscales, *lead, _f8_blocks(N), _f8_blocks(K))
+    _contig("wscales", wscales)
+    return (*lead, N, K)
+
+
+def gq_f8_matvec(W: torch.Tensor, wscales: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
+                 stream=None) -> torch.Tensor:
+    """y [batch][N] (fp32 / bf16) = x [batch][K] (fp32 / bf16) times the
+    weights W [N][K] e4m3 with wscales [ceil(N / 128)][ceil(K / 128)]."""
+    N, K = _f8_weights(W, wscales, 2)
+    _tensor("x", x, _ACT)
+    _tensor("y", y, _ACT)
+    _need(x.dim() == 2 and x.shape[1] == K, "x must be [batch][%d]" % K)
+    _shape("y", y, x.shape[0], N)
+    _contig("x", x)
+    _contig("y", y)
+    dev = _one_device(W=W, wscales=wscales, x=x, y=y)
+    _launch("gq_f8_matvec", stream, dev, _ptr(W), _ptr(wscales), N, K, _ptr(x), _DTYPES[x.dtype], x.shape[0], _ptr(y),
+            _DTYPES[y.dtype])
+    return y
+
+
+def _f8_x(X: torch.Tensor, xscales: torch.Tensor, K: int) -> None:
+    _tensor("X", X, _F8)
+    _f8_rows("X", X)
+    _need(X.shape[1] == K, "X must have rows of K = %d" % K)
+    _f8_scales("xscales", xscales, _f8_blocks(K), X.shape[0])
+    _f8_rows("xscales", xscales)
+
+
+def gq_f8_matmul(W: torch.Tensor, wscales: torch.Tensor, X: torch.Tensor, xscales: torch.Tensor, Y: torch.Tensor,
+                 stream=None) -> torch.Tensor:
+    """Y [M][N] (fp32 / bf16) = X [M][K] e4m3 with xscales [ceil(K / 128)][M]
+    times the weights W [N][K] with wscales [ceil(N / 128)][ceil(K / 128)]."""
+    N, K = _f8_weights(W, wscales, 2)
+    _f8_x(X, xscales, K)
+    _tensor("Y", Y, _ACT)
+    _f8_rows("Y", Y)
+    M = X.shape[0]
+    _shape("Y", Y, M, N)
+    dev = _one_device(W=W, wscales=wscales, X=X, xscales=xscales, Y=Y)
+    _launch("gq_f8_matmul", stream, dev, _ptr(W), _ptr(wscales), N, K, _ptr(X), _ptr(xscales), M, _ld(X),
+            _ld(xscales), _ptr(Y), _DTYPES[Y.dtype], _ld(Y))
+    return Y
+
+
+def gq_f8_matmul_id_workspace(n_experts: int, n_tokens: int, top_k: int, N: int, y_dtype=torch.float32,
+                              weighted: bool = True) -> int:
+    b = SZ()
+    _need(y_dtype in _ACT, "y_dtype must be %s" % " or ".join(map(str, _ACT)), TypeError)
+    _check("gq_f8_matmul_id_workspace", _lib.gq_f8_matmul_id_workspace(
+        n_experts, n_tokens, top_k, N, _DTYPES[y_dtype], 1 if weighted else 0, ctypes.byref(b)))
+    return b.value
+
+
+def gq_f8_matmul_id(W: torch.Tensor, wscales: torch.Tensor, ids, X: torch.Tensor, xscales: torch.Tensor,
+                    Y: torch.Tensor, ws: torch.Tensor, route_w: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Routed product with the experts W [n_experts][N][K], wscales
+    [n_experts][ceil(N / 128)][ceil(K / 128)]; X [n_tokens][K], or
+    [n_tokens * top_k][K] with a row for each slot; Y [n_tokens][top_k][N], or
+    [n_tokens][N] weighted by route_w [n_tokens][top_k].  ids may be a
+    (n_tokens, top_k) tuple: the table already in ws is used."""
+    n_experts, N, K = _f8_weights(W, wscales, 3)
+    reuse = isinstance(ids, tuple)
+    n_tokens, top_k = ids if reuse else _ids(ids)
+    _f8_x(X, xscales, K)
+    rows = X.shape[0]
+    _need(rows == n_tokens or rows == n_tokens * top_k, "X must have n_tokens = %d or n_tokens * top_k = %d rows"
+          % (n_tokens, n_tokens * top_k))
+    _tensor("Y", Y, _ACT)
+    _contig("Y", Y)
+    if route_w is None:
+        _shape("Y", Y, n_tokens, top_k, N)
+    else:
+        _shape("Y", Y, n_tokens, N)
+        _tensor("route_w", route_w, _F32)
+        _shape("route_w", route_w, n_tokens, top_k)
+        _contig("route_w", route_w)
+    _workspace(ws)
+    dev = _one_device(W=W, wscales=wscales, ids=None if reuse else ids, X=X, xscales=xscales, Y=Y, ws=ws,
+                      route_w=route_w)
+    _launch("gq_f8_matmul_id", stream, dev, _ptr(W), _ptr(wscales), n_experts, N, K, None if reuse else _ptr(ids),
+            n_tokens, top_k, _ptr(X), _ptr(xscales), _ld(X), _ld(xscales), 0 if rows == n_tokens else 1,
+            _ptr(route_w), _ptr(Y), _DTYPES[Y.dtype], _ptr(ws), ws.numel())
+    return Y
+
+
+def gq_f8_matmul_id_check(ws: torch.Tensor, stream=None) -> int:
+    """Ids outside [0, n_experts) in the last gq_f8_matmul_id call given ids that used ws (waits for the stream)."""
+    _workspace(ws)
+    dev = _one_device(ws=ws)
+    n = I32()
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with torch.cuda.device(dev):
+        _check("gq_f8_matmul_id_check", _lib.gq_f8_matmul_id_check(_ptr(ws), stream.cuda_stream, ctypes.byref(n)))
+    return n.value
+
+
+def gq_route_scored(logits: torch.Tensor, top_k: int, ids: torch.Tensor, weights: torch.Tensor,
+                    score: str = "softmax", bias: torch.Tensor | None = None, n_groups: int = 1, top_groups: int = 1,
+                    group_rank: str = "max", renorm: bool = True, scale: float = 1.0,
+                    stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """ids / weights [n_tokens][top_k] (int32 / fp32) of fp32 or bf16 ``logits``
+    [n_tokens][n_experts]: softmax or sigmoid scores, chosen by score + bias
+    among the experts of the best top_groups of n_groups groups."""
+    _tensor("logits", logits, _ACT)
+    _tensor("ids", ids, _I32)
+    _tensor("weights", weights, _F32)
+    _need(logits.dim() == 2, "logits must be [n_tokens][n_experts]")
+    n_tokens, n_experts = logits.shape
+    _shape("ids", ids, n_tokens, top_k)
+    _shape("weights", weights, n_tokens, top_k)
+    _need(score in SCORES, "score must be one of %s" % sorted(SCORES))
+    _need(group_rank in GROUP_RANKS, "group_rank must be one of %s" % sorted(GROUP_RANKS))
+    if bias is not None:
+        _tensor("bias", bias, _F32)
+        _shape("bias", bias, n_experts)
+        _contig("bias", bias)
+    for name, v in (("logits", logits), ("ids", ids), ("weights", weights)):
+        _contig(name, v)
+    dev = _one_device(logits=logits, ids=ids, weights=weights, bias=bias)
+    _launch("gq_route_scored", stream, dev, _ptr(logits), _DTYPES[logits.dtype], n_tokens, n_experts, top_k,
+            SCORES[score], _ptr(bias), n_groups, top_groups, GROUP_RANKS[group_rank], 1 if renorm else 0, scale,
+            _ptr(ids), _ptr(weights))
+    return ids, weights
 
 
 # raw handle for the tests that check the exported symbols
