@@ -20,5 +20,6 @@ __all__ = [
 def __getattr__(name):
     if name in __all__:
         from . import _binding
-        return getattr(_binding, name)
+        globals()[name] = value = getattr(_binding, name)  # found directly from now on
+        return value
     raise AttributeError(name)

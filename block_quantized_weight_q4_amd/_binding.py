@@ -428,9 +428,24 @@ def gq_route_matvec_id_glu(t, experts_gate: torch.Tensor, experts_up: torch.Tens
 # These take the sizes from the tensors' shapes, rows may have a stride of
 # their own, and the work goes to the current stream of the tensors' device,
 # whichever device is current.
+#
+# A decode step makes these calls by the hundred and each costs the host more
+# than the GPU, so every function first tests that all is as it should be in
+# one expression of cheap properties (about 1 us); only if that fails the
+# checks run one by one, to name what is wrong -- or to pass, for the forms
+# that the short test leaves out (single rows, empty tensors).
 
 _F8 = (torch.float8_e4m3fn, torch.uint8)
 _HALF_OR_F32 = (torch.float32, torch.bfloat16, torch.float16)
+_f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
+
+
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same handle without building a Stream object, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _f8_blocks(n: int) -> int:
@@ -453,28 +468,29 @@ def _shape(name: str, t: torch.Tensor, *shape) -> None:
     _need(tuple(t.shape) == shape, "%s must be %s, not %s" % (name, list(shape), list(t.shape)))
 
 
-def _launch(fn: str, stream, device, *args) -> None:
-    """Calls the C entry point with the device current and its stream last."""
-    f = getattr(_lib, fn)
+def _launch(fn: str, f, index: int, stream, *args) -> None:
+    """Calls the C entry point with device ``index`` current and its stream last."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        s = _raw_stream(index)
     else:
-        _need(stream.device == device, "stream belongs to %s, the tensors to %s" % (stream.device, device))
-    if device.index == torch.cuda.current_device():
-        _check(fn, f(*args, stream.cuda_stream))
+        _need(stream.device.index == index, "stream belongs to %s, the tensors to cuda:%d" % (stream.device, index))
+        s = stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = f(*args, s)
     else:
-        with torch.cuda.device(device):
-            _check(fn, f(*args, stream.cuda_stream))
+        with torch.cuda.device(index):
+            status = f(*args, s)
+    if status:
+        raise GqError(fn, status)
 
 
-def _one_device(**tensors) -> torch.device:
+def _one_device(**tensors) -> None:
     _on_gpu(**tensors)
     device = None
     for name, t in tensors.items():
         if t is not None:
             _need(device is None or t.device == device, "%s is on %s, other tensors on %s" % (name, t.device, device))
             device = t.device
-    return device
 
 
 def _f8_scales(name: str, s: torch.Tensor, *shape) -> None:
@@ -482,73 +498,102 @@ def _f8_scales(name: str, s: torch.Tensor, *shape) -> None:
     _shape(name, s, *shape)
 
 
-def _quantised(q: torch.Tensor, scales: torch.Tensor, M: int, K: int) -> None:
+def _check_quant(x, q, scales, g=None, u=None) -> None:
+    _tensor("g" if u is not None else "x", x, _HALF_OR_F32)
+    _f8_rows("g" if u is not None else "x", x)
+    M, K = x.shape
+    if u is not None:
+        _tensor("u", u, (x.dtype,))
+        _f8_rows("u", u)
+        _shape("u", u, M, K)
     _tensor("q", q, _F8)
     _f8_rows("q", q)
     _shape("q", q, M, K)
     _f8_scales("scales", scales, _f8_blocks(K), M)
     _f8_rows("scales", scales)
+    _one_device(x=x, u=u, q=q, scales=scales)
 
 
 def gq_f8_quant(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, pow2: bool = False,
                 stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """q, scales of x [M][K] (fp32 / bf16 / fp16): e4m3 bytes [M][K] and one
     fp32 scale for 128 inputs of a row, [ceil(K / 128)][M]."""
-    _tensor("x", x, _HALF_OR_F32)
-    _f8_rows("x", x)
-    M, K = x.shape
-    _quantised(q, scales, M, K)
-    dev = _one_device(x=x, q=q, scales=scales)
-    _launch("gq_f8_quant", stream, dev, _ptr(x), _DTYPES[x.dtype], M, K, _ld(x), 1 if pow2 else 0, _ptr(q), _ld(q),
-            _ptr(scales), _ld(scales))
+    try:
+        (M, K), d = x.shape, x.get_device()
+        ok = (M > 1 and d >= 0 and d == q.get_device() == scales.get_device() and x.dtype in _HALF_OR_F32 and
+              q.dtype in _F8 and scales.dtype is _f32 and q.shape == (M, K) and
+              scales.shape == ((K + 127) // 128, M) and x.stride(1) == q.stride(1) == scales.stride(1) == 1)
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _check_quant(x, q, scales)
+    _launch("gq_f8_quant", _lib.gq_f8_quant, d, stream, x.data_ptr(), _DTYPES[x.dtype], M, K, _ld(x), pow2,
+            q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales))
     return q, scales
 
 
 def gq_f8_glu_quant(g: torch.Tensor, u: torch.Tensor, act: str, q: torch.Tensor, scales: torch.Tensor,
                     pow2: bool = False, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """gq_f8_quant of act(g) * u; g, u [M][K] of one type (fp32 / bf16 / fp16)."""
-    _tensor("g", g, _HALF_OR_F32)
-    _tensor("u", u, (g.dtype,))
-    _f8_rows("g", g)
-    _f8_rows("u", u)
-    _need(act in ACTS, "act must be one of %s" % sorted(ACTS))
-    M, K = g.shape
-    _shape("u", u, M, K)
-    _quantised(q, scales, M, K)
-    dev = _one_device(g=g, u=u, q=q, scales=scales)
-    _launch("gq_f8_glu_quant", stream, dev, _ptr(g), _ptr(u), _DTYPES[g.dtype], M, K, _ld(g), _ld(u), ACTS[act],
-            1 if pow2 else 0, _ptr(q), _ld(q), _ptr(scales), _ld(scales))
+    try:
+        (M, K), d = g.shape, g.get_device()
+        ok = (M > 1 and d >= 0 and d == u.get_device() == q.get_device() == scales.get_device() and
+              g.dtype in _HALF_OR_F32 and u.dtype is g.dtype and q.dtype in _F8 and scales.dtype is _f32 and
+              u.shape == q.shape == (M, K) and scales.shape == ((K + 127) // 128, M) and act in ACTS and
+              g.stride(1) == u.stride(1) == q.stride(1) == scales.stride(1) == 1)
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _need(act in ACTS, "act must be one of %s" % sorted(ACTS))
+        _tensor("u", u, _HALF_OR_F32)
+        _check_quant(g, q, scales, u=u)
+    _launch("gq_f8_glu_quant", _lib.gq_f8_glu_quant, d, stream, g.data_ptr(), u.data_ptr(), _DTYPES[g.dtype], M, K,
+            _ld(g), _ld(u), ACTS[act], pow2, q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales))
     return q, scales
 
 
-def _f8_weights(W: torch.Tensor, wscales: torch.Tensor, dims: int) -> tuple:
+def _check_f8_weights(W, wscales, dims: int) -> None:
     _tensor("W", W, _F8)
     _need(W.dim() == dims, "W must be %d-D" % dims)
     _contig("W", W)
     *lead, N, K = W.shape
     _f8_scales("wscales", wscales, *lead, _f8_blocks(N), _f8_blocks(K))
     _contig("wscales", wscales)
-    return (*lead, N, K)
 
 
-def gq_f8_matvec(W: torch.Tensor, wscales: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
-                 stream=None) -> torch.Tensor:
-    """y [batch][N] (fp32 / bf16) = x [batch][K] (fp32 / bf16) times the
-    weights W [N][K] e4m3 with wscales [ceil(N / 128)][ceil(K / 128)]."""
-    N, K = _f8_weights(W, wscales, 2)
+def _check_matvec(W, wscales, x, y) -> None:
+    _check_f8_weights(W, wscales, 2)
+    N, K = W.shape
     _tensor("x", x, _ACT)
     _tensor("y", y, _ACT)
     _need(x.dim() == 2 and x.shape[1] == K, "x must be [batch][%d]" % K)
     _shape("y", y, x.shape[0], N)
     _contig("x", x)
     _contig("y", y)
-    dev = _one_device(W=W, wscales=wscales, x=x, y=y)
-    _launch("gq_f8_matvec", stream, dev, _ptr(W), _ptr(wscales), N, K, _ptr(x), _DTYPES[x.dtype], x.shape[0], _ptr(y),
-            _DTYPES[y.dtype])
+    _one_device(W=W, wscales=wscales, x=x, y=y)
+
+
+def gq_f8_matvec(W: torch.Tensor, wscales: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
+                 stream=None) -> torch.Tensor:
+    """y [batch][N] (fp32 / bf16) = x [batch][K] (fp32 / bf16) times the
+    weights W [N][K] e4m3 with wscales [ceil(N / 128)][ceil(K / 128)]."""
+    try:
+        (N, K), d, batch = W.shape, W.get_device(), x.shape[0]
+        ok = (d >= 0 and d == wscales.get_device() == x.get_device() == y.get_device() and W.dtype in _F8 and
+              wscales.dtype is _f32 and x.dtype in _ACT and y.dtype in _ACT and
+              wscales.shape == ((N + 127) // 128, (K + 127) // 128) and x.shape == (batch, K) and
+              y.shape == (batch, N) and W.is_contiguous() and wscales.is_contiguous() and x.is_contiguous() and
+              y.is_contiguous())
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _check_matvec(W, wscales, x, y)
+    _launch("gq_f8_matvec", _lib.gq_f8_matvec, d, stream, W.data_ptr(), wscales.data_ptr(), N, K, x.data_ptr(),
+            _DTYPES[x.dtype], batch, y.data_ptr(), _DTYPES[y.dtype])
     return y
 
 
-def _f8_x(X: torch.Tensor, xscales: torch.Tensor, K: int) -> None:
+def _check_f8_x(X, xscales, K: int) -> None:
     _tensor("X", X, _F8)
     _f8_rows("X", X)
     _need(X.shape[1] == K, "X must have rows of K = %d" % K)
@@ -556,24 +601,41 @@ def _f8_x(X: torch.Tensor, xscales: torch.Tensor, K: int) -> None:
     _f8_rows("xscales", xscales)
 
 
+def _check_matmul(W, wscales, X, xscales, Y) -> None:
+    _check_f8_weights(W, wscales, 2)
+    N, K = W.shape
+    _check_f8_x(X, xscales, K)
+    _tensor("Y", Y, _ACT)
+    _f8_rows("Y", Y)
+    _shape("Y", Y, X.shape[0], N)
+    _one_device(W=W, wscales=wscales, X=X, xscales=xscales, Y=Y)
+
+
 def gq_f8_matmul(W: torch.Tensor, wscales: torch.Tensor, X: torch.Tensor, xscales: torch.Tensor, Y: torch.Tensor,
                  stream=None) -> torch.Tensor:
     """Y [M][N] (fp32 / bf16) = X [M][K] e4m3 with xscales [ceil(K / 128)][M]
     times the weights W [N][K] with wscales [ceil(N / 128)][ceil(K / 128)]."""
-    N, K = _f8_weights(W, wscales, 2)
-    _f8_x(X, xscales, K)
-    _tensor("Y", Y, _ACT)
-    _f8_rows("Y", Y)
-    M = X.shape[0]
-    _shape("Y", Y, M, N)
-    dev = _one_device(W=W, wscales=wscales, X=X, xscales=xscales, Y=Y)
-    _launch("gq_f8_matmul", stream, dev, _ptr(W), _ptr(wscales), N, K, _ptr(X), _ptr(xscales), M, _ld(X),
-            _ld(xscales), _ptr(Y), _DTYPES[Y.dtype], _ld(Y))
+    try:
+        (N, K), d, M = W.shape, W.get_device(), X.shape[0]
+        ok = (M > 1 and d >= 0 and
+              d == wscales.get_device() == X.get_device() == xscales.get_device() == Y.get_device() and
+              W.dtype in _F8 and X.dtype in _F8 and wscales.dtype is _f32 and xscales.dtype is _f32 and
+              Y.dtype in _ACT and wscales.shape == ((N + 127) // 128, (K + 127) // 128) and X.shape == (M, K) and
+              xscales.shape == ((K + 127) // 128, M) and Y.shape == (M, N) and
+              W.is_contiguous() and wscales.is_contiguous() and
+              X.stride(1) == xscales.stride(1) == Y.stride(1) == 1)
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _check_matmul(W, wscales, X, xscales, Y)
+    _launch("gq_f8_matmul", _lib.gq_f8_matmul, d, stream, W.data_ptr(), wscales.data_ptr(), N, K, X.data_ptr(),
+            xscales.data_ptr(), M, _ld(X), _ld(xscales), Y.data_ptr(), _DTYPES[Y.dtype], _ld(Y))
     return Y
 
 
 def gq_f8_matmul_id_workspace(n_experts: int, n_tokens: int, top_k: int, N: int, y_dtype=torch.float32,
                               weighted: bool = True) -> int:
+    """Bytes of the workspace of gq_f8_matmul_id for these sizes."""
     b = SZ()
     _need(y_dtype in _ACT, "y_dtype must be %s" % " or ".join(map(str, _ACT)), TypeError)
     _check("gq_f8_matmul_id_workspace", _lib.gq_f8_matmul_id_workspace(
@@ -581,20 +643,13 @@ def gq_f8_matmul_id_workspace(n_experts: int, n_tokens: int, top_k: int, N: int,
     return b.value
 
 
-def gq_f8_matmul_id(W: torch.Tensor, wscales: torch.Tensor, ids, X: torch.Tensor, xscales: torch.Tensor,
-                    Y: torch.Tensor, ws: torch.Tensor, route_w: torch.Tensor | None = None,
-                    stream=None) -> torch.Tensor:
-    """Routed product with the experts W [n_experts][N][K], wscales
-    [n_experts][ceil(N / 128)][ceil(K / 128)]; X [n_tokens][K], or
-    [n_tokens * top_k][K] with a row for each slot; Y [n_tokens][top_k][N], or
-    [n_tokens][N] weighted by route_w [n_tokens][top_k].  ids may be a
-    (n_tokens, top_k) tuple: the table already in ws is used."""
-    n_experts, N, K = _f8_weights(W, wscales, 3)
+def _check_matmul_id(W, wscales, ids, X, xscales, Y, ws, route_w) -> None:
+    _check_f8_weights(W, wscales, 3)
+    n_experts, N, K = W.shape
     reuse = isinstance(ids, tuple)
     n_tokens, top_k = ids if reuse else _ids(ids)
-    _f8_x(X, xscales, K)
-    rows = X.shape[0]
-    _need(rows == n_tokens or rows == n_tokens * top_k, "X must have n_tokens = %d or n_tokens * top_k = %d rows"
+    _check_f8_x(X, xscales, K)
+    _need(X.shape[0] in (n_tokens, n_tokens * top_k), "X must have n_tokens = %d or n_tokens * top_k = %d rows"
           % (n_tokens, n_tokens * top_k))
     _tensor("Y", Y, _ACT)
     _contig("Y", Y)
@@ -606,33 +661,55 @@ def gq_f8_matmul_id(W: torch.Tensor, wscales: torch.Tensor, ids, X: torch.Tensor
         _shape("route_w", route_w, n_tokens, top_k)
         _contig("route_w", route_w)
     _workspace(ws)
-    dev = _one_device(W=W, wscales=wscales, ids=None if reuse else ids, X=X, xscales=xscales, Y=Y, ws=ws,
-                      route_w=route_w)
-    _launch("gq_f8_matmul_id", stream, dev, _ptr(W), _ptr(wscales), n_experts, N, K, None if reuse else _ptr(ids),
-            n_tokens, top_k, _ptr(X), _ptr(xscales), _ld(X), _ld(xscales), 0 if rows == n_tokens else 1,
-            _ptr(route_w), _ptr(Y), _DTYPES[Y.dtype], _ptr(ws), ws.numel())
+    _one_device(W=W, wscales=wscales, ids=None if reuse else ids, X=X, xscales=xscales, Y=Y, ws=ws, route_w=route_w)
+
+
+def gq_f8_matmul_id(W: torch.Tensor, wscales: torch.Tensor, ids, X: torch.Tensor, xscales: torch.Tensor,
+                    Y: torch.Tensor, ws: torch.Tensor, route_w: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Routed product with the experts W [n_experts][N][K], wscales
+    [n_experts][ceil(N / 128)][ceil(K / 128)]; X [n_tokens][K], or
+    [n_tokens * top_k][K] with a row for each slot; Y [n_tokens][top_k][N], or
+    [n_tokens][N] weighted by route_w [n_tokens][top_k].  ids may be a
+    (n_tokens, top_k) tuple: the table already in ws is used."""
+    reuse = isinstance(ids, tuple)
+    try:
+        (n_experts, N, K), d, rows = W.shape, W.get_device(), X.shape[0]
+        n_tokens, top_k = ids if reuse else ids.shape
+        ok = (n_tokens > 1 and d >= 0 and d == wscales.get_device() == X.get_device() == xscales.get_device() ==
+              Y.get_device() == ws.get_device() and W.dtype in _F8 and X.dtype in _F8 and wscales.dtype is _f32 and
+              xscales.dtype is _f32 and Y.dtype in _ACT and ws.dtype is _u8 and
+              wscales.shape == (n_experts, (N + 127) // 128, (K + 127) // 128) and X.shape == (rows, K) and
+              (rows == n_tokens or rows == n_tokens * top_k) and xscales.shape == ((K + 127) // 128, rows) and
+              (reuse or (ids.dtype is _i32 and ids.get_device() == d and ids.is_contiguous())) and
+              (Y.shape == (n_tokens, top_k, N) if route_w is None else
+               Y.shape == (n_tokens, N) and route_w.shape == (n_tokens, top_k) and route_w.dtype is _f32 and
+               route_w.get_device() == d and route_w.is_contiguous()) and
+              X.stride(1) == xscales.stride(1) == 1 and W.is_contiguous() and wscales.is_contiguous() and
+              Y.is_contiguous() and ws.is_contiguous())
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _check_matmul_id(W, wscales, ids, X, xscales, Y, ws, route_w)
+    _launch("gq_f8_matmul_id", _lib.gq_f8_matmul_id, d, stream, W.data_ptr(), wscales.data_ptr(), n_experts, N, K,
+            None if reuse else ids.data_ptr(), n_tokens, top_k, X.data_ptr(), xscales.data_ptr(), _ld(X),
+            _ld(xscales), rows != n_tokens, None if route_w is None else route_w.data_ptr(), Y.data_ptr(),
+            _DTYPES[Y.dtype], ws.data_ptr(), ws.numel())
     return Y
 
 
 def gq_f8_matmul_id_check(ws: torch.Tensor, stream=None) -> int:
     """Ids outside [0, n_experts) in the last gq_f8_matmul_id call given ids that used ws (waits for the stream)."""
     _workspace(ws)
-    dev = _one_device(ws=ws)
+    _on_gpu(ws=ws)
     n = I32()
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev):
-        _check("gq_f8_matmul_id_check", _lib.gq_f8_matmul_id_check(_ptr(ws), stream.cuda_stream, ctypes.byref(n)))
+    # (the C call takes the stream before its last argument)
+    _launch("gq_f8_matmul_id_check", lambda s: _lib.gq_f8_matmul_id_check(ws.data_ptr(), s, ctypes.byref(n)),
+            ws.get_device(), stream)
     return n.value
 
 
-def gq_route_scored(logits: torch.Tensor, top_k: int, ids: torch.Tensor, weights: torch.Tensor,
-                    score: str = "softmax", bias: torch.Tensor | None = None, n_groups: int = 1, top_groups: int = 1,
-                    group_rank: str = "max", renorm: bool = True, scale: float = 1.0,
-                    stream=None) -> tuple[torch.Tensor, torch.Tensor]:
-    """ids / weights [n_tokens][top_k] (int32 / fp32) of fp32 or bf16 ``logits``
-    [n_tokens][n_experts]: softmax or sigmoid scores, chosen by score + bias
-    among the experts of the best top_groups of n_groups groups."""
+def _check_route_scored(logits, top_k, ids, weights, score, bias, group_rank) -> None:
     _tensor("logits", logits, _ACT)
     _tensor("ids", ids, _I32)
     _tensor("weights", weights, _F32)
@@ -648,10 +725,30 @@ def gq_route_scored(logits: torch.Tensor, top_k: int, ids: torch.Tensor, weights
         _contig("bias", bias)
     for name, v in (("logits", logits), ("ids", ids), ("weights", weights)):
         _contig(name, v)
-    dev = _one_device(logits=logits, ids=ids, weights=weights, bias=bias)
-    _launch("gq_route_scored", stream, dev, _ptr(logits), _DTYPES[logits.dtype], n_tokens, n_experts, top_k,
-            SCORES[score], _ptr(bias), n_groups, top_groups, GROUP_RANKS[group_rank], 1 if renorm else 0, scale,
-            _ptr(ids), _ptr(weights))
+    _one_device(logits=logits, ids=ids, weights=weights, bias=bias)
+
+
+def gq_route_scored(logits: torch.Tensor, top_k: int, ids: torch.Tensor, weights: torch.Tensor,
+                    score: str = "softmax", bias: torch.Tensor | None = None, n_groups: int = 1, top_groups: int = 1,
+                    group_rank: str = "max", renorm: bool = True, scale: float = 1.0,
+                    stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """ids / weights [n_tokens][top_k] (int32 / fp32) of fp32 or bf16 ``logits``
+    [n_tokens][n_experts]: softmax or sigmoid scores, chosen by score + bias
+    among the experts of the best top_groups of n_groups groups."""
+    try:
+        (n_tokens, n_experts), d = logits.shape, logits.get_device()
+        ok = (d >= 0 and d == ids.get_device() == weights.get_device() and logits.dtype in _ACT and
+              ids.dtype is _i32 and weights.dtype is _f32 and ids.shape == weights.shape == (n_tokens, top_k) and
+              score in SCORES and group_rank in GROUP_RANKS and logits.is_contiguous() and ids.is_contiguous() and
+              weights.is_contiguous() and (bias is None or (bias.dtype is _f32 and bias.shape == (n_experts,) and
+                                                            bias.get_device() == d and bias.is_contiguous())))
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _check_route_scored(logits, top_k, ids, weights, score, bias, group_rank)
+    _launch("gq_route_scored", _lib.gq_route_scored, d, stream, logits.data_ptr(), _DTYPES[logits.dtype], n_tokens,
+            n_experts, top_k, SCORES[score], None if bias is None else bias.data_ptr(), n_groups, top_groups,
+            GROUP_RANKS[group_rank], renorm, scale, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 

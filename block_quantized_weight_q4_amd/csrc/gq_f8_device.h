@@ -62,6 +62,75 @@ __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi) {
     return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+
+// Buffer resource of `bytes` (< 2^31) from base; loads beyond them give zeros.
+__device__ __forceinline__ Rsrc make_rsrc(const void* base, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t NOWHERE = 0x80000000u;  // an offset beyond every resource
+__device__ __forceinline__ u32x4 bld16(Rsrc r, uint32_t off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+}
+
+// Stores four neighbouring results of a row (n .. n + 3, those below N) as fp32
+// or, rounded to nearest even, as bf16; at once where the row's stride allows.
+template <typename T>
+__device__ __forceinline__ void store4(T* row, int64_t n, int64_t N, bool vec, f32x4 v) {
+    if (vec && n + 4 <= N) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<f32x4*>(row + n) = v;
+        } else {
+            const bf16x2 a = {(__bf16)v[0], (__bf16)v[1]}, b = {(__bf16)v[2], (__bf16)v[3]};
+            *reinterpret_cast<u32x2*>(row + n) =
+                u32x2{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+        }
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (n + r < N) {
+            if constexpr (sizeof(T) == 4) row[n + r] = v[r];
+            else row[n + r] = gqd::f2bf(v[r]);
+        }
+}
+
+// ---- global-to-LDS copies (the loads that write LDS without registers) ----
+// Each lane of an instruction brings 16 bytes from an address of its own; they
+// land at lds + 16 * lane.  A kernel that uses them waits for them itself.
+typedef __attribute__((address_space(3))) void* LdsPtr;
+typedef const __attribute__((address_space(1))) void* GlobalPtr;
+
+__device__ __forceinline__ void copy16(Rsrc r, uint32_t off, uint8_t* lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)lds, 16, (int)off, 0, 0, 0);
+}
+__device__ __forceinline__ void copy16(const uint8_t* p, uint8_t* lds) {
+    __builtin_amdgcn_global_load_lds((GlobalPtr)p, (LdsPtr)lds, 16, 0, 0);
+}
+// 4 bytes a lane, at lds + 4 * lane.
+__device__ __forceinline__ void copy4(const float* p, uint8_t* lds) {
+    __builtin_amdgcn_global_load_lds((GlobalPtr)p, (LdsPtr)lds, 4, 0, 0);
+}
+
+// Until at most N of this wavefront's loads and copies are outstanding
+// (gfx9 encoding: vmcnt in bits 3:0 and 15:14, the other counters at their
+// maxima); what reads the copied data stays behind it.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+// Until this wavefront's LDS reads have returned: what overwrites the LDS that
+// they read stays behind it.
+__device__ __forceinline__ void wait_reads() {
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));  // lgkmcnt(0)
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // Stores a value as fp32 or, rounded to nearest even, as bf16.
 template <typename T>
 __device__ __forceinline__ void store_as(T* p, float v) {

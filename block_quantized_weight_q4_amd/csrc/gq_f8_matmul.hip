@@ -14,6 +14,7 @@
 
 #include "gq_f8_device.h"
 #include "gq_f8_internal.h"
+#include "gq_f8_stream.h"
 
 using namespace gqf8;
 
@@ -160,108 +161,222 @@ __device__ __forceinline__ void tile_of(const Table& t, int i, int TM, int& e, i
     rows = (int)(b - a < TM ? b - a : TM);
 }
 
-// ------------------------------------------------------------- the product ----
-constexpr int TM = 64, TN = 64;
+// ------------------------------------------------------- many rows (tiles) ----
+// Order of the tiles: workgroups go to the 8 XCDs in turn, so XCD x takes a run
+// of neighbouring tiles (each XCD has an L2 of its own), and a run walks the
+// row tiles of one column of tiles first: 32 CUs then share a few panels of W
+// and all (at most G) panels of X.
+__device__ __forceinline__ int xcd_order(int id, int total) {
+    const int x = id & 7, q = total >> 3, r = total & 7;
+    return x * q + (x < r ? x : r) + (id >> 3);
+}
 
-// One 64 x 64 tile of Y: 4 wavefronts, each 32 x 32 as 2 x 2 MFMA tiles.
-template <typename TY, bool ROUTED>
-__global__ __launch_bounds__(256) void k_f8_matmul(const uint8_t* __restrict__ W, const float* __restrict__ wsc,
-                                                   int64_t N, int64_t K, const uint8_t* __restrict__ X,
-                                                   const float* __restrict__ xs, int64_t M, int64_t ldx,
-                                                   int64_t xs_ld, TY* __restrict__ Y, int64_t ldy, int gn, Table t) {
-    __shared__ __align__(16) uint8_t lx[TM * BLK], lw[TN * BLK];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int tn = blockIdx.x % gn, tm = blockIdx.x / gn;
-    const int64_t n0 = (int64_t)tn * TN;
-    const int64_t KB = (K + BLK - 1) / BLK;
-    int e = 0, start = 0, rows;
+// BM rows of X by BN rows of W; WM x WN wavefronts of (BM / WM) x (BN / WN).
+// Both tiles of a 128-input block go to LDS by global-to-LDS copies, NB - 1
+// blocks ahead, in rows of 128 bytes whose 16-byte chunks are swizzled so that
+// operand reads cover all banks; the block's activation scales come along.
+// One barrier a block.
+template <int BM, int BN, int WM, int WN, int NB, typename TY, bool ROUTED>
+struct Tile {
+    static constexpr int WV = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
+    static constexpr int XI = BM / 8 / WV, WI = BN / 8 / WV;  // copies of a wavefront and block
+    static constexpr int SX = (BM + BN) * BLK, STAGE = SX + WV * 256;
+    static constexpr int LOADS = XI + WI + 1;
+    static_assert(BM % (8 * WV) == 0 && BN % (8 * WV) == 0 && WV > BM / 64 && BN / WN <= BLK, "tile shape");
+
+    static __device__ __forceinline__ void run(const uint8_t* __restrict__ W, const float* __restrict__ wsc,
+                                               int64_t N, int64_t K, const uint8_t* __restrict__ X,
+                                               const float* __restrict__ xs, int64_t ldx, int64_t xs_ld,
+                                               TY* __restrict__ Y, int64_t ldy, int64_t m0, int64_t n0, int rows,
+                                               int start, const Table& t, uint8_t* smem) {
+        const int lane = threadIdx.x & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int fr = lane & 15, fq = lane >> 4;
+        const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
+        const int KB = (int)((K + BLK - 1) / BLK);
+        const int64_t w_rows = N - n0 < BN ? N - n0 : BN;
+        const Rsrc wr = make_rsrc(W + n0 * K, w_rows * K);
+        const Rsrc xr = make_rsrc(X + m0 * ldx, (int64_t)rows * ldx);  // (dense)
+        auto slot_of = [&](int i) -> int64_t {
+            const unsigned s = (unsigned)t.slot[start + (i < rows ? i : rows - 1)];
+            return s < (unsigned)t.S ? (int64_t)s : t.S - 1;
+        };
+        auto x_row = [&](int i) -> int64_t {
+            if constexpr (ROUTED) return t.per_slot ? slot_of(i) : slot_of(i) / t.top_k;
+            else return m0 + (i < rows ? i : rows - 1);
+        };
+        // copies: wavefront w brings rows 8 (w + WV u) .. + 7 of either tile
+        uint32_t xoff[XI], woff[WI];
+        const uint8_t* xp[XI];
+#pragma unroll
+        for (int u = 0; u < XI; ++u) {
+            const int r = 8 * (wave + WV * u) + (lane >> 3);
+            if constexpr (ROUTED) xp[u] = X + x_row(r) * ldx;
+            else xoff[u] = (uint32_t)(r * ldx);
+        }
+#pragma unroll
+        for (int u = 0; u < WI; ++u) woff[u] = (uint32_t)((8 * (wave + WV * u) + (lane >> 3)) * K);
+        // the chunk of row r that its lane copies: (lane % 8) ^ (r / 2 % 8), r = 8 (wave + WV u) + lane / 8
+        const uint32_t chunk = 16u * (uint32_t)((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
+        static_assert(WV % 2 == 0, "the swizzle of a lane's rows is the same for all of its copies");
+        // one copy of 64 scales: wavefronts below BM / 64 those of X, the others W's (of wavefront w's columns: lane w)
+        const float* sp;
+        int64_t sstep;
+        if (wave < BM / 64) {
+            sp = xs + x_row(64 * wave + lane);
+            sstep = xs_ld;
+        } else {
+            const int64_t n = n0 + (lane % WV / WM) * (BN / WN);
+            sp = wsc + ((n < N ? n : N - 1) / BLK) * KB;
+            sstep = 1;
+        }
+        auto load = [&](int kb) {
+            uint8_t* d = smem + (kb % NB) * STAGE;
+            const int64_t k = (int64_t)kb * BLK + chunk;
+            const bool in = k < K;
+#pragma unroll
+            for (int u = 0; u < XI; ++u) {
+                uint8_t* l = d + (wave + WV * u) * 1024;
+                if constexpr (ROUTED) copy16(xp[u] + (in ? k : 0), l);
+                else copy16(xr, in ? xoff[u] + (uint32_t)k : NOWHERE, l);
+            }
+#pragma unroll
+            for (int u = 0; u < WI; ++u)
+                copy16(wr, in ? woff[u] + (uint32_t)k : NOWHERE, d + BM * BLK + (wave + WV * u) * 1024);
+            copy4(sp + (kb < KB ? kb : KB - 1) * sstep, d + SX + wave * 256);
+        };
+        f32x4 acc[NT][MT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{};
+        if (KB > 0) {
+#pragma unroll
+            for (int s = 0; s < NB - 1; ++s) load(s);
+            wait_copies<(NB - 2) * LOADS>();
+            gqd::lds_barrier();
+        }
+        // 16-byte positions of this lane's two chunks of an operand row (rows 16 i + fr: the same for every i)
+        const int p0 = pos128(fr, fq), p1 = pos128(fr, 4 + fq);
+        for (int kb = 0; kb < KB; ++kb) {
+            load(kb + NB - 1);
+            const uint8_t* d = smem + (kb % NB) * STAGE;
+            const u32x4* dx = reinterpret_cast<const u32x4*>(d + wm * BLK);
+            const u32x4* dw = reinterpret_cast<const u32x4*>(d + (BM + wn) * BLK);
+            const float* ds = reinterpret_cast<const float*>(d + SX);
+            const float s_w = ds[(BM / 64) * 64 + wave];
+            float s[MT];
+            i32x8 x[MT];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                x[j] = join(dx[128 * j + p0], dx[128 * j + p1]);
+                s[j] = s_w * ds[wm + 16 * j + fr];
+            }
+            if constexpr (sizeof(TY) == 4) {
+                Wide xw[MT];
+#pragma unroll
+                for (int j = 0; j < MT; ++j) xw[j] = widen(x[j]);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const Wide a = widen(join(dw[128 * i + p0], dw[128 * i + p1]));
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) {
+                        const f32x4 p = mfma16(a, xw[j]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], s[j], acc[i][j][r]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const i32x8 a = join(dw[128 * i + p0], dw[128 * i + p1]);
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) {
+                        const f32x4 p = mfma8(a, x[j]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], s[j], acc[i][j][r]);
+                    }
+                }
+            }
+            wait_copies<(NB - 2) * LOADS>();
+            gqd::lds_barrier();
+        }
+        wait_copies<0>();
+        const bool vec = (ldy & 3) == 0;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int row = wm + 16 * j + fr;
+            if (row >= rows) continue;
+            TY* y = Y + (ROUTED ? slot_of(row) : m0 + row) * ldy;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) store4(y, n0 + wn + 16 * i + 4 * fq, N, vec, acc[i][j]);
+        }
+    }
+};
+
+template <int BM, int BN, int WM, int WN, int NB, typename TY, bool ROUTED>
+__global__ __launch_bounds__(64 * WM * WN) void k_f8_tile(const uint8_t* __restrict__ W, const float* __restrict__ wsc,
+                                                          int64_t N, int64_t K, const uint8_t* __restrict__ X,
+                                                          const float* __restrict__ xs, int64_t M, int64_t ldx,
+                                                          int64_t xs_ld, TY* __restrict__ Y, int64_t ldy, int gm,
+                                                          int gn, Table t) {
+    using T = Tile<BM, BN, WM, WN, NB, TY, ROUTED>;
+    __shared__ __align__(16) uint8_t smem[NB * T::STAGE];
+    const int id = xcd_order(blockIdx.x, gm * gn);
+    int tm, tn, e = 0, start = 0, rows;
     if constexpr (ROUTED) {
-        tile_of(t, tm, TM, e, start, rows);
+        tm = id / gn;  // an expert's tiles side by side: they share its rows of X
+        tn = id % gn;
+        tile_of(t, tm, BM, e, start, rows);
         if (rows == 0) return;
         W += (int64_t)e * N * K;
-        wsc += (int64_t)e * ((N + BLK - 1) / BLK) * KB;
+        wsc += (int64_t)e * ((N + BLK - 1) / BLK) * ((K + BLK - 1) / BLK);
     } else {
-        const int64_t left = M - (int64_t)tm * TM;
-        rows = (int)(left < TM ? left : TM);
+        // bands of at most 12 row tiles
+        const int bands = (gm + 11) / 12, h = (gm + bands - 1) / bands;
+        const int band = id / (h * gn), hb = gm - band * h < h ? gm - band * h : h;
+        const int r = id - band * h * gn;
+        tm = band * h + r % hb;
+        tn = r / hb;
+        const int64_t left = M - (int64_t)tm * BM;
+        rows = (int)(left < BM ? left : BM);
     }
-    // rows of X and of Y that tile row i stands for
-    auto y_row = [&](int i) -> int64_t {
+    T::run(W, wsc, N, K, X, xs, ldx, xs_ld, Y, ldy, (int64_t)tm * BM, (int64_t)tn * BN, rows, start, t, smem);
+}
+
+// A few rows: the stream kernel, 16 MT rows of X and 16 NT of W a workgroup.
+template <int MT, int NT, int WV, int D, typename TY, bool ROUTED>
+__global__ __launch_bounds__(64 * WV) void k_f8_stream(const uint8_t* __restrict__ W, const float* __restrict__ wsc,
+                                                       int64_t N, int64_t K, const uint8_t* __restrict__ X,
+                                                       const float* __restrict__ xs, int64_t M, int64_t ldx,
+                                                       int64_t xs_ld, TY* __restrict__ Y, int64_t ldy, int gn,
+                                                       Table t) {
+    constexpr int RING = WV * D * Stream<MT, NT, X_E4M3, 16 * MT>::BYTES, JOIN = WV * NT * MT * 1024;
+    __shared__ __align__(16) uint8_t smem[RING > JOIN ? RING : JOIN];
+    const int tn = blockIdx.x % gn, tm = blockIdx.x / gn;
+    int e = 0, start = 0, rows;
+    if constexpr (ROUTED) {
+        tile_of(t, tm, 16 * MT, e, start, rows);
+        if (rows == 0) return;
+        W += (int64_t)e * N * K;
+        wsc += (int64_t)e * ((N + BLK - 1) / BLK) * ((K + BLK - 1) / BLK);
+    } else {
+        const int64_t left = M - (int64_t)tm * (16 * MT);
+        rows = (int)(left < 16 * MT ? left : 16 * MT);
+    }
+    auto row_of = [&](int i) -> int64_t {
+        const int c = i < rows ? i : rows - 1;
         if constexpr (ROUTED) {
-            const unsigned s = (unsigned)t.slot[start + (i < rows ? i : 0)];
+            const unsigned s = (unsigned)t.slot[start + c];
             return s < (unsigned)t.S ? (int64_t)s : t.S - 1;
         } else {
-            return (int64_t)tm * TM + (i < rows ? i : 0);
+            return (int64_t)tm * (16 * MT) + c;
         }
     };
-    auto x_row = [&](int i) -> int64_t {
-        const int64_t r = y_row(i);
-        return ROUTED && !t.per_slot ? r / t.top_k : r;
-    };
-    const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
-    const int fr = lane & 15, fq = lane >> 4;
-    f32x4 acc[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{};
-    int64_t xr[2];  // rows of X whose scales this lane uses
-#pragma unroll
-    for (int j = 0; j < 2; ++j) xr[j] = x_row(wm + 16 * j + fr);
-    int64_t lr[2];  // rows of X that this thread loads
-#pragma unroll
-    for (int i = 0; i < 2; ++i) lr[i] = x_row((tid + 256 * i) >> 3);
-
-    for (int64_t b = 0; b < KB; ++b) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int c = tid + 256 * i, r = c >> 3, ch = c & 7;
-            const int64_t k = b * BLK + 16 * ch;
-            u32x4 vx{}, vw{};
-            if (k < K && r < rows) vx = *reinterpret_cast<const u32x4*>(X + lr[i] * ldx + k);
-            if (k < K && n0 + r < N) vw = *reinterpret_cast<const u32x4*>(W + (n0 + r) * K + k);
-            const int at = r * BLK + ((ch ^ (r & 7)) << 4);  // swizzled: conflict-free reads
-            *reinterpret_cast<u32x4*>(lx + at) = vx;
-            *reinterpret_cast<u32x4*>(lw + at) = vw;
-        }
-        __syncthreads();
-        i32x8 a[2], x[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int rw = wn + 16 * i + fr, rx = wm + 16 * i + fr;
-            const int c0 = ((2 * fq) ^ (fr & 7)) << 4, c1 = ((2 * fq + 1) ^ (fr & 7)) << 4;
-            a[i] = join(*reinterpret_cast<const u32x4*>(lw + rw * BLK + c0),
-                        *reinterpret_cast<const u32x4*>(lw + rw * BLK + c1));
-            x[i] = join(*reinterpret_cast<const u32x4*>(lx + rx * BLK + c0),
-                        *reinterpret_cast<const u32x4*>(lx + rx * BLK + c1));
-        }
-        const float w_s = wsc[(n0 / BLK) * KB + b];  // (a 64-row tile lies in one block of 128 rows)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float s = w_s * xs[b * xs_ld + xr[j]];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                f32x4 p;
-                if constexpr (sizeof(TY) == 4) p = mfma16(widen(a[i]), widen(x[j]));
-                else p = mfma8(a[i], x[j]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], s, acc[i][j][r]);
-            }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int row = wm + 16 * j + fr;
-        if (row >= rows) continue;
-        TY* y = Y + y_row(row) * ldy;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t n = n0 + wn + 16 * i + 4 * fq + r;
-                if (n < N) store_as(y + n, acc[i][j][r]);
-            }
-    }
+    stream_tile<MT, NT, WV, D, X_E4M3, 16 * MT, TY>(
+        W, wsc, (int64_t)tn * (16 * NT), N, K, X, xs, ldx, xs_ld, rows, (ldy & 3) == 0,
+        [&](int i) { return ROUTED && !t.per_slot ? row_of(i) / t.top_k : row_of(i); },
+        [&](int i) { return Y + row_of(i) * ldy; }, smem);
 }
 
 // y[t][n] = sum_j rw[t][j] slot[t][j][n], j in increasing order, slots of
@@ -288,46 +403,88 @@ __global__ __launch_bounds__(256) void k_f8_combine(const TY* __restrict__ slots
 
 bool grid_ok(int64_t groups, int threads) { return groups * threads < ((int64_t)1 << 32); }
 
+// One call's operands.
 template <typename TY>
-hipError_t matmul(const uint8_t* W, const float* ws, int64_t N, int64_t K, const uint8_t* X, const float* xs,
-                  int64_t M, int64_t ldx, int64_t xs_ld, TY* Y, int64_t ldy, hipStream_t s) {
-    const int64_t gn = (N + TN - 1) / TN, gm = (M + TM - 1) / TM;
-    if (!grid_ok(gn * gm, 256)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_f8_matmul<TY, false>), dim3((unsigned)(gn * gm)), dim3(256), 0, s, W, ws, N, K, X, xs, M,
-                       ldx, xs_ld, Y, ldy, (int)gn, Table{});
+struct Call {
+    const uint8_t* W;
+    const float* wsc;
+    int64_t N, K;
+    const uint8_t* X;
+    const float* xs;
+    int64_t M, ldx, xs_ld;  // M: rows of X, or slots
+    TY* Y;
+    int64_t ldy;
+    Table t;
+    hipStream_t s;
+};
+
+// gm: tiles of rows (of slots: the most there can be)
+template <int MT, int NT, int WV, int D, bool ROUTED, typename TY>
+hipError_t stream(const Call<TY>& c, int64_t gm) {
+    const int64_t gn = (c.N + 16 * NT - 1) / (16 * NT);
+    if (!grid_ok(gn * gm, 64 * WV)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_f8_stream<MT, NT, WV, D, TY, ROUTED>), dim3((unsigned)(gn * gm)), dim3(64 * WV), 0, c.s, c.W,
+                       c.wsc, c.N, c.K, c.X, c.xs, c.M, c.ldx, c.xs_ld, c.Y, c.ldy, (int)gn, c.t);
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, int NB, bool ROUTED, typename TY>
+hipError_t tile(const Call<TY>& c, int64_t gm) {
+    const int64_t gn = (c.N + BN - 1) / BN;
+    if (!grid_ok(gn * gm, 64 * WM * WN)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_f8_tile<BM, BN, WM, WN, NB, TY, ROUTED>), dim3((unsigned)(gn * gm)), dim3(64 * WM * WN), 0,
+                       c.s, c.W, c.wsc, c.N, c.K, c.X, c.xs, c.M, c.ldx, c.xs_ld, c.Y, c.ldy, (int)gm, (int)gn, c.t);
     return hipGetLastError();
 }
 
 template <typename TY>
-hipError_t matmul_id(const uint8_t* W, const float* wsc, int n_experts, int64_t N, int64_t K, const int32_t* ids,
-                     int n_tokens, int top_k, const uint8_t* X, const float* xs, int64_t ldx, int64_t xs_ld,
-                     int x_per_slot, const float* route_w, TY* Y, int y_dtype, void* ws, hipStream_t s) {
+hipError_t matmul(const Call<TY>& c) {
+    auto tiles = [&](int h) { return (c.M + h - 1) / h; };
+    if (c.M <= 16) return stream<1, 2, 8, 1, false>(c, tiles(16));
+    if (c.M <= 256) return stream<2, 2, 8, 1, false>(c, tiles(32));
+    if constexpr (sizeof(TY) == 2)
+        if (c.M >= 1024 && c.N >= 2048) return tile<256, 256, 4, 2, 2, false>(c, tiles(256));
+    return tile<128, 128, 2, 2, 2, false>(c, tiles(128));
+}
+
+// Rows of a tile of slots, from what every product of a layer has in common.
+int tile_rows(int64_t S, int n_experts) {
+    return S <= 16 * (int64_t)n_experts ? 16 : S <= 64 * (int64_t)n_experts ? 32 : 128;
+}
+
+template <typename TY>
+hipError_t matmul_id(Call<TY> c, int n_experts, const int32_t* ids, int n_tokens, int top_k, int x_per_slot,
+                     const float* route_w, int y_dtype, void* ws) {
     const int S = n_tokens * top_k;
-    const WsLayout L = layout(n_experts, S, N, y_dtype, route_w != nullptr);
+    const WsLayout L = layout(n_experts, S, c.N, y_dtype, route_w != nullptr);
     uint8_t* base = static_cast<uint8_t*>(ws);
     int* hdr = reinterpret_cast<int*>(base);
     int* first = reinterpret_cast<int*>(base + L.off_first);
-    int* tile = reinterpret_cast<int*>(base + L.off_tile);
+    int* tile_at = reinterpret_cast<int*>(base + L.off_tile);
     int* slot_e = reinterpret_cast<int*>(base + L.off_expert);
     int* slot = reinterpret_cast<int*>(base + L.off_slot);
-    TY* out = route_w ? reinterpret_cast<TY*>(base + L.off_out) : Y;
-    // tiles of the worst case: every expert may end with a partial one
-    const int64_t gm = S / TM + (S < n_experts ? S : n_experts), gn = (N + TN - 1) / TN;
-    if (!grid_ok(gm * gn, 256)) return hipErrorInvalidValue;
+    TY* y = c.Y;
+    if (route_w) c.Y = reinterpret_cast<TY*>(base + L.off_out);
+    c.M = S;
+    c.ldy = c.N;
+    c.t = Table{first, tile_at, slot, n_experts, S, top_k, x_per_slot};
+    const int h = tile_rows(S, n_experts);
     if (ids) {
-        hipLaunchKernelGGL((k_f8_plan<TY>), dim3(n_experts + 1), dim3(PLAN_THREADS), 0, s, ids, S, n_experts, TM, hdr,
-                           first, tile, slot_e, slot, route_w ? nullptr : Y, N);
+        hipLaunchKernelGGL((k_f8_plan<TY>), dim3(n_experts + 1), dim3(PLAN_THREADS), 0, c.s, ids, S, n_experts, h, hdr,
+                           first, tile_at, slot_e, slot, route_w ? nullptr : y, c.N);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const Table t{first, tile, slot, n_experts, S, top_k, x_per_slot};
-    hipLaunchKernelGGL((k_f8_matmul<TY, true>), dim3((unsigned)(gn * gm)), dim3(256), 0, s, W, wsc, N, K, X, xs,
-                       (int64_t)0, ldx, xs_ld, out, N, (int)gn, t);
-    hipError_t e = hipGetLastError();
+    // tiles of the worst case: every expert may end with a partial one
+    const int64_t gm = S / h + (S < n_experts ? S : n_experts);
+    hipError_t e;
+    if (h == 16) e = stream<1, 2, 8, 1, true>(c, gm);
+    else if (h == 32) e = stream<2, 2, 8, 1, true>(c, gm);
+    else e = tile<128, 128, 2, 2, 2, true>(c, gm);
     if (e != hipSuccess || !route_w) return e;
-    const int64_t want = ((int64_t)n_tokens * N + 255) / 256;
-    hipLaunchKernelGGL((k_f8_combine<TY>), dim3((unsigned)(want < 65536 ? want : 65536)), dim3(256), 0, s, out,
-                       slot_e, route_w, n_tokens, top_k, N, Y);
+    const int64_t want = ((int64_t)n_tokens * c.N + 255) / 256;
+    hipLaunchKernelGGL((k_f8_combine<TY>), dim3((unsigned)(want < 65536 ? want : 65536)), dim3(256), 0, c.s, c.Y,
+                       slot_e, route_w, n_tokens, top_k, c.N, y);
     return hipGetLastError();
 }
 
@@ -336,8 +493,8 @@ hipError_t matmul_id(const uint8_t* W, const float* wsc, int n_experts, int64_t 
 hipError_t gqk_f8_matmul(const uint8_t* W, const float* ws, int64_t N, int64_t K, const uint8_t* X, const float* xs,
                          int64_t M, int64_t ldx, int64_t xs_ld, void* Y, int y_dtype, int64_t ldy, hipStream_t s) {
     if (y_dtype == gqd::DT_F32)
-        return matmul(W, ws, N, K, X, xs, M, ldx, xs_ld, static_cast<float*>(Y), ldy, s);
-    return matmul(W, ws, N, K, X, xs, M, ldx, xs_ld, static_cast<uint16_t*>(Y), ldy, s);
+        return matmul(Call<float>{W, ws, N, K, X, xs, M, ldx, xs_ld, static_cast<float*>(Y), ldy, Table{}, s});
+    return matmul(Call<uint16_t>{W, ws, N, K, X, xs, M, ldx, xs_ld, static_cast<uint16_t*>(Y), ldy, Table{}, s});
 }
 
 size_t gqk_f8_matmul_id_ws_bytes(int n_experts, int n_tokens, int top_k, int64_t N, int y_dtype, int weighted) {
@@ -349,10 +506,10 @@ hipError_t gqk_f8_matmul_id(const uint8_t* W, const float* wsc, int n_experts, i
                             int64_t ldx, int64_t xs_ld, int x_per_slot, const float* route_w, void* Y, int y_dtype,
                             void* ws, hipStream_t s) {
     if (y_dtype == gqd::DT_F32)
-        return matmul_id(W, wsc, n_experts, N, K, ids, n_tokens, top_k, X, xs, ldx, xs_ld, x_per_slot, route_w,
-                         static_cast<float*>(Y), y_dtype, ws, s);
-    return matmul_id(W, wsc, n_experts, N, K, ids, n_tokens, top_k, X, xs, ldx, xs_ld, x_per_slot, route_w,
-                     static_cast<uint16_t*>(Y), y_dtype, ws, s);
+        return matmul_id(Call<float>{W, wsc, N, K, X, xs, 0, ldx, xs_ld, static_cast<float*>(Y), 0, Table{}, s},
+                         n_experts, ids, n_tokens, top_k, x_per_slot, route_w, y_dtype, ws);
+    return matmul_id(Call<uint16_t>{W, wsc, N, K, X, xs, 0, ldx, xs_ld, static_cast<uint16_t*>(Y), 0, Table{}, s},
+                     n_experts, ids, n_tokens, top_k, x_per_slot, route_w, y_dtype, ws);
 }
 
 hipError_t gqk_f8_matmul_id_bad_count(const void* ws, hipStream_t s, int32_t* n_bad) {
