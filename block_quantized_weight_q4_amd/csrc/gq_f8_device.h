@@ -62,6 +62,9 @@ __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi) {
     return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
+// Host: a grid dimension counts its threads in 32 bits.
+inline bool grid_ok(int64_t groups, int threads) { return groups * threads < ((int64_t)1 << 32); }
+
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 
 // Buffer resource of `bytes` (< 2^31) from base; loads beyond them give zeros.
@@ -69,8 +72,10 @@ __device__ __forceinline__ Rsrc make_rsrc(const void* base, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
 }
 constexpr uint32_t NOWHERE = 0x80000000u;  // an offset beyond every resource
-__device__ __forceinline__ u32x4 bld16(Rsrc r, uint32_t off) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+// off (below 2^31) where at < end, otherwise beyond every resource; in
+// arithmetic, because a branch would change how many loads are issued.
+__device__ __forceinline__ uint32_t within(uint32_t off, int at, int end) {
+    return off | ((uint32_t)(end - 1 - at) & NOWHERE);
 }
 
 // Stores four neighbouring results of a row (n .. n + 3, those below N) as fp32
@@ -95,14 +100,37 @@ __device__ __forceinline__ void store4(T* row, int64_t n, int64_t N, bool vec, f
         }
 }
 
+// Eight neighbouring results: lo, then hi.
+template <typename T>
+__device__ __forceinline__ void store8(T* row, int64_t n, int64_t N, bool vec, f32x4 lo, f32x4 hi) {
+    if constexpr (sizeof(T) == 2) {
+        if (vec && n + 8 <= N) {
+            const bf16x2 a = {(__bf16)lo[0], (__bf16)lo[1]}, b = {(__bf16)lo[2], (__bf16)lo[3]};
+            const bf16x2 c = {(__bf16)hi[0], (__bf16)hi[1]}, d = {(__bf16)hi[2], (__bf16)hi[3]};
+            *reinterpret_cast<u32x4*>(row + n) =
+                u32x4{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
+                      __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d)};
+            return;
+        }
+    }
+    const bool vec4 = sizeof(T) == 4 && vec;
+    store4(row, n, N, vec4, lo);
+    store4(row, n + 4, N, vec4, hi);
+}
+
+__device__ __forceinline__ u32x4 bld16(Rsrc r, uint32_t off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+}
+
 // ---- global-to-LDS copies (the loads that write LDS without registers) ----
 // Each lane of an instruction brings 16 bytes from an address of its own; they
 // land at lds + 16 * lane.  A kernel that uses them waits for them itself.
 typedef __attribute__((address_space(3))) void* LdsPtr;
 typedef const __attribute__((address_space(1))) void* GlobalPtr;
 
-__device__ __forceinline__ void copy16(Rsrc r, uint32_t off, uint8_t* lds) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)lds, 16, (int)off, 0, 0, 0);
+// (base: the same for the whole wavefront, off + base below 2^31)
+__device__ __forceinline__ void copy16(Rsrc r, uint32_t off, uint8_t* lds, uint32_t base = 0) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)lds, 16, (int)off, (int)base, 0, 0);
 }
 __device__ __forceinline__ void copy16(const uint8_t* p, uint8_t* lds) {
     __builtin_amdgcn_global_load_lds((GlobalPtr)p, (LdsPtr)lds, 16, 0, 0);
@@ -110,6 +138,9 @@ __device__ __forceinline__ void copy16(const uint8_t* p, uint8_t* lds) {
 // 4 bytes a lane, at lds + 4 * lane.
 __device__ __forceinline__ void copy4(const float* p, uint8_t* lds) {
     __builtin_amdgcn_global_load_lds((GlobalPtr)p, (LdsPtr)lds, 4, 0, 0);
+}
+__device__ __forceinline__ void copy4(Rsrc r, uint32_t off, uint8_t* lds, uint32_t base) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)lds, 4, (int)off, (int)base, 0, 0);
 }
 
 // Until at most N of this wavefront's loads and copies are outstanding

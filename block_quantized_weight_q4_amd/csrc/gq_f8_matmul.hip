@@ -10,6 +10,7 @@
 // the A operand and X the B operand, so a lane holds four consecutive columns
 // of one row of Y: one activation scale per lane and tile, and adjacent stores.
 #include <hip/hip_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "gq_f8_device.h"
@@ -21,21 +22,31 @@ using namespace gqf8;
 namespace {
 
 // ------------------------------------------------- slots by expert (plan) ----
-// Workspace: header (int [0] = invalid ids), the first slot and the first tile
-// of each expert (n_experts + 1 entries, the last one the totals), each slot's
+// Workspace: header (int [0] = invalid ids, [1] = tiles), the tiles, each slot's
 // expert (-1: invalid id), the slots by expert, the per-slot outputs of a
 // weighted product.
 struct WsLayout {
-    size_t off_first, off_tile, off_expert, off_slot, off_out, total;
+    int TM, max_tiles;
+    size_t off_tile, off_expert, off_slot, off_out, total;
 };
+
+// A tile: rows slots, from position start of the slots by expert, of expert e.
+struct alignas(16) TileEntry {
+    int e, start, rows, unused;
+};
+
+// Slots of a tile, from what every product of a layer has in common.
+int tile_rows(int64_t S, int n_experts);
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 WsLayout layout(int n_experts, int64_t S, int64_t N, int y_dtype, int weighted) {
     WsLayout L;
-    L.off_first = 256;
-    L.off_tile = L.off_first + up256(4 * ((size_t)n_experts + 1));
-    L.off_expert = L.off_tile + up256(4 * ((size_t)n_experts + 1));
+    L.TM = tile_rows(S, n_experts);
+    // the worst case: every expert ends with a partial tile
+    L.max_tiles = (int)(S / L.TM + (S < n_experts ? S : n_experts));
+    L.off_tile = 256;
+    L.off_expert = L.off_tile + up256(sizeof(TileEntry) * (size_t)L.max_tiles);
     L.off_slot = L.off_expert + up256(4 * (size_t)S);
     L.off_out = L.off_slot + up256(4 * (size_t)S);
     L.total = L.off_out + (weighted ? (size_t)S * (size_t)N * (y_dtype == gqd::DT_F32 ? 4 : 2) : 0);
@@ -43,23 +54,46 @@ WsLayout layout(int n_experts, int64_t S, int64_t N, int y_dtype, int weighted) 
 }
 
 struct Table {
-    const int *first, *tile, *slot;
+    const int* hdr;
+    const TileEntry* tile;
+    const int* slot;
     int n_experts, S, top_k, per_slot;
 };
 
-constexpr int PLAN_THREADS = 256;
 constexpr int MAX_E = 4096;
+
+// f(slot, id) for every slot, 4 * blockDim.x slots at a time; every thread of
+// the workgroup makes the same number of calls (past the end: id INT_MAX, which
+// no expert has).
+template <typename F>
+__device__ __forceinline__ void each_slot(const int32_t* __restrict__ ids, int S, F f) {
+    for (int s0 = 0; s0 < S; s0 += 4 * blockDim.x) {
+        const int s = s0 + 4 * threadIdx.x;
+        int4 v = make_int4(INT_MAX, INT_MAX, INT_MAX, INT_MAX);
+        if (s + 4 <= S) {
+            v = *reinterpret_cast<const int4*>(ids + s);  // (ids are 16-byte aligned)
+        } else {
+            if (s < S) v.x = ids[s];
+            if (s + 1 < S) v.y = ids[s + 1];
+            if (s + 2 < S) v.z = ids[s + 2];
+        }
+        f(s, v.x);
+        f(s + 1, v.y);
+        f(s + 2, v.z);
+        f(s + 3, v.w);
+    }
+}
 
 // Workgroup e < n_experts lists the slots of expert e (their order among
 // themselves does not reach any result: each output row is computed on its
-// own).  The last workgroup counts the slots of every expert and writes the
-// first slot, the first tile (of TM slots) and the totals, and zeroes the
-// output rows of invalid slots.
+// own): once over the ids to count the smaller ones, once to place its own.
+// The last workgroup counts the slots of every expert, cuts them into tiles of
+// at most TM and zeroes the output rows of invalid slots.  All read all ids, from the caches: one launch instead
+// of a chain of counting, scanning and placing.
 template <typename TY>
-__global__ __launch_bounds__(PLAN_THREADS) void k_f8_plan(const int32_t* __restrict__ ids, int S, int n_experts,
-                                                          int TM, int* __restrict__ hdr, int* __restrict__ first,
-                                                          int* __restrict__ tile, int* __restrict__ slot_e,
-                                                          int* __restrict__ slot, TY* __restrict__ y, int64_t N) {
+__global__ __launch_bounds__(1024) void k_f8_plan(const int32_t* __restrict__ ids, int S, int n_experts, int TM,
+                                                  int* __restrict__ hdr, TileEntry* __restrict__ tile,
+                                                  int* __restrict__ slot_e, int* __restrict__ slot, TY* __restrict__ y, int64_t N) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int e = blockIdx.x;
     if (e < n_experts) {
@@ -70,35 +104,33 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_f8_plan(const int32_t* __restr
         }
         __syncthreads();
         int less = 0;
-        for (int s = tid; s < S; s += PLAN_THREADS) less += ids[s] >= 0 && ids[s] < e;
+        each_slot(ids, S, [&](int, int id) { less += id >= 0 && id < e; });
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) less += __shfl_xor(less, off, 64);
         if (lane == 0) atomicAdd(&n_less, less);
         __syncthreads();
         const int base = n_less;
-        for (int s0 = 0; s0 < S; s0 += PLAN_THREADS) {
-            const int s = s0 + tid;
-            const bool mine = s < S && ids[s] == e;
-            const uint64_t vote = __ballot(mine);
-            if (vote == 0) continue;
+        each_slot(ids, S, [&](int s, int id) {
+            const uint64_t vote = __ballot(id == e);
+            if (vote == 0) return;  // (the same for the whole wavefront)
             int at = 0;
             if (lane == 0) at = atomicAdd(&n_here, __popcll(vote));
             at = __builtin_amdgcn_readfirstlane(at);
-            if (mine) slot[base + at + __popcll(vote & ((1ull << lane) - 1))] = s;
-        }
+            if (id == e) slot[base + at + __popcll(vote & ((1ull << lane) - 1))] = s;
+        });
         return;
     }
     __shared__ int count[MAX_E];
     __shared__ int n_bad;
     if (tid == 0) n_bad = 0;
-    for (int i = tid; i < n_experts; i += PLAN_THREADS) count[i] = 0;
+    for (int i = tid; i < n_experts; i += blockDim.x) count[i] = 0;
     __syncthreads();
-    for (int s = tid; s < S; s += PLAN_THREADS) {
-        const int i = ids[s];
-        const bool ok = i >= 0 && i < n_experts;
-        slot_e[s] = ok ? i : -1;
-        atomicAdd(ok ? &count[i] : &n_bad, 1);
-    }
+    each_slot(ids, S, [&](int s, int id) {
+        if (s >= S) return;
+        const bool ok = id >= 0 && id < n_experts;
+        slot_e[s] = ok ? id : -1;
+        atomicAdd(ok ? &count[id] : &n_bad, 1);
+    });
     __syncthreads();
     if (tid < 64) {
         // exclusive scans over the experts by one wavefront: each lane a run
@@ -121,44 +153,33 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_f8_plan(const int32_t* __restr
         }
         int ra = ia - a, rb = ib - b;
         for (int i = lo; i < hi; ++i) {
-            first[i] = ra;
-            tile[i] = rb;
+            for (int c = 0; c < count[i]; c += TM)
+                tile[rb++] = TileEntry{i, ra + c, count[i] - c < TM ? count[i] - c : TM, 0};
             ra += count[i];
-            rb += (count[i] + TM - 1) / TM;
         }
         if (tid == 63) {
-            first[n_experts] = ia;
-            tile[n_experts] = ib;
             hdr[0] = n_bad;
+            hdr[1] = ib;
         }
     }
     if (y && n_bad)
         for (int s = 0; s < S; ++s) {
             const int i = ids[s];
             if (i < 0 || i >= n_experts)
-                for (int64_t n = tid; n < N; n += PLAN_THREADS) store_as(y + s * N + n, 0.0f);
+                for (int64_t n = tid; n < N; n += blockDim.x) store_as(y + s * N + n, 0.0f);
         }
 }
 
-// The expert and the slots [start, start + rows) of tile i; rows == 0 where
-// the table has no such tile.  Every field is clamped to its range.
-__device__ __forceinline__ void tile_of(const Table& t, int i, int TM, int& e, int& start, int& rows) {
-    int lo = 0, hi = t.n_experts;  // the last e with tile[e] <= i
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (t.tile[mid] <= i) lo = mid;
-        else hi = mid;
-    }
-    e = lo;
-    rows = 0;
-    start = 0;
-    if (i >= t.tile[t.n_experts]) return;
-    const int64_t a = (int64_t)t.first[e] + ((int64_t)i - t.tile[e]) * TM;
-    int64_t b = t.first[e + 1];
-    b = b < t.S ? b : t.S;
-    if (a < 0 || a >= b) return;
-    start = (int)a;
-    rows = (int)(b - a < TM ? b - a : TM);
+// The expert and the slots [start, start + rows) of tile i; false where the
+// table has no such tile.  Every field is clamped to its range.
+__device__ __forceinline__ bool tile_of(const Table& t, int i, int TM, int& e, int& start, int& rows) {
+    const TileEntry v = t.tile[i];
+    if (i >= t.hdr[1]) return false;
+    e = (unsigned)v.e < (unsigned)t.n_experts ? v.e : t.n_experts - 1;
+    start = (unsigned)v.start < (unsigned)t.S ? v.start : t.S - 1;
+    const int most = t.S - start < TM ? t.S - start : TM;
+    rows = v.rows < most ? v.rows : most;
+    return rows > 0;
 }
 
 // ------------------------------------------------------- many rows (tiles) ----
@@ -172,176 +193,317 @@ __device__ __forceinline__ int xcd_order(int id, int total) {
 }
 
 // BM rows of X by BN rows of W; WM x WN wavefronts of (BM / WM) x (BN / WN).
-// Both tiles of a 128-input block go to LDS by global-to-LDS copies, NB - 1
-// blocks ahead, in rows of 128 bytes whose 16-byte chunks are swizzled so that
+// Both tiles of a 128-input block go to LDS by global-to-LDS copies, NB blocks
+// ahead, in rows of 128 bytes whose 16-byte chunks are swizzled so that
 // operand reads cover all banks; the block's activation scales come along.
 // One barrier a block.
-template <int BM, int BN, int WM, int WN, int NB, typename TY, bool ROUTED>
+//
+// Operand row a of the MFMA tiles 2 p and 2 p + 1 is the tile's column 32 p +
+// 8 (a / 4) + a % 4 (+ 4 for the second), so that a lane ends up with eight
+// neighbouring columns of one row of Y: 16-byte stores, 64-byte runs.
+//
+// FAR (routed): X may span more than 2^31 bytes, so its rows are addressed by
+// pointers, two registers each, instead of offsets.
+template <int BM, int BN, int WM, int WN, int NB, typename TY, bool ROUTED, bool FAR>
 struct Tile {
     static constexpr int WV = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
     static constexpr int XI = BM / 8 / WV, WI = BN / 8 / WV;  // copies of a wavefront and block
     static constexpr int SX = (BM + BN) * BLK, STAGE = SX + WV * 256;
     static constexpr int LOADS = XI + WI + 1;
+    static constexpr bool MANY = ROUTED && BM < 256;  // (with the 256 x 256 tile's registers the longer loop does not fit)
     static_assert(BM % (8 * WV) == 0 && BN % (8 * WV) == 0 && WV > BM / 64 && BN / WN <= BLK, "tile shape");
 
+    // swizzle of W's rows: (r / 2 % 2, r / 8 % 4), the rows of one operand read
+    static __device__ __forceinline__ int wswz(int r) { return ((r >> 1) & 1) | (((r >> 3) & 3) << 1); }
+
+    // rows of X from m0 (routed: the slots from `start`) by `count` tiles of
+    // columns from n0, one after another without a gap: the copies run NB blocks
+    // ahead of the products, over the end of a tile into the next (MANY).
     static __device__ __forceinline__ void run(const uint8_t* __restrict__ W, const float* __restrict__ wsc,
                                                int64_t N, int64_t K, const uint8_t* __restrict__ X,
                                                const float* __restrict__ xs, int64_t ldx, int64_t xs_ld,
                                                TY* __restrict__ Y, int64_t ldy, int64_t m0, int64_t n0, int rows,
-                                               int start, const Table& t, uint8_t* smem) {
+                                               int start, int count, const Table& t, uint8_t* smem) {
         const int lane = threadIdx.x & 63;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int fr = lane & 15, fq = lane >> 4;
         const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
         const int KB = (int)((K + BLK - 1) / BLK);
-        const int64_t w_rows = N - n0 < BN ? N - n0 : BN;
-        const Rsrc wr = make_rsrc(W + n0 * K, w_rows * K);
-        const Rsrc xr = make_rsrc(X + m0 * ldx, (int64_t)rows * ldx);  // (dense)
         auto slot_of = [&](int i) -> int64_t {
             const unsigned s = (unsigned)t.slot[start + (i < rows ? i : rows - 1)];
             return s < (unsigned)t.S ? (int64_t)s : t.S - 1;
         };
-        auto x_row = [&](int i) -> int64_t {
-            if constexpr (ROUTED) return t.per_slot ? slot_of(i) : slot_of(i) / t.top_k;
-            else return m0 + (i < rows ? i : rows - 1);
-        };
-        // copies: wavefront w brings rows 8 (w + WV u) .. + 7 of either tile
-        uint32_t xoff[XI], woff[WI];
-        const uint8_t* xp[XI];
+        auto routed_row = [&](int i) -> int64_t { return t.per_slot ? slot_of(i) : slot_of(i) / t.top_k; };
+
+        // Copies.  Wavefront w brings rows 8 (w + WV u) .. + 7 of either tile; the
+        // chunk of row r that a lane copies is the one its position holds.
+        const int lr = 8 * wave + (lane >> 3);
+        static_assert(WV % 4 == 0, "the swizzle of a lane's rows is the same for all of its copies");
+        const uint32_t xchunk = 16u * (uint32_t)((lane & 7) ^ ((lr >> 1) & 7));
+        const uint32_t wchunk = 16u * (uint32_t)((lane & 7) ^ wswz(lr));
+        const uint32_t woff = (uint32_t)(lr * K) + wchunk;
+        // X: one offset and a common step, or (routed) each copy's own row
+        uint32_t xoff[ROUTED ? XI : 1];
+        const uint8_t* xp[FAR ? XI : 1];
 #pragma unroll
-        for (int u = 0; u < XI; ++u) {
-            const int r = 8 * (wave + WV * u) + (lane >> 3);
-            if constexpr (ROUTED) xp[u] = X + x_row(r) * ldx;
-            else xoff[u] = (uint32_t)(r * ldx);
+        for (int u = 0; u < (ROUTED ? XI : 1); ++u) {
+            if constexpr (FAR) xp[u] = X + routed_row(lr + 8 * WV * u) * ldx;
+            else if constexpr (ROUTED) xoff[u] = (uint32_t)(routed_row(lr + 8 * WV * u) * ldx) + xchunk;
+            else xoff[u] = (uint32_t)(lr * ldx) + xchunk;
         }
-#pragma unroll
-        for (int u = 0; u < WI; ++u) woff[u] = (uint32_t)((8 * (wave + WV * u) + (lane >> 3)) * K);
-        // the chunk of row r that its lane copies: (lane % 8) ^ (r / 2 % 8), r = 8 (wave + WV u) + lane / 8
-        const uint32_t chunk = 16u * (uint32_t)((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
-        static_assert(WV % 2 == 0, "the swizzle of a lane's rows is the same for all of its copies");
-        // one copy of 64 scales: wavefronts below BM / 64 those of X, the others W's (of wavefront w's columns: lane w)
-        const float* sp;
-        int64_t sstep;
-        if (wave < BM / 64) {
-            sp = xs + x_row(64 * wave + lane);
-            sstep = xs_ld;
+        const int64_t x_rows = t.per_slot ? t.S : t.S / (t.top_k > 0 ? t.top_k : 1);
+        const Rsrc xr = ROUTED ? make_rsrc(X, FAR ? 0 : x_rows * ldx) : make_rsrc(X + m0 * ldx, (int64_t)rows * ldx);
+        // one copy of 64 scales: wavefronts below BM / 64 those of X, the others
+        // W's (lane w: of wavefront w's columns), from sbase[slane + ck * sstep];
+        // a tile further (routed), W's lie snext on, as far as the last row of blocks
+        static_assert(!ROUTED || BN % BLK == 0, "whole blocks of columns");
+        const bool xwave = wave < BM / 64;
+        const float* sbase = xwave ? xs : wsc;
+        const int64_t sstep = xwave ? xs_ld : 1;
+        const int slast = xwave ? INT_MAX : (int)((N - 1) / BLK) * KB, snext = xwave ? 0 : BN / BLK * KB;
+        int slane;
+        if (xwave) {
+            const int i = 64 * wave + lane;
+            if constexpr (ROUTED) slane = (int)routed_row(i);
+            else slane = (int)m0 + (i < rows ? i : rows - 1);
         } else {
             const int64_t n = n0 + (lane % WV / WM) * (BN / WN);
-            sp = wsc + ((n < N ? n : N - 1) / BLK) * KB;
-            sstep = 1;
+            slane = (int)((n < N ? n : N - 1) / BLK) * KB;
         }
-        auto load = [&](int kb) {
-            uint8_t* d = smem + (kb % NB) * STAGE;
-            const int64_t k = (int64_t)kb * BLK + chunk;
-            const bool in = k < K;
+        // what the copies read next: block ck of the columns from cn, into buffer cg
+        int ck = 0, cg = 0;
+        int64_t cn = n0;
+        const int64_t n_end = n0 + (int64_t)count * BN;
+        auto load = [&]() {
+            uint8_t* d = smem + cg * STAGE;
+            cg = cg + 1 == NB ? 0 : cg + 1;
+            const int k = ck * BLK;
+            const int left = (int)K - k, wleft = cn < n_end ? left : 0;  // (W past the last tile: zeros)
+            const uint32_t wo = within(woff, (int)wchunk, wleft);
+            const int xk = k + ((int)xchunk < left ? (int)xchunk : -k);  // (FAR: past K the row's first chunk, times zeros)
+            const Rsrc wr = make_rsrc(W + cn * K, cn < N ? (N - cn < BN ? N - cn : BN) * K : 0);
 #pragma unroll
             for (int u = 0; u < XI; ++u) {
                 uint8_t* l = d + (wave + WV * u) * 1024;
-                if constexpr (ROUTED) copy16(xp[u] + (in ? k : 0), l);
-                else copy16(xr, in ? xoff[u] + (uint32_t)k : NOWHERE, l);
+                if constexpr (FAR) copy16(xp[u] + xk, l);
+                else if constexpr (ROUTED) copy16(xr, within(xoff[u], (int)xchunk, left), l, (uint32_t)k);
+                else copy16(xr, within(xoff[0], (int)xchunk, left), l, (uint32_t)(8 * WV * u * ldx + k));
             }
 #pragma unroll
             for (int u = 0; u < WI; ++u)
-                copy16(wr, in ? woff[u] + (uint32_t)k : NOWHERE, d + BM * BLK + (wave + WV * u) * 1024);
-            copy4(sp + (kb < KB ? kb : KB - 1) * sstep, d + SX + wave * 256);
+                copy16(wr, wo, d + BM * BLK + (wave + WV * u) * 1024, (uint32_t)(8 * WV * u * K + k));
+            copy4(sbase + (slane + (ck < KB ? ck : KB - 1) * sstep), d + SX + wave * 256);
+            ++ck;
+            if constexpr (MANY) {
+                const bool wrap = ck == KB;  // (no branch: it would split what is scheduled together)
+                ck = wrap ? 0 : ck;
+                cn += wrap ? BN : 0;
+                slane += wrap ? snext : 0;
+                slane = slane < slast ? slane : slast;
+            }
         };
         f32x4 acc[NT][MT];
+        auto clear = [&]() {
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{};
-        if (KB > 0) {
+                for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{};
+        };
+        const bool vec = (ldy & (16 / (int)sizeof(TY) - 1)) == 0;
+        int y_slot[ROUTED ? MT : 1];
+        if constexpr (ROUTED) {
 #pragma unroll
-            for (int s = 0; s < NB - 1; ++s) load(s);
-            wait_copies<(NB - 2) * LOADS>();
-            gqd::lds_barrier();
+            for (int j = 0; j < MT; ++j) y_slot[j] = (int)slot_of(wm + 16 * j + fr);
         }
-        // 16-byte positions of this lane's two chunks of an operand row (rows 16 i + fr: the same for every i)
-        const int p0 = pos128(fr, fq), p1 = pos128(fr, 4 + fq);
-        for (int kb = 0; kb < KB; ++kb) {
-            load(kb + NB - 1);
-            const uint8_t* d = smem + (kb % NB) * STAGE;
-            const u32x4* dx = reinterpret_cast<const u32x4*>(d + wm * BLK);
-            const u32x4* dw = reinterpret_cast<const u32x4*>(d + (BM + wn) * BLK);
-            const float* ds = reinterpret_cast<const float*>(d + SX);
-            const float s_w = ds[(BM / 64) * 64 + wave];
-            float s[MT];
-            i32x8 x[MT];
+        auto store = [&]() {
+            int l = lane;  // opaque: otherwise all the addresses are computed ahead of the loop, and spilled
+            __asm__ volatile("" : "+v"(l));
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
-                x[j] = join(dx[128 * j + p0], dx[128 * j + p1]);
-                s[j] = s_w * ds[wm + 16 * j + fr];
+                const int row = wm + 16 * j + (l & 15);
+                if (row >= rows) continue;
+                TY* y = Y + (ROUTED ? y_slot[ROUTED ? j : 0] : m0 + row) * ldy;
+#pragma unroll
+                for (int i = 0; i < NT; i += 2)
+                    store8(y, n0 + wn + 16 * i + 8 * (l >> 4), N, vec, acc[i][j], acc[i + 1][j]);
             }
+        };
+        clear();
+        if (KB == 0) {
+            for (int i = 0; i < count; ++i, n0 += BN) store();
+            return;
+        }
+
+        // Operands.  16-byte positions of this lane's two chunks of an operand row: of X in rows 16 j + fr, of W in
+        // rows 32 (i / 2) + 8 (fr / 4) + 4 (i % 2) + fr % 4 (whose swizzle is the same for every i).
+        const int p0 = pos128(fr, fq), p1 = pos128(fr, 4 + fq);
+        const int ar = 8 * (fr >> 2) + (fr & 3), w0 = ar * 8 + (fq ^ wswz(ar)), w1 = ar * 8 + ((4 + fq) ^ wswz(ar));
+        auto w_operand = [&](int g, int i) {
+            const u32x4* d = reinterpret_cast<const u32x4*>(smem + g * STAGE + (BM + wn) * BLK);
+            const int at = 256 * (i >> 1) + 32 * (i & 1);
+            return join(d[at + w0], d[at + w1]);
+        };
+        auto x_operand = [&](int g, int j) {
+            const u32x4* d = reinterpret_cast<const u32x4*>(smem + g * STAGE + wm * BLK);
+            return join(d[128 * j + p0], d[128 * j + p1]);
+        };
+        auto scales = [&](int g, float (&s)[MT]) {
+            const float* d = reinterpret_cast<const float*>(smem + g * STAGE + SX);
+            const float s_w = d[(BM / 64) * 64 + wave];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) s[j] = s_w * d[wm + 16 * j + fr];
+        };
+        auto product = [&](i32x8 a, const i32x8 (&x)[MT], f32x4 (&p)[MT]) {
             if constexpr (sizeof(TY) == 4) {
-                Wide xw[MT];
+                const Wide aw = widen(a);
 #pragma unroll
-                for (int j = 0; j < MT; ++j) xw[j] = widen(x[j]);
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const Wide a = widen(join(dw[128 * i + p0], dw[128 * i + p1]));
-#pragma unroll
-                    for (int j = 0; j < MT; ++j) {
-                        const f32x4 p = mfma16(a, xw[j]);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], s[j], acc[i][j][r]);
-                    }
-                }
+                for (int j = 0; j < MT; ++j) p[j] = mfma16(aw, widen(x[j]));
             } else {
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const i32x8 a = join(dw[128 * i + p0], dw[128 * i + p1]);
+                for (int j = 0; j < MT; ++j) p[j] = mfma8(a, x[j]);
+            }
+        };
+        auto add = [&](int i, const f32x4 (&p)[MT], const float (&s)[MT]) {
 #pragma unroll
-                    for (int j = 0; j < MT; ++j) {
-                        const f32x4 p = mfma8(a, x[j]);
+            for (int j = 0; j < MT; ++j)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], s[j], acc[i][j][r]);
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[j][r], s[j], acc[i][j][r]);
+        };
+        // A block, whose operands x, first a and scales s are in registers: each
+        // W operand is read while the one before it is multiplied, the last before
+        // the barrier.  The barrier then says two things: the next block has landed
+        // for everyone, and nobody needs this block's buffer, into which the one NB
+        // ahead is sent; the next block's first operands are read while the last
+        // products run.
+#pragma unroll
+        for (int b = 0; b < NB; ++b) load();
+        wait_copies<(NB - 1) * LOADS>();
+        gqd::lds_barrier();
+        if (ROUTED && wm >= rows) {
+            // nothing of this wavefront's rows is used: it brings data only
+            for (int64_t b = 0; b < (int64_t)count * KB; ++b) {
+                wait_copies<(NB - 2) * LOADS>();
+                gqd::lds_barrier();
+                load();
+            }
+            wait_copies<0>();
+            return;
+        }
+        i32x8 x[MT], a = w_operand(0, 0);
+        float s[MT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) x[j] = x_operand(0, j);
+        scales(0, s);
+        int g = 0;
+        for (int tile = 0;;) {
+            int kb = 0;
+            do {
+                f32x4 p[MT];
+#pragma unroll
+                for (int i = 0; i < NT - 1; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    const i32x8 next = w_operand(g, i + 1);
+                    f32x4 q[MT];
+                    product(a, x, q);
+                    if (i > 0) add(i - 1, p, s);
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) p[j] = q[j];
+                    a = next;
+                    if constexpr (sizeof(TY) == 2) {
+                        // the reads after the first product: at its wait nothing younger is outstanding
+#pragma unroll
+                        for (int j = 0; j < MT; ++j) {
+                            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);              // MFMA
+                            if (j == 0) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+                            if (i > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // VALU
+                        }
                     }
                 }
-            }
-            wait_copies<(NB - 2) * LOADS>();
-            gqd::lds_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+                wait_copies<(NB - 2) * LOADS>();
+                gqd::lds_barrier();
+                load();
+                g = g + 1 == NB ? 0 : g + 1;
+                f32x4 q[MT];
+                product(a, x, q);
+                __builtin_amdgcn_sched_barrier(0);  // (x, a are read into their own registers again)
+                add(NT - 2, p, s);
+                a = w_operand(g, 0);
+#pragma unroll
+                for (int j = 0; j < MT; ++j) x[j] = x_operand(g, j);
+                add(NT - 1, q, s);
+                scales(g, s);
+            } while (++kb < KB);
+            store();
+            if (!MANY || ++tile == count) break;
+            clear();
+            n0 += BN;
         }
         wait_copies<0>();
-        const bool vec = (ldy & 3) == 0;
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            const int row = wm + 16 * j + fr;
-            if (row >= rows) continue;
-            TY* y = Y + (ROUTED ? slot_of(row) : m0 + row) * ldy;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) store4(y, n0 + wn + 16 * i + 4 * fq, N, vec, acc[i][j]);
-        }
     }
 };
 
-template <int BM, int BN, int WM, int WN, int NB, typename TY, bool ROUTED>
+// Dense.  Workgroups from n_full on take quarters of the tiles from n_full on
+// (QUARTERS): the last, partial round of 256 x 256 tiles would take as long as a
+// whole one on a part of the CUs.
+template <int BM, int BN, int WM, int WN, int NB, typename TY, bool QUARTERS>
 __global__ __launch_bounds__(64 * WM * WN) void k_f8_tile(const uint8_t* __restrict__ W, const float* __restrict__ wsc,
                                                           int64_t N, int64_t K, const uint8_t* __restrict__ X,
                                                           const float* __restrict__ xs, int64_t M, int64_t ldx,
                                                           int64_t xs_ld, TY* __restrict__ Y, int64_t ldy, int gm,
-                                                          int gn, Table t) {
-    using T = Tile<BM, BN, WM, WN, NB, TY, ROUTED>;
-    __shared__ __align__(16) uint8_t smem[NB * T::STAGE];
-    const int id = xcd_order(blockIdx.x, gm * gn);
-    int tm, tn, e = 0, start = 0, rows;
-    if constexpr (ROUTED) {
-        tm = id / gn;  // an expert's tiles side by side: they share its rows of X
-        tn = id % gn;
-        tile_of(t, tm, BM, e, start, rows);
-        if (rows == 0) return;
-        W += (int64_t)e * N * K;
-        wsc += (int64_t)e * ((N + BLK - 1) / BLK) * ((K + BLK - 1) / BLK);
-    } else {
-        // bands of at most 12 row tiles
+                                                          int gn, int n_full) {
+    using T = Tile<BM, BN, WM, WN, NB, TY, false, false>;
+    constexpr int D = QUARTERS ? 2 : 1;
+    using Q = Tile<BM / D, BN / D, WM, WN, NB * D, TY, false, false>;
+    constexpr int LDS = NB * T::STAGE, QLDS = NB * D * Q::STAGE;
+    __shared__ __align__(16) uint8_t smem[LDS > QLDS ? LDS : QLDS];
+    const Table none{};
+    auto place = [&](int id, int64_t& m0, int64_t& n0) {
+        // bands of at most 12 row tiles, each walked column of tiles by column
         const int bands = (gm + 11) / 12, h = (gm + bands - 1) / bands;
         const int band = id / (h * gn), hb = gm - band * h < h ? gm - band * h : h;
-        const int r = id - band * h * gn;
-        tm = band * h + r % hb;
-        tn = r / hb;
-        const int64_t left = M - (int64_t)tm * BM;
-        rows = (int)(left < BM ? left : BM);
+        const int c = id - band * h * gn;
+        m0 = (int64_t)(band * h + c % hb) * BM;
+        n0 = (int64_t)(c / hb) * BN;
+    };
+    int64_t m0, n0;
+    if constexpr (QUARTERS) {
+        const int q = (int)blockIdx.x - n_full;
+        if (q >= 0) {
+            place(n_full + (q >> 2), m0, n0);
+            m0 += (q & 1) * (BM / 2);
+            n0 += (q >> 1 & 1) * (BN / 2);
+            if (m0 >= M || n0 >= N) return;
+            const int64_t left = M - m0;
+            Q::run(W, wsc, N, K, X, xs, ldx, xs_ld, Y, ldy, m0, n0, (int)(left < BM / 2 ? left : BM / 2), 0, 1, none,
+                   smem);
+            return;
+        }
     }
-    T::run(W, wsc, N, K, X, xs, ldx, xs_ld, Y, ldy, (int64_t)tm * BM, (int64_t)tn * BN, rows, start, t, smem);
+    place(xcd_order(blockIdx.x, n_full), m0, n0);
+    T::run(W, wsc, N, K, X, xs, ldx, xs_ld, Y, ldy, m0, n0, (int)(M - m0 < BM ? M - m0 : BM), 0, 1, none, smem);
+}
+
+// Routed: the rows of table tile blockIdx.x / split and the blockIdx.x % split-th
+// share of the gn columns of tiles.
+template <int BM, int BN, int WM, int WN, int NB, typename TY, bool FAR>
+__global__ __launch_bounds__(64 * WM * WN) void k_f8_tile_id(const uint8_t* __restrict__ W,
+                                                             const float* __restrict__ wsc, int64_t N, int64_t K,
+                                                             const uint8_t* __restrict__ X,
+                                                             const float* __restrict__ xs, int64_t ldx, int64_t xs_ld,
+                                                             TY* __restrict__ Y, int gm, int gn, int split, Table t) {
+    using T = Tile<BM, BN, WM, WN, NB, TY, true, FAR>;
+    __shared__ __align__(16) uint8_t smem[NB * T::STAGE];
+    // (the grid is sized for the most tiles there can be: only the real ones are dealt out to the XCDs)
+    const int tiles = t.hdr[1], real = (tiles < gm ? tiles : gm) * split;
+    if ((int)blockIdx.x >= real) return;
+    const int id = xcd_order(blockIdx.x, real), tm = id / split, part = id % split;
+    const int first = (int)((int64_t)gn * part / split), end = (int)((int64_t)gn * (part + 1) / split);
+    int e, start, rows;
+    if (!tile_of(t, tm, BM, e, start, rows)) return;
+    W += (int64_t)e * N * K;
+    wsc += (int64_t)e * ((N + BLK - 1) / BLK) * ((K + BLK - 1) / BLK);
+    T::run(W, wsc, N, K, X, xs, ldx, xs_ld, Y, N, 0, (int64_t)first * BN, rows, start, end - first, t, smem);
 }
 
 // A few rows: the stream kernel, 16 MT rows of X and 16 NT of W a workgroup.
@@ -356,8 +518,7 @@ __global__ __launch_bounds__(64 * WV) void k_f8_stream(const uint8_t* __restrict
     const int tn = blockIdx.x % gn, tm = blockIdx.x / gn;
     int e = 0, start = 0, rows;
     if constexpr (ROUTED) {
-        tile_of(t, tm, 16 * MT, e, start, rows);
-        if (rows == 0) return;
+        if (!tile_of(t, tm, 16 * MT, e, start, rows)) return;
         W += (int64_t)e * N * K;
         wsc += (int64_t)e * ((N + BLK - 1) / BLK) * ((K + BLK - 1) / BLK);
     } else {
@@ -380,28 +541,58 @@ __global__ __launch_bounds__(64 * WV) void k_f8_stream(const uint8_t* __restrict
 }
 
 // y[t][n] = sum_j rw[t][j] slot[t][j][n], j in increasing order, slots of
-// invalid ids left out.
-template <typename TY>
+// invalid ids left out.  Bound by the slots' bytes; a workgroup takes a token
+// and 256 V columns of it, V of them a thread (16 bytes, where N allows).
+template <typename TY, int V>
 __global__ __launch_bounds__(256) void k_f8_combine(const TY* __restrict__ slots, const int* __restrict__ slot_e,
-                                                    const float* __restrict__ rw, int n_tokens, int top_k, int64_t N,
+                                                    const float* __restrict__ rw, int top_k, int64_t N,
                                                     TY* __restrict__ y) {
-    const int64_t total = (int64_t)n_tokens * N;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / N, n = i - t * N;
-        float sum = 0.0f;
-        for (int j = 0; j < top_k; ++j) {
-            const int64_t s = t * top_k + j;
-            if (slot_e[s] < 0) continue;
-            float v;
-            if constexpr (sizeof(TY) == 4) v = slots[s * N + n];
-            else v = gqd::bf2f(slots[s * N + n]);
-            sum = __builtin_fmaf(rw[s], v, sum);
+    const int64_t t = blockIdx.x;
+    const int64_t n = ((int64_t)blockIdx.y * 256 + threadIdx.x) * V;
+    if (n >= N) return;
+    float sum[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] = 0.0f;
+#pragma unroll 4
+    for (int j = 0; j < top_k; ++j) {
+        const int64_t s = t * top_k + j;
+        const float w = rw[s];
+        const bool ok = slot_e[s] >= 0;  // (otherwise nobody wrote the row)
+        const TY* p = slots + s * N + n;
+        if constexpr (V == 1) {
+            const float v = sizeof(TY) == 4 ? (float)*p : gqd::bf2f((uint16_t)*p);
+            sum[0] = ok ? __builtin_fmaf(w, v, sum[0]) : sum[0];
+        } else if constexpr (sizeof(TY) == 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] = ok ? __builtin_fmaf(w, v[i], sum[i]) : sum[i];
+        } else {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float f = __builtin_bit_cast(float, i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+                sum[i] = ok ? __builtin_fmaf(w, f, sum[i]) : sum[i];
+            }
         }
-        store_as(y + i, sum);
+    }
+    if constexpr (V == 1) {
+        store_as(y + t * N + n, sum[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            store4(y + t * N, n + i, N, true, f32x4{sum[i], sum[i + 1], sum[i + 2], sum[i + 3]});
     }
 }
 
-bool grid_ok(int64_t groups, int threads) { return groups * threads < ((int64_t)1 << 32); }
+template <int V, typename TY>
+hipError_t combine(const TY* slots, const int* slot_e, const float* rw, int n_tokens, int top_k, int64_t N, TY* y,
+                   hipStream_t s) {
+    const int64_t gx = (N + 256 * V - 1) / (256 * V);
+    if (gx > 65535) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_f8_combine<TY, V>), dim3((unsigned)n_tokens, (unsigned)gx), dim3(256), 0, s, slots, slot_e,
+                       rw, top_k, N, y);
+    return hipGetLastError();
+}
 
 // One call's operands.
 template <typename TY>
@@ -428,28 +619,75 @@ hipError_t stream(const Call<TY>& c, int64_t gm) {
     return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, int NB, bool ROUTED, typename TY>
-hipError_t tile(const Call<TY>& c, int64_t gm) {
-    const int64_t gn = (c.N + BN - 1) / BN;
-    if (!grid_ok(gn * gm, 64 * WM * WN)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_f8_tile<BM, BN, WM, WN, NB, TY, ROUTED>), dim3((unsigned)(gn * gm)), dim3(64 * WM * WN), 0,
-                       c.s, c.W, c.wsc, c.N, c.K, c.X, c.xs, c.M, c.ldx, c.xs_ld, c.Y, c.ldy, (int)gm, (int)gn, c.t);
+template <int BM, int BN, int WM, int WN, int NB, bool QUARTERS, typename TY>
+hipError_t tile(const Call<TY>& c) {
+    const int64_t gm = (c.M + BM - 1) / BM, gn = (c.N + BN - 1) / BN, tiles = gm * gn;
+    const int64_t cus = gqk_cu_count(), tail = tiles % cus;
+    // quarters of the last round's tiles where they fit in one round themselves
+    const int64_t n_full = QUARTERS && tiles > cus && 4 * tail <= cus ? tiles - tail : tiles;
+    const int64_t grid = n_full + 4 * (tiles - n_full);
+    if (!grid_ok(grid, 64 * WM * WN)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_f8_tile<BM, BN, WM, WN, NB, TY, QUARTERS>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, c.s,
+                       c.W, c.wsc, c.N, c.K, c.X, c.xs, c.M, c.ldx, c.xs_ld, c.Y, c.ldy, (int)gm, (int)gn,
+                       (int)n_full);
     return hipGetLastError();
 }
 
-template <typename TY>
-hipError_t matmul(const Call<TY>& c) {
-    auto tiles = [&](int h) { return (c.M + h - 1) / h; };
-    if (c.M <= 16) return stream<1, 2, 8, 1, false>(c, tiles(16));
-    if (c.M <= 256) return stream<2, 2, 8, 1, false>(c, tiles(32));
-    if constexpr (sizeof(TY) == 2)
-        if (c.M >= 1024 && c.N >= 2048) return tile<256, 256, 4, 2, 2, false>(c, tiles(256));
-    return tile<128, 128, 2, 2, 2, false>(c, tiles(128));
+template <int BM, int BN, int WM, int WN, int NB, bool FAR, typename TY>
+hipError_t tile_id(const Call<TY>& c, int64_t gm) {
+    // two tiles of columns a workgroup (one with 256 rows): the second one's copies hide the first one's end
+    const int64_t gn = (c.N + BN - 1) / BN, split = BM < 256 ? (gn + 1) / 2 : gn;
+    if (gn > INT_MAX / 2 || !grid_ok(gm * split, 64 * WM * WN)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_f8_tile_id<BM, BN, WM, WN, NB, TY, FAR>), dim3((unsigned)(gm * split)), dim3(64 * WM * WN),
+                       0, c.s, c.W, c.wsc, c.N, c.K, c.X, c.xs, c.ldx, c.xs_ld, c.Y, (int)gm, (int)gn, (int)split,
+                       c.t);
+    return hipGetLastError();
 }
 
-// Rows of a tile of slots, from what every product of a layer has in common.
+// Which kernel: measured at N x K of 1024 x 2560, 5120 x 5120, 2560 x 9728 and
+// 17408 x 5120, 16 to 2048 rows.  What decides is how many tiles there are for
+// the CUs.  Few 64 x 128 tiles: the stream kernel, which splits K (256 rows of
+// 2560 x 9728: 15.8 us against 31.6 us in tiles).  Up to one a CU: those tiles,
+// eight wavefronts each and four blocks ahead (2048 rows of 1024 x 2560: 12.1
+// against 14.8 us two blocks ahead, 19.9 us streamed); up to one 128 x 128 tile
+// a CU: those in the same way (512 rows of 5120 x 5120: 28.8 against 32.6 us);
+// then two of these a CU, two blocks ahead (2048 rows of 2560 x 9728: 74.1
+// against 93.1 us), until 256 x 256 tiles fill half of the CUs (2048 rows of
+// 5120 x 5120: 71.0 against 73.2 us, of 17408 x 5120: 225 against 243 us).  An
+// fp32 result's products run at half the rate, which favours the stream kernel
+// longer (512 rows of 2560 x 9728: 37.3 against 53.8 us) and leaves 256 x 256
+// without registers.
+template <typename TY>
+hipError_t matmul(const Call<TY>& c) {
+    auto tiles = [&](int64_t h, int64_t w) { return ((c.M + h - 1) / h) * ((c.N + w - 1) / w); };
+    const int64_t cus = gqk_cu_count();
+    if (tiles(64, 128) <= (sizeof(TY) == 4 ? 3 * cus / 4 : cus / 2)) {
+        // rows of X and of W a workgroup: tall ones read either side less often, as long as 3 in 4 CUs have one
+        if (c.M <= 16) return stream<1, 2, 8, 1, false>(c, (c.M + 15) / 16);
+        if (c.M <= 64) return stream<2, 2, 8, 1, false>(c, (c.M + 31) / 32);
+        if (tiles(48, 64) >= 3 * cus / 4) return stream<3, 4, 8, 1, false>(c, (c.M + 47) / 48);
+        return stream<3, 2, 8, 1, false>(c, (c.M + 47) / 48);
+    }
+    if constexpr (sizeof(TY) == 2) {
+        if (c.M <= 32) return stream<2, 2, 8, 1, false>(c, (c.M + 31) / 32);
+        if (tiles(64, 128) <= cus) return tile<64, 128, 2, 4, 4, false>(c);
+        if (tiles(128, 128) <= cus) return tile<128, 128, 4, 2, 4, false>(c);
+        if (tiles(256, 256) >= cus / 2) return tile<256, 256, 4, 2, 2, true>(c);
+    } else {
+        if (c.M <= 64) return stream<2, 2, 8, 1, false>(c, (c.M + 31) / 32);
+    }
+    return tile<128, 128, 4, 2, 2, false>(c);
+}
+
+// Measured at 64 experts of 1408 x 2816 and 2816 x 704 by the slots an expert
+// has on average: 16 slots a tile up to 8 (4 each: 45 us against 56 us with 64;
+// 34.5 us against 30.4 us with short rows, where the tile kernel takes the
+// small tiles), 64 up to 48 (24 each: 63 against 77 and 65 us with 16 and 128),
+// 128 up to 320 (256 each: 134 against 160 and 137 us with 64 and 256), 256
+// above (375 each: 158 against 184 us).
 int tile_rows(int64_t S, int n_experts) {
-    return S <= 16 * (int64_t)n_experts ? 16 : S <= 64 * (int64_t)n_experts ? 32 : 128;
+    const int64_t E = n_experts;
+    return S <= 8 * E ? 16 : S <= 48 * E ? 64 : S <= 320 * E ? 128 : 256;
 }
 
 template <typename TY>
@@ -459,33 +697,33 @@ hipError_t matmul_id(Call<TY> c, int n_experts, const int32_t* ids, int n_tokens
     const WsLayout L = layout(n_experts, S, c.N, y_dtype, route_w != nullptr);
     uint8_t* base = static_cast<uint8_t*>(ws);
     int* hdr = reinterpret_cast<int*>(base);
-    int* first = reinterpret_cast<int*>(base + L.off_first);
-    int* tile_at = reinterpret_cast<int*>(base + L.off_tile);
+    auto* tiles = reinterpret_cast<TileEntry*>(base + L.off_tile);
     int* slot_e = reinterpret_cast<int*>(base + L.off_expert);
     int* slot = reinterpret_cast<int*>(base + L.off_slot);
     TY* y = c.Y;
     if (route_w) c.Y = reinterpret_cast<TY*>(base + L.off_out);
     c.M = S;
     c.ldy = c.N;
-    c.t = Table{first, tile_at, slot, n_experts, S, top_k, x_per_slot};
-    const int h = tile_rows(S, n_experts);
+    c.t = Table{hdr, tiles, slot, n_experts, S, top_k, x_per_slot};
+    const int h = L.TM, gm = L.max_tiles;
+    const int64_t rows = x_per_slot ? S : n_tokens;
     if (ids) {
-        hipLaunchKernelGGL((k_f8_plan<TY>), dim3(n_experts + 1), dim3(PLAN_THREADS), 0, c.s, ids, S, n_experts, h, hdr,
-                           first, tile_at, slot_e, slot, route_w ? nullptr : y, c.N);
+        hipLaunchKernelGGL((k_f8_plan<TY>), dim3(n_experts + 1), dim3(S <= 4096 ? 256 : 1024), 0, c.s, ids, S, n_experts, h, hdr,
+                           tiles, slot_e, slot, route_w ? nullptr : y, c.N);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    // tiles of the worst case: every expert may end with a partial one
-    const int64_t gm = S / h + (S < n_experts ? S : n_experts);
     hipError_t e;
-    if (h == 16) e = stream<1, 2, 8, 1, true>(c, gm);
-    else if (h == 32) e = stream<2, 2, 8, 1, true>(c, gm);
-    else e = tile<128, 128, 2, 2, 2, true>(c, gm);
+    if (rows * c.ldx >= INT_MAX) e = h == 16 ? stream<1, 2, 8, 1, true>(c, gm) : tile_id<256, 128, 4, 2, 2, true>(c, gm);
+    else if (h == 16) e = c.K < 1024 ? tile_id<64, 128, 1, 4, 2, false>(c, gm) : stream<1, 2, 8, 1, true>(c, gm);
+    else if (h == 64) e = tile_id<64, 128, 1, 4, 2, false>(c, gm);
+    else if (h == 128) e = tile_id<128, 128, 2, 2, 2, false>(c, gm);
+    else if constexpr (sizeof(TY) == 2) e = tile_id<256, 256, 4, 2, 2, false>(c, gm);
+    else e = tile_id<256, 128, 4, 2, 2, false>(c, gm);
     if (e != hipSuccess || !route_w) return e;
-    const int64_t want = ((int64_t)n_tokens * c.N + 255) / 256;
-    hipLaunchKernelGGL((k_f8_combine<TY>), dim3((unsigned)(want < 65536 ? want : 65536)), dim3(256), 0, c.s, c.Y,
-                       slot_e, route_w, n_tokens, top_k, c.N, y);
-    return hipGetLastError();
+    constexpr int V = 16 / sizeof(TY);
+    if (c.N % V == 0) return combine<V>(c.Y, slot_e, route_w, n_tokens, top_k, c.N, y, c.s);
+    return combine<1>(c.Y, slot_e, route_w, n_tokens, top_k, c.N, y, c.s);
 }
 
 }  // namespace

@@ -29,21 +29,23 @@ enum { X_E4M3 = 0, X_BF16 = 1, X_F32 = 2 };
 __device__ __forceinline__ int pos128(int r, int c) { return r * 8 + (c ^ ((r >> 1) & 7)); }
 __device__ __forceinline__ int pos_wide(int r, int c, int chunks) { return r * chunks + (c ^ (r & 15)); }
 
-// hi and lo operands of eight fp32 values: hi their upper 16 bits, lo the
-// remainder rounded to bf16 (together within 2^-17 of the value).
-__device__ __forceinline__ void split8(const u32x4& p, const u32x4& q, bf16x8& hi, bf16x8& lo) {
-    u32x4 h, l;
+// Eight fp32 values as three bf16 operands whose sum they are: the upper 16
+// bits, those of what is left, and the rest (8 + 8 + 8 bits of the mantissa:
+// exact while the last is a normal number).
+__device__ __forceinline__ void split8(const u32x4& p, const u32x4& q, bf16x8 (&x)[3]) {
+    u32x4 part[3];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t u0 = i < 2 ? p[2 * i] : q[2 * i - 4], u1 = i < 2 ? p[2 * i + 1] : q[2 * i - 3];
-        h[i] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);  // the upper halves of both
-        const float r0 = __builtin_bit_cast(float, u0) - __builtin_bit_cast(float, u0 & 0xffff0000u);
-        const float r1 = __builtin_bit_cast(float, u1) - __builtin_bit_cast(float, u1 & 0xffff0000u);
-        const bf16x2 t = {(__bf16)r0, (__bf16)r1};
-        l[i] = __builtin_bit_cast(uint32_t, t);
+        uint32_t u0 = i < 2 ? p[2 * i] : q[2 * i - 4], u1 = i < 2 ? p[2 * i + 1] : q[2 * i - 3];
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+            part[c][i] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);  // the upper halves of both
+            u0 = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u0) - __builtin_bit_cast(float, u0 & 0xffff0000u));
+            u1 = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u1) - __builtin_bit_cast(float, u1 & 0xffff0000u));
+        }
     }
-    hi = __builtin_bit_cast(bf16x8, h);
-    lo = __builtin_bit_cast(bf16x8, l);
+#pragma unroll
+    for (int c = 0; c < 3; ++c) x[c] = __builtin_bit_cast(bf16x8, part[c]);
 }
 
 // Sizes of one block of one wavefront.  XR: rows of X held (a vector product
@@ -55,12 +57,16 @@ struct Stream {
     static constexpr int XI = XR * ROW / 1024;                                // copies of X
     static constexpr int SCALES = 1024 * (WI + XI);                           // 64 fp32: of X's rows, the last of W
     static constexpr int BYTES = SCALES + 256;
+    // fp32 vectors, eight at most: each value is split once, by one lane, and
+    // passed on through LDS (sixteen fill all the operand's columns anyway)
+    static constexpr bool SHARE = XM == X_F32 && XR <= 8;
+    static constexpr int PARTS = SHARE ? 3 * XR * 256 : 0;
     static_assert(XR * ROW % 1024 == 0 && XR <= 16 * MT && MT <= 3, "whole copies, one of scales");
 };
 
 // x_row(i): row of X that row i of the tile stands for, any valid
 // one past the tile's rows; y_row(i): address of the output row (i < rows).
-// smem: W * D * BYTES bytes, at least W * NT * MT KB.
+// smem: W * (D * BYTES + PARTS) bytes, at least W * NT * MT KB.
 template <int MT, int NT, int W, int D, int XM, int XR, typename TY, typename XRow, typename YRow>
 __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, const float* __restrict__ wsc, int64_t n0,
                                             int64_t N, int64_t K, const uint8_t* __restrict__ X,
@@ -75,7 +81,7 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
     const int64_t w_rows = N - n0 < 16 * NT ? N - n0 : 16 * NT;
     const Rsrc wr = make_rsrc(Wt + n0 * K, w_rows * K);
     const float* wsb = wsc + (n0 / BLK) * KB;  // (16 NT rows lie in one block of 128)
-    uint8_t* mine = smem + wave * (D * S::BYTES);
+    uint8_t* mine = smem + wave * (D * S::BYTES + S::PARTS);
 
     // copies: lane's row and 16-byte chunk of each instruction.  What lies past
     // K is read as zeros from W (beyond the resource), and from X as the row's
@@ -108,9 +114,10 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
         const int kc = kb < KB ? kb : KB - 1;
         uint8_t* d = mine + slot * S::BYTES;
         const int64_t k = (int64_t)kb * BLK;
+        const int left = k < K ? (int)(K - k) : 0;
 #pragma unroll
         for (int t = 0; t < S::WI; ++t)
-            copy16(wr, k + wchunk[t & 1] < K ? woff[t] + (uint32_t)k : NOWHERE, d + 1024 * t);
+            copy16(wr, within(woff[t], wchunk[t & 1], left), d + 1024 * t, (uint32_t)k);
 #pragma unroll
         for (int t = 0; t < S::XI; ++t)
             copy16(xp[t] + (k * XB + xchunk[t] < xbytes ? k * XB + xchunk[t] : 0), d + 1024 * (S::WI + t));
@@ -165,22 +172,44 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
         } else {
             // chunk c = 4 h + q of the weights meets inputs 16 c .. 16 c + 15 of the vectors
             constexpr int PER = XM == X_BF16 ? 2 : 4;  // 16-byte pieces of them
+            constexpr int PARTS = XM == X_BF16 ? 1 : 3;
             const int xr = fr & (XR - 1);
-            u32x4 x[2][PER];
+            bf16x8 v[2][2][PARTS];
+            if constexpr (S::SHARE) {
+                // eight inputs a lane and turn; their three parts at [part][row][eight]
+                bf16x8* parts = reinterpret_cast<bf16x8*>(mine + D * S::BYTES);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                for (int u = 0; u < XR / 4; ++u) {
+                    const int row = 4 * u + (lane >> 4), o = lane & 15;
+                    bf16x8 y[3];
+                    split8(xd[pos_wide(row, 2 * o, CH)], xd[pos_wide(row, 2 * o + 1, CH)], y);
 #pragma unroll
-                for (int c = 0; c < PER; ++c) x[h][c] = xd[pos_wide(xr, PER * (4 * h + fq) + c, CH)];
-            wait_reads();
-            load(kb + D * W, slot);
-            bf16x8 hi[2][2], lo[2][2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if constexpr (XM == X_BF16) hi[h][c] = __builtin_bit_cast(bf16x8, x[h][c]);
-                    else split8(x[h][2 * c], x[h][2 * c + 1], hi[h][c], lo[h][c]);
+                    for (int e = 0; e < 3; ++e) parts[pos_wide(e * XR + row, o, 16)] = y[e];
                 }
+                wait_reads();
+                load(kb + D * W, slot);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 3; ++e) v[h][c][e] = parts[pos_wide(e * XR + xr, 2 * (4 * h + fq) + c, 16)];
+            } else {
+                u32x4 x[2][PER];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < PER; ++c) x[h][c] = xd[pos_wide(xr, PER * (4 * h + fq) + c, CH)];
+                wait_reads();
+                load(kb + D * W, slot);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if constexpr (XM == X_BF16) v[h][c][0] = __builtin_bit_cast(bf16x8, x[h][c]);
+                        else split8(x[h][2 * c], x[h][2 * c + 1], v[h][c]);
+                    }
+            }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 p[i][0] = f32x4{};
@@ -189,9 +218,9 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const bf16x8 w = widen((int)a[i][h][2 * c], (int)a[i][h][2 * c + 1]);
-                        if constexpr (XM == X_F32)
-                            p[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, lo[h][c], p[i][0], 0, 0, 0);
-                        p[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, hi[h][c], p[i][0], 0, 0, 0);
+#pragma unroll
+                        for (int e = PARTS - 1; e >= 0; --e)
+                            p[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, v[h][c][e], p[i][0], 0, 0, 0);
                     }
             }
         }

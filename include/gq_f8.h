@@ -58,10 +58,11 @@ gq_status gq_f8_glu_quant(const void* g, const void* u, gq_dtype dtype, int64_t 
  * vectors (GQ_ERR_UNSUPPORTED above).  x: [batch][K] of x_dtype (GQ_F32 or
  * GQ_BF16), not quantised; y: [batch][N] of y_dtype (GQ_F32 or GQ_BF16).
  * N == 0 is a no-op; K == 0 writes zeros.
- * Accuracy: weights and bf16 activations enter exactly, fp32 activations with
- * a relative error of at most 2^-17; products are exact and sums fp32: within
- * (K / 128 + 162) * 2^-23 (+ 2^-17) times sum |w x|, then y_dtype's rounding.
- * Each vector's result does not depend on the other vectors' values. */
+ * Accuracy: weights and activations enter exactly (fp32 ones as three bf16
+ * parts; what of a value lies below 2^-126 is lost), products are exact and
+ * sums fp32: within (K / 128 + 162) * 2^-23 times sum |w x| (fp32 vectors:
+ * K / 128 + 418, their parts being three sums), then y_dtype's rounding.  An infinite activation gives NaN or an infinity.  Each vector's
+ * result does not depend on the other vectors' values. */
 gq_status gq_f8_matvec(const void* W, const float* wscales, int64_t N, int64_t K, const void* x, gq_dtype x_dtype,
                        int32_t batch, void* y, gq_dtype y_dtype, hipStream_t stream);
 

@@ -321,3 +321,38 @@ def test_matmul_id_edges(gq):
         assert (Y == 0).all()
     r = Routed(4, 0, 2, 20, 64, False, "f32")
     r.call(gq, False)
+
+
+@pytest.mark.parametrize("T,out", [(560, "f32"), (3000, "bf16"), (40, "bf16")])
+def test_rows_far_apart(gq, T, out):
+    """Rows of X 4 MB apart, so that their offsets pass 2^31 bytes: the routed and the dense product."""
+    ld, K, N = 1 << 22, 144, 72
+    r = Routed(8, T, 2, N, K, False, out)
+    big = torch.empty(T, ld, dtype=torch.uint8, device="cuda")
+    X = big[:, :K]
+    X.copy_(dev(r.xq))
+    n = gq.gq_f8_matmul_id_workspace(8, T, 2, N, DT[out], False)
+    ws = torch.full((n,), 0xAB, dtype=torch.uint8, device="cuda")
+    Y = torch.full((T, 2, N), float("nan"), dtype=DT[out], device="cuda")
+    gq.gq_f8_matmul_id(dev(r.q), dev(r.s), dev(r.ids), X, dev(r.xs), Y, ws)
+    ref, tol = r.ref()
+    near(Y, ref, tol)
+    Z = torch.full((T, N), float("nan"), dtype=DT[out], device="cuda")
+    gq.gq_f8_matmul(dev(r.q[0]), dev(r.s[0]), X, dev(r.xs), Z)
+    near(Z, *matmul_ref(r.q[0], r.s[0], r.xq, r.xs, out))
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("E,T,k,N,K", [(2, 700, 1, 515, 400), (3, 1100, 1, 130, 1040), (2, 90, 1, 260, 272),
+                                       (5, 45, 2, 390, 1168), (40, 33, 4, 130, 2064)])
+def test_matmul_id_tile_heights(gq, E, T, k, N, K, out):
+    """Average slots an expert from few to many: every height of tile, with partial ones."""
+    Routed(E, T, k, N, K, False, out, skew=0.3).check(gq, False)
+
+
+@pytest.mark.parametrize("M,N,K,out", [(70, 20000, 128, "bf16"), (300, 9000, 256, "bf16"), (1500, 2600, 144, "bf16"),
+                                       (1030, 17300, 128, "bf16"), (150, 17000, 144, "f32"), (2000, 130, 272, "bf16"),
+                                       (100, 40, 1040, "bf16"), (130, 7000, 272, "f32")])
+def test_matmul_every_kernel(gq, M, N, K, out):
+    """Sizes on both sides of the rules that choose a kernel, the split last round of tiles among them."""
+    matmul_case(gq, M, N, K, out)
