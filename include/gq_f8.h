@@ -47,8 +47,8 @@ gq_status gq_f8_quant(const void* x, gq_dtype x_dtype, int64_t M, int64_t K, int
 
 /* The gated unit's elementwise step straight to 8 bits: gq_f8_quant of
  *   h[m][k] = act(g[m][k]) * u[m][k]
- * computed in fp32 and not rounded in between (act as gq_matvec_glu's; h
- * within 2^-20 |h| + the fp32 rounding of exp / tanh).  g, u: [M][ldg],
+ * computed in fp32 and not rounded in between (act as gq_matvec_glu's; h within
+ * 2^-20 |h|, with the tanh form within 2^-20 (|h| + |g u|)).  g, u: [M][ldg],
  * [M][ldu] of dtype (the halves of one gate|up product, or two). */
 gq_status gq_f8_glu_quant(const void* g, const void* u, gq_dtype dtype, int64_t M, int64_t K, int64_t ldg,
                           int64_t ldu, gq_act act, int32_t pow2, void* q, int64_t ldq, float* scales, int64_t s_ld,
