@@ -433,7 +433,7 @@ def gq_route_matvec_id_glu(t, experts_gate: torch.Tensor, experts_up: torch.Tens
 # than the GPU, so every function first tests that all is as it should be in
 # one expression of cheap properties (about 1 us); only if that fails the
 # checks run one by one, to name what is wrong -- or to pass, for the forms
-# that the short test leaves out (single rows, empty tensors).
+# that the short test leaves out (odd strides of single rows and empty tensors).
 
 _F8 = (torch.float8_e4m3fn, torch.uint8)
 _HALF_OR_F32 = (torch.float32, torch.bfloat16, torch.float16)
@@ -520,9 +520,10 @@ def gq_f8_quant(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, pow2: bo
     fp32 scale for 128 inputs of a row, [ceil(K / 128)][M]."""
     try:
         (M, K), d = x.shape, x.get_device()
-        ok = (M > 1 and d >= 0 and d == q.get_device() == scales.get_device() and x.dtype in _HALF_OR_F32 and
+        ok = (d >= 0 and d == q.get_device() == scales.get_device() and x.dtype in _HALF_OR_F32 and
               q.dtype in _F8 and scales.dtype is _f32 and q.shape == (M, K) and
-              scales.shape == ((K + 127) // 128, M) and x.stride(1) == q.stride(1) == scales.stride(1) == 1)
+              scales.shape == ((K + 127) // 128, M) and x.stride(1) == q.stride(1) == 1 and
+              (scales.stride(1) == 1 or M == 1))
     except (AttributeError, ValueError):
         ok = False
     if not ok:
@@ -537,10 +538,10 @@ def gq_f8_glu_quant(g: torch.Tensor, u: torch.Tensor, act: str, q: torch.Tensor,
     """gq_f8_quant of act(g) * u; g, u [M][K] of one type (fp32 / bf16 / fp16)."""
     try:
         (M, K), d = g.shape, g.get_device()
-        ok = (M > 1 and d >= 0 and d == u.get_device() == q.get_device() == scales.get_device() and
+        ok = (d >= 0 and d == u.get_device() == q.get_device() == scales.get_device() and
               g.dtype in _HALF_OR_F32 and u.dtype is g.dtype and q.dtype in _F8 and scales.dtype is _f32 and
               u.shape == q.shape == (M, K) and scales.shape == ((K + 127) // 128, M) and act in ACTS and
-              g.stride(1) == u.stride(1) == q.stride(1) == scales.stride(1) == 1)
+              g.stride(1) == u.stride(1) == q.stride(1) == 1 and (scales.stride(1) == 1 or M == 1))
     except (AttributeError, ValueError):
         ok = False
     if not ok:
@@ -617,13 +618,13 @@ def gq_f8_matmul(W: torch.Tensor, wscales: torch.Tensor, X: torch.Tensor, xscale
     times the weights W [N][K] with wscales [ceil(N / 128)][ceil(K / 128)]."""
     try:
         (N, K), d, M = W.shape, W.get_device(), X.shape[0]
-        ok = (M > 1 and d >= 0 and
+        ok = (d >= 0 and
               d == wscales.get_device() == X.get_device() == xscales.get_device() == Y.get_device() and
               W.dtype in _F8 and X.dtype in _F8 and wscales.dtype is _f32 and xscales.dtype is _f32 and
               Y.dtype in _ACT and wscales.shape == ((N + 127) // 128, (K + 127) // 128) and X.shape == (M, K) and
               xscales.shape == ((K + 127) // 128, M) and Y.shape == (M, N) and
               W.is_contiguous() and wscales.is_contiguous() and
-              X.stride(1) == xscales.stride(1) == Y.stride(1) == 1)
+              X.stride(1) == Y.stride(1) == 1 and (xscales.stride(1) == 1 or M == 1))
     except (AttributeError, ValueError, IndexError):
         ok = False
     if not ok:
@@ -676,7 +677,7 @@ def gq_f8_matmul_id(W: torch.Tensor, wscales: torch.Tensor, ids, X: torch.Tensor
     try:
         (n_experts, N, K), d, rows = W.shape, W.get_device(), X.shape[0]
         n_tokens, top_k = ids if reuse else ids.shape
-        ok = (n_tokens > 1 and d >= 0 and d == wscales.get_device() == X.get_device() == xscales.get_device() ==
+        ok = (d >= 0 and d == wscales.get_device() == X.get_device() == xscales.get_device() ==
               Y.get_device() == ws.get_device() and W.dtype in _F8 and X.dtype in _F8 and wscales.dtype is _f32 and
               xscales.dtype is _f32 and Y.dtype in _ACT and ws.dtype is _u8 and
               wscales.shape == (n_experts, (N + 127) // 128, (K + 127) // 128) and X.shape == (rows, K) and
@@ -685,7 +686,7 @@ def gq_f8_matmul_id(W: torch.Tensor, wscales: torch.Tensor, ids, X: torch.Tensor
               (Y.shape == (n_tokens, top_k, N) if route_w is None else
                Y.shape == (n_tokens, N) and route_w.shape == (n_tokens, top_k) and route_w.dtype is _f32 and
                route_w.get_device() == d and route_w.is_contiguous()) and
-              X.stride(1) == xscales.stride(1) == 1 and W.is_contiguous() and wscales.is_contiguous() and
+              X.stride(1) == 1 and (xscales.stride(1) == 1 or rows == 1) and W.is_contiguous() and wscales.is_contiguous() and
               Y.is_contiguous() and ws.is_contiguous())
     except (AttributeError, ValueError, IndexError):
         ok = False

@@ -54,11 +54,15 @@ WsLayout layout(int n_experts, int64_t S, int64_t N, int y_dtype, int weighted) 
 }
 
 struct Table {
-    const int* hdr;
-    const TileEntry* tile;
-    const int* slot;
+    int* hdr;
+    TileEntry* tile;
+    int *slot_e, *slot;
     int n_experts, S, top_k, per_slot;
+    const int32_t* ids;  // given: the kernel makes the table itself (SMALL slots at most)
+    int zero;            // it also zeroes the rows of invalid slots
 };
+
+constexpr int SMALL = 64;
 
 constexpr int MAX_E = 4096;
 
@@ -187,6 +191,61 @@ __device__ __forceinline__ bool tile_of(const Table& t, int i, int TM, int& e, i
     const int most = t.S - start < TM ? t.S - start : TM;
     rows = v.rows < most ? v.rows : most;
     return rows > 0;
+}
+
+// The same for a call with at most SMALL slots that is given ids: every
+// wavefront finds tile i's slots itself, lane s standing for slot s, and the
+// launch of a plan is saved (8 tokens x 8 of 128 experts: 5 of 22 us).  Slots of
+// one expert find each other by a ballot for each bit of the id; the experts
+// take their places in the order of their first slots.  own: the tile's slots.
+// Workgroup 0 writes the header and each slot's expert, the first one of each
+// tile its part of the table, for later calls without ids.
+__device__ __forceinline__ bool tile_from_ids(const Table& t, int i, int TM, bool first_column, int& e, int& start,
+                                              int& rows, int* own) {
+    const int lane = threadIdx.x & 63;
+    const bool lead = threadIdx.x < 64;
+    const int id = lane < t.S ? t.ids[lane] : -1;
+    const bool ok = id >= 0 && id < t.n_experts;
+    const uint64_t valid = __ballot(ok);
+    uint64_t same = valid;
+#pragma unroll
+    for (int b = 0; b < 12; ++b) {  // (n_experts <= 4096)
+        const bool bit = (id >> b) & 1;
+        const uint64_t m = __ballot(bit);
+        same &= bit ? m : ~m;
+    }
+    const int count = __popcll(same), rank = __popcll(same & ((1ull << lane) - 1));
+    const bool head = ok && rank == 0;
+    // slots (low half) and tiles of the experts up to this lane's
+    const int n = head ? count | (((count + TM - 1) / TM) << 16) : 0;
+    int incl = n;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(incl, off, 64);
+        if (lane >= off) incl += v;
+    }
+    const int before = incl - n, tb = before >> 16;
+    if (blockIdx.x == 0 && lead) {
+        if (lane < t.S) t.slot_e[lane] = ok ? id : -1;
+        if (lane == 63) {
+            t.hdr[0] = t.S - __popcll(valid);
+            t.hdr[1] = incl >> 16;
+        }
+    }
+    const uint64_t hit = __ballot(head && tb <= i && i < tb + (n >> 16));
+    if (hit == 0) return false;
+    const int l = __builtin_ctzll(hit);
+    e = __builtin_amdgcn_readlane(id, l);
+    const int c = i - __builtin_amdgcn_readlane(tb, l), left = __builtin_amdgcn_readlane(count, l) - c * TM;
+    start = (__builtin_amdgcn_readlane(before, l) & 0xffff) + c * TM;
+    rows = left < TM ? left : TM;
+    const int place = rank - c * TM;
+    if (ok && id == e && place >= 0 && place < rows) {
+        own[place] = lane;
+        if (first_column && lead) t.slot[start + place] = lane;
+    }
+    if (first_column && threadIdx.x == 0) t.tile[i] = TileEntry{e, start, rows, 0};
+    return true;
 }
 
 // ------------------------------------------------------- many rows (tiles) ----
@@ -528,8 +587,23 @@ __global__ __launch_bounds__(64 * WV) void k_f8_stream(const uint8_t* __restrict
     __shared__ __align__(16) uint8_t smem[RING > JOIN ? RING : JOIN];
     const int tn = blockIdx.x % gn, tm = blockIdx.x / gn;
     int e = 0, start = 0, rows;
+    __shared__ int own[ROUTED ? 16 * MT : 1];
+    const int* slots = nullptr;
     if constexpr (ROUTED) {
-        if (!tile_of(t, tm, 16 * MT, e, start, rows)) return;
+        if (t.ids) {
+            if (blockIdx.x == 0 && t.zero)
+                for (int s = 0; s < t.S; ++s) {
+                    const int id = t.ids[s];
+                    if (id < 0 || id >= t.n_experts)
+                        for (int64_t n = threadIdx.x; n < N; n += 64 * WV) store_as(Y + s * N + n, 0.0f);
+                }
+            if (!tile_from_ids(t, tm, 16 * MT, tn == 0, e, start, rows, own)) return;
+            __syncthreads();
+            slots = own;
+        } else {
+            if (!tile_of(t, tm, 16 * MT, e, start, rows)) return;
+            slots = t.slot + start;
+        }
         W += (int64_t)e * N * K;
         wsc += (int64_t)e * ((N + BLK - 1) / BLK) * ((K + BLK - 1) / BLK);
     } else {
@@ -539,7 +613,7 @@ __global__ __launch_bounds__(64 * WV) void k_f8_stream(const uint8_t* __restrict
     auto row_of = [&](int i) -> int64_t {
         const int c = i < rows ? i : rows - 1;
         if constexpr (ROUTED) {
-            const unsigned s = (unsigned)t.slot[start + c];
+            const unsigned s = (unsigned)slots[c];
             return s < (unsigned)t.S ? (int64_t)s : t.S - 1;
         } else {
             return (int64_t)tm * (16 * MT) + c;
@@ -691,14 +765,25 @@ hipError_t matmul(const Call<TY>& c) {
 }
 
 // Measured at 64 experts of 1408 x 2816 and 2816 x 704 by the slots an expert
-// has on average: 16 slots a tile up to 8 (4 each: 45 us against 56 us with 64;
-// 34.5 us against 30.4 us with short rows, where the tile kernel takes the
-// small tiles), 64 up to 48 (24 each: 63 against 77 and 65 us with 16 and 128),
+// has on average: 16 slots a tile up to 8 (4 each: 45 us against 56 us with
+// 64), 64 up to 48 (24 each: 63 against 77 and 65 us with 16 and 128),
 // 128 up to 320 (256 each: 134 against 160 and 137 us with 64 and 256), 256
 // above (375 each: 158 against 184 us).
 int tile_rows(int64_t S, int n_experts) {
     const int64_t E = n_experts;
     return S <= 8 * E ? 16 : S <= 48 * E ? 64 : S <= 320 * E ? 128 : 256;
+}
+
+// Few slots an expert.  There are many workgroups, so wavefronts that share one
+// cost more (the join, the blocks that do not divide) than they hide, but for
+// long rows (8 tokens x 8 of 128 experts, 704 x 2816: 17.7, 17.7 and 20.7 us
+// with 2, 4 and 8 wavefronts; 2816 x 704: 18.4, 21.9 and 31.6 us; 2 tokens x 4
+// of 16, 2560 x 9728: 35.7, 28.4 and 29.6 us).
+template <typename TY>
+hipError_t stream_id(const Call<TY>& c, int64_t gm) {
+    if (c.K <= 8 * BLK) return stream<1, 2, 2, 1, true>(c, gm);
+    if (c.K <= 32 * BLK) return stream<1, 2, 4, 1, true>(c, gm);
+    return stream<1, 2, 8, 1, true>(c, gm);
 }
 
 template <typename TY>
@@ -715,18 +800,19 @@ hipError_t matmul_id(Call<TY> c, int n_experts, const int32_t* ids, int n_tokens
     if (route_w) c.Y = reinterpret_cast<TY*>(base + L.off_out);
     c.M = S;
     c.ldy = c.N;
-    c.t = Table{hdr, tiles, slot, n_experts, S, top_k, x_per_slot};
     const int h = L.TM, gm = L.max_tiles;
+    const bool small = ids && S <= SMALL && h == 16;
+    c.t = Table{hdr, tiles, slot_e, slot, n_experts, S, top_k, x_per_slot, small ? ids : nullptr, !route_w};
     const int64_t rows = x_per_slot ? S : n_tokens;
-    if (ids) {
+    if (ids && !small) {
         hipLaunchKernelGGL((k_f8_plan<TY>), dim3(n_experts + 1), dim3(S <= 4096 ? 256 : 1024), 0, c.s, ids, S, n_experts, h, hdr,
                            tiles, slot_e, slot, route_w ? nullptr : y, c.N);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     hipError_t e;
-    if (rows * c.ldx >= INT_MAX) e = h == 16 ? stream<1, 2, 8, 1, true>(c, gm) : tile_id<256, 128, 4, 2, 2, true>(c, gm);
-    else if (h == 16) e = c.K < 1024 ? tile_id<64, 128, 1, 4, 2, false>(c, gm) : stream<1, 2, 8, 1, true>(c, gm);
+    if (h == 16) e = stream_id(c, gm);
+    else if (rows * c.ldx >= INT_MAX) e = tile_id<256, 128, 4, 2, 2, true>(c, gm);
     else if (h == 64) e = tile_id<64, 128, 1, 4, 2, false>(c, gm);
     else if (h == 128) e = tile_id<128, 128, 2, 2, 2, false>(c, gm);
     else if constexpr (sizeof(TY) == 2) e = tile_id<256, 256, 4, 2, 2, false>(c, gm);
