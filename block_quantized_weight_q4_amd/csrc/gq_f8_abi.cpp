@@ -24,8 +24,11 @@ int64_t blocks(int64_t n) { return (n + 127) / 128; }
 
 bool bad_k(int64_t K) { return K < 0 || K % 16 != 0 || K > MAX_K; }
 
-// M, N <= 2^31 - 256: tiles are counted in 32 bits
+// M <= 2^31 - 256: tiles are counted in 32 bits; N and a call's tokens to route:
+// a launch has at most 2^32 threads
 constexpr int64_t MAX_ROWS = ((int64_t)1 << 31) - 256;
+constexpr int64_t MAX_N = ((int64_t)1 << 28) - 256;
+constexpr int64_t MAX_TOKENS = (int64_t)1 << 25;
 
 gq_status check_quant(gq_dtype dtype, int64_t M, int64_t K, int64_t ld0, int64_t ld1, int64_t ldq, int64_t s_ld) {
     if (dtype != GQ_F32 && dtype != GQ_BF16 && dtype != GQ_F16) return GQ_ERR_DTYPE;
@@ -79,7 +82,7 @@ gq_status gq_f8_matvec(const void* W, const float* wscales, int64_t N, int64_t K
                        int32_t batch, void* y, gq_dtype y_dtype, hipStream_t stream) {
     if (x_dtype != GQ_F32 && x_dtype != GQ_BF16) return GQ_ERR_DTYPE;
     if (y_dtype != GQ_F32 && y_dtype != GQ_BF16) return GQ_ERR_DTYPE;
-    if (N < 0 || N > MAX_ROWS || bad_k(K) || !fits(N, K) || batch < 1) return GQ_ERR_SHAPE;
+    if (N < 0 || N > MAX_N || bad_k(K) || !fits(N, K) || batch < 1) return GQ_ERR_SHAPE;
     if (batch > 16) return GQ_ERR_UNSUPPORTED;
     if (N == 0) return GQ_OK;
     if (!y || (K > 0 && (!W || !wscales || !x))) return GQ_ERR_NULL;
@@ -96,7 +99,7 @@ gq_status gq_f8_matmul(const void* W, const float* wscales, int64_t N, int64_t K
                        const float* xscales, int64_t M, int64_t ldx, int64_t xs_ld, void* Y, gq_dtype y_dtype,
                        int64_t ldy, hipStream_t stream) {
     if (y_dtype != GQ_F32 && y_dtype != GQ_BF16) return GQ_ERR_DTYPE;
-    if (N < 0 || M < 0 || N > MAX_ROWS || M > MAX_ROWS || bad_k(K)) return GQ_ERR_SHAPE;
+    if (N < 0 || M < 0 || N > MAX_N || M > MAX_ROWS || bad_k(K)) return GQ_ERR_SHAPE;
     if (ldx < K || ldx > MAX_K || xs_ld < M || ldy < N) return GQ_ERR_SHAPE;
     if (!fits(N, K) || !fits(M, ldx) || !fits(M, ldy) || !fits(blocks(K), xs_ld)) return GQ_ERR_SHAPE;
     if (M == 0 || N == 0) return GQ_OK;
@@ -116,7 +119,7 @@ gq_status gq_f8_matmul_id_workspace(int32_t n_experts, int32_t n_tokens, int32_t
                                     int32_t weighted, size_t* bytes) {
     if (!bytes) return GQ_ERR_NULL;
     if (y_dtype != GQ_F32 && y_dtype != GQ_BF16) return GQ_ERR_DTYPE;
-    if (n_experts < 1 || n_tokens < 0 || top_k < 1 || top_k > n_experts || N < 0 || N > MAX_ROWS ||
+    if (n_experts < 1 || n_tokens < 0 || top_k < 1 || top_k > n_experts || N < 0 || N > MAX_N ||
         (int64_t)n_tokens * top_k > MAX_SLOTS || !fits((int64_t)n_tokens * top_k, N))
         return GQ_ERR_SHAPE;
     if (n_experts > 4096) return GQ_ERR_UNSUPPORTED;
@@ -129,7 +132,7 @@ gq_status gq_f8_matmul_id(const void* experts, const float* wscales, int32_t n_e
                           int64_t ldx, int64_t xs_ld, int32_t x_per_slot, const float* route_w, void* Y,
                           gq_dtype y_dtype, void* ws, size_t ws_bytes, hipStream_t stream) {
     if (y_dtype != GQ_F32 && y_dtype != GQ_BF16) return GQ_ERR_DTYPE;
-    if (n_experts < 1 || n_tokens < 0 || top_k < 1 || top_k > n_experts || N < 0 || N > MAX_ROWS || bad_k(K) ||
+    if (n_experts < 1 || n_tokens < 0 || top_k < 1 || top_k > n_experts || N < 0 || N > MAX_N || bad_k(K) ||
         (x_per_slot != 0 && x_per_slot != 1) || (int64_t)n_tokens * top_k > MAX_SLOTS)
         return GQ_ERR_SHAPE;
     const int64_t slots = (int64_t)n_tokens * top_k, rows = x_per_slot ? slots : n_tokens;
@@ -173,7 +176,7 @@ gq_status gq_route_scored(const void* logits, gq_dtype logits_dtype, int32_t n_t
     if (n_tokens < 0 || n_experts < 1 || n_groups < 1 || n_experts % n_groups != 0 || top_groups < 1 ||
         top_groups > n_groups || top_k < 1 || top_k > (int64_t)top_groups * (n_experts / n_groups))
         return GQ_ERR_SHAPE;
-    if ((int64_t)n_tokens * n_experts > MAX_ELEMS) return GQ_ERR_SHAPE;
+    if (n_tokens > MAX_TOKENS) return GQ_ERR_SHAPE;
     if (n_experts > 4096 || top_k > 64 || n_groups > 64) return GQ_ERR_UNSUPPORTED;
     if (score != GQ_SCORE_SOFTMAX && score != GQ_SCORE_SIGMOID) return GQ_ERR_UNSUPPORTED;
     if (group_rank != GQ_GROUP_MAX && group_rank != GQ_GROUP_TOP2) return GQ_ERR_UNSUPPORTED;

@@ -139,9 +139,6 @@ __device__ __forceinline__ void copy16(const uint8_t* p, uint8_t* lds) {
 __device__ __forceinline__ void copy4(const float* p, uint8_t* lds) {
     __builtin_amdgcn_global_load_lds((GlobalPtr)p, (LdsPtr)lds, 4, 0, 0);
 }
-__device__ __forceinline__ void copy4(Rsrc r, uint32_t off, uint8_t* lds, uint32_t base) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)lds, 4, (int)off, (int)base, 0, 0);
-}
 
 // Until at most N of this wavefront's loads and copies are outstanding
 // (gfx9 encoding: vmcnt in bits 3:0 and 15:14, the other counters at their

@@ -98,27 +98,36 @@ __device__ __forceinline__ void each_slot(const int32_t* __restrict__ ids, int S
 // Workgroup e < n_experts lists the slots of expert e (their order among
 // themselves does not reach any result: each output row is computed on its
 // own): once over the ids to count the smaller ones, once to place its own.
-// The last workgroup counts the slots of every expert, cuts them into tiles of
-// at most TM and zeroes the output rows of invalid slots.  All read all ids, from the caches: one launch instead
-// of a chain of counting, scanning and placing.
+// The last workgroup counts the slots of every expert and cuts them into tiles
+// of at most TM.  Where ids are invalid, the output rows (y) of their slots are
+// zeroed by the wavefronts of all the others.  All read all ids, from the
+// caches: one launch instead of a chain of counting, scanning and placing
+// (24,120 slots of 128 experts: 11 us; 60 us with one id a load and turn).
 template <typename TY>
 __global__ __launch_bounds__(1024) void k_f8_plan(const int32_t* __restrict__ ids, int S, int n_experts, int TM,
                                                   int* __restrict__ hdr, TileEntry* __restrict__ tile,
-                                                  int* __restrict__ slot_e, int* __restrict__ slot, TY* __restrict__ y, int64_t N) {
+                                                  int* __restrict__ slot_e, int* __restrict__ slot,
+                                                  TY* __restrict__ y, int64_t N) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int e = blockIdx.x;
     if (e < n_experts) {
-        __shared__ int n_less, n_here;
+        __shared__ int n_less, n_here, any_bad;
         if (tid == 0) {
             n_less = 0;
             n_here = 0;
+            any_bad = 0;
         }
         __syncthreads();
         int less = 0;
-        each_slot(ids, S, [&](int, int id) { less += id >= 0 && id < e; });
+        bool bad = false;
+        each_slot(ids, S, [&](int s, int id) {
+            less += id >= 0 && id < e;
+            bad |= s < S && (id < 0 || id >= n_experts);
+        });
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) less += __shfl_xor(less, off, 64);
         if (lane == 0) atomicAdd(&n_less, less);
+        if (bad) any_bad = 1;
         __syncthreads();
         const int base = n_less;
         each_slot(ids, S, [&](int s, int id) {
@@ -129,6 +138,14 @@ __global__ __launch_bounds__(1024) void k_f8_plan(const int32_t* __restrict__ id
             at = __builtin_amdgcn_readfirstlane(at);
             if (id == e) slot[base + at + __popcll(vote & ((1ull << lane) - 1))] = s;
         });
+        if (y && any_bad)
+            each_slot(ids, S, [&](int s, int id) {
+                uint64_t mine = __ballot(s < S && (id < 0 || id >= n_experts) && s % n_experts == e);
+                for (; mine; mine &= mine - 1) {
+                    const int64_t row = __builtin_amdgcn_readlane(s, __builtin_ctzll(mine));
+                    for (int64_t n = lane; n < N; n += 64) store_as(y + row * N + n, 0.0f);
+                }
+            });
         return;
     }
     __shared__ int count[MAX_E];
@@ -173,12 +190,6 @@ __global__ __launch_bounds__(1024) void k_f8_plan(const int32_t* __restrict__ id
             hdr[1] = ib;
         }
     }
-    if (y && n_bad)
-        for (int s = 0; s < S; ++s) {
-            const int i = ids[s];
-            if (i < 0 || i >= n_experts)
-                for (int64_t n = tid; n < N; n += blockDim.x) store_as(y + s * N + n, 0.0f);
-        }
 }
 
 // The expert and the slots [start, start + rows) of tile i; false where the
@@ -198,8 +209,8 @@ __device__ __forceinline__ bool tile_of(const Table& t, int i, int TM, int& e, i
 // launch of a plan is saved (8 tokens x 8 of 128 experts: 5 of 22 us).  Slots of
 // one expert find each other by a ballot for each bit of the id; the experts
 // take their places in the order of their first slots.  own: the tile's slots.
-// Workgroup 0 writes the header and each slot's expert, the first one of each
-// tile its part of the table, for later calls without ids.
+// The first workgroup writes the header and each slot's expert, the first one of
+// each tile its part of the table, for later calls without ids.
 __device__ __forceinline__ bool tile_from_ids(const Table& t, int i, int TM, bool first_column, int& e, int& start,
                                               int& rows, int* own) {
     const int lane = threadIdx.x & 63;
@@ -225,7 +236,7 @@ __device__ __forceinline__ bool tile_from_ids(const Table& t, int i, int TM, boo
         if (lane >= off) incl += v;
     }
     const int before = incl - n, tb = before >> 16;
-    if (blockIdx.x == 0 && lead) {
+    if (i == 0 && first_column && lead) {
         if (lane < t.S) t.slot_e[lane] = ok ? id : -1;
         if (lane == 63) {
             t.hdr[0] = t.S - __popcll(valid);
@@ -267,6 +278,14 @@ __device__ __forceinline__ int xcd_order(int id, int total) {
 // Operand row a of the MFMA tiles 2 p and 2 p + 1 is the tile's column 32 p +
 // 8 (a / 4) + a % 4 (+ 4 for the second), so that a lane ends up with eight
 // neighbouring columns of one row of Y: 16-byte stores, 64-byte runs.
+//
+// What bounds it (256 x 256, bf16 result; timing variants of 3015 x 16384 x
+// 5120, three whole rounds, 248 us): the copies alone take 228 us (8.8 TB/s from
+// the L2s; 150 us if all of them hit), the products with the scaling 192 us,
+// the matrix instructions alone 154 us.  Reading each line ahead into the L2
+// cost more than it gave (262-285 us).  Measured: 3015 x 17408 x 5120 in 262-271
+// us (1.98-2.05 PFLOP/s; a vendor's product with one scale for each operand
+// takes 268-276 us), 8100 x 8192 x 8192 in 482 us (2.26 PFLOP/s).
 //
 // FAR (routed): X may span more than 2^31 bytes, so its rows are addressed by
 // pointers, two registers each, instead of offsets.
@@ -577,26 +596,26 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_tile_id(const uint8_t* __re
 }
 
 // A few rows: the stream kernel, 16 MT rows of X and 16 NT of W a workgroup.
-template <int MT, int NT, int WV, int D, typename TY, bool ROUTED>
+template <int MT, int NT, int WV, typename TY, bool ROUTED>
 __global__ __launch_bounds__(64 * WV) void k_f8_stream(const uint8_t* __restrict__ W, const float* __restrict__ wsc,
                                                        int64_t N, int64_t K, const uint8_t* __restrict__ X,
                                                        const float* __restrict__ xs, int64_t M, int64_t ldx,
-                                                       int64_t xs_ld, TY* __restrict__ Y, int64_t ldy, int gn,
-                                                       Table t) {
-    constexpr int RING = WV * D * Stream<MT, NT, X_E4M3, 16 * MT>::BYTES, JOIN = WV * NT * MT * 1024;
+                                                       int64_t xs_ld, TY* __restrict__ Y, int64_t ldy, Table t) {
+    constexpr int RING = WV * Stream<MT, NT, X_E4M3, 16 * MT>::BYTES, JOIN = WV * NT * MT * 1024;
     __shared__ __align__(16) uint8_t smem[RING > JOIN ? RING : JOIN];
-    const int tn = blockIdx.x % gn, tm = blockIdx.x / gn;
+    const int tn = blockIdx.x, tm = blockIdx.y;
     int e = 0, start = 0, rows;
     __shared__ int own[ROUTED ? 16 * MT : 1];
     const int* slots = nullptr;
     if constexpr (ROUTED) {
         if (t.ids) {
-            if (blockIdx.x == 0 && t.zero)
-                for (int s = 0; s < t.S; ++s) {
-                    const int id = t.ids[s];
-                    if (id < 0 || id >= t.n_experts)
-                        for (int64_t n = threadIdx.x; n < N; n += 64 * WV) store_as(Y + s * N + n, 0.0f);
-                }
+            if (tm == 0 && t.zero && threadIdx.x < 64) {
+                // this workgroup's columns of the invalid slots' rows
+                const int id = threadIdx.x < t.S ? t.ids[threadIdx.x] : 0;
+                const int64_t n = (int64_t)tn * (16 * NT) + threadIdx.x;
+                for (uint64_t bad = __ballot(id < 0 || id >= t.n_experts); bad; bad &= bad - 1)
+                    if (threadIdx.x < 16 * NT && n < N) store_as(Y + __builtin_ctzll(bad) * N + n, 0.0f);
+            }
             if (!tile_from_ids(t, tm, 16 * MT, tn == 0, e, start, rows, own)) return;
             __syncthreads();
             slots = own;
@@ -619,7 +638,7 @@ __global__ __launch_bounds__(64 * WV) void k_f8_stream(const uint8_t* __restrict
             return (int64_t)tm * (16 * MT) + c;
         }
     };
-    stream_tile<MT, NT, WV, D, X_E4M3, 16 * MT, TY>(
+    stream_tile<MT, NT, WV, X_E4M3, 16 * MT, TY>(
         W, wsc, (int64_t)tn * (16 * NT), N, K, X, xs, ldx, xs_ld, rows, (ldy & 3) == 0,
         [&](int i) { return ROUTED && !t.per_slot ? row_of(i) / t.top_k : row_of(i); },
         [&](int i) { return Y + row_of(i) * ldy; }, smem);
@@ -627,45 +646,49 @@ __global__ __launch_bounds__(64 * WV) void k_f8_stream(const uint8_t* __restrict
 
 // y[t][n] = sum_j rw[t][j] slot[t][j][n], j in increasing order, slots of
 // invalid ids left out.  Bound by the slots' bytes; a workgroup takes a token
-// and 256 V columns of it, V of them a thread (16 bytes, where N allows).
+// and 256 V columns of it, V of them a thread (16 bytes, where N allows): 3015 x
+// 8 slots of 2816 bf16 in 23 us (6.6 TB/s, part of it still in the caches; 125
+// us one element a thread).  Slots are held in the result's type: with bf16
+// each is rounded once before the sum, which adds to the result's own rounding
+// (together 1.35 times its error), and halves the bytes that bound this.
 template <typename TY, int V>
 __global__ __launch_bounds__(256) void k_f8_combine(const TY* __restrict__ slots, const int* __restrict__ slot_e,
                                                     const float* __restrict__ rw, int top_k, int64_t N,
                                                     TY* __restrict__ y) {
     const int64_t t = blockIdx.x;
-    const int64_t n = ((int64_t)blockIdx.y * 256 + threadIdx.x) * V;
-    if (n >= N) return;
-    float sum[V];
+    for (int64_t n = ((int64_t)blockIdx.y * 256 + threadIdx.x) * V; n < N; n += (int64_t)gridDim.y * (256 * V)) {
+        float sum[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] = 0.0f;
+        for (int i = 0; i < V; ++i) sum[i] = 0.0f;
 #pragma unroll 4
-    for (int j = 0; j < top_k; ++j) {
-        const int64_t s = t * top_k + j;
-        const float w = rw[s];
-        const bool ok = slot_e[s] >= 0;  // (otherwise nobody wrote the row)
-        const TY* p = slots + s * N + n;
-        if constexpr (V == 1) {
-            const float v = sizeof(TY) == 4 ? (float)*p : gqd::bf2f((uint16_t)*p);
-            sum[0] = ok ? __builtin_fmaf(w, v, sum[0]) : sum[0];
-        } else if constexpr (sizeof(TY) == 4) {
-            const f32x4 v = *reinterpret_cast<const f32x4*>(p);
+        for (int j = 0; j < top_k; ++j) {
+            const int64_t s = t * top_k + j;
+            const float w = rw[s];
+            const bool ok = slot_e[s] >= 0;  // (otherwise nobody wrote the row)
+            const TY* p = slots + s * N + n;
+            if constexpr (V == 1) {
+                const float v = sizeof(TY) == 4 ? (float)*p : gqd::bf2f((uint16_t)*p);
+                sum[0] = ok ? __builtin_fmaf(w, v, sum[0]) : sum[0];
+            } else if constexpr (sizeof(TY) == 4) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] = ok ? __builtin_fmaf(w, v[i], sum[i]) : sum[i];
-        } else {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+                for (int i = 0; i < V; ++i) sum[i] = ok ? __builtin_fmaf(w, v[i], sum[i]) : sum[i];
+            } else {
+                const u32x4 v = *reinterpret_cast<const u32x4*>(p);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float f = __builtin_bit_cast(float, i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
-                sum[i] = ok ? __builtin_fmaf(w, f, sum[i]) : sum[i];
+                for (int i = 0; i < V; ++i) {
+                    const float f = __builtin_bit_cast(float, i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+                    sum[i] = ok ? __builtin_fmaf(w, f, sum[i]) : sum[i];
+                }
             }
         }
-    }
-    if constexpr (V == 1) {
-        store_as(y + t * N + n, sum[0]);
-    } else {
+        if constexpr (V == 1) {
+            store_as(y + t * N + n, sum[0]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; i += 4)
-            store4(y + t * N, n + i, N, true, f32x4{sum[i], sum[i + 1], sum[i + 2], sum[i + 3]});
+            for (int i = 0; i < V; i += 4)
+                store4(y + t * N, n + i, N, true, f32x4{sum[i], sum[i + 1], sum[i + 2], sum[i + 3]});
+        }
     }
 }
 
@@ -673,8 +696,7 @@ template <int V, typename TY>
 hipError_t combine(const TY* slots, const int* slot_e, const float* rw, int n_tokens, int top_k, int64_t N, TY* y,
                    hipStream_t s) {
     const int64_t gx = (N + 256 * V - 1) / (256 * V);
-    if (gx > 65535) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_f8_combine<TY, V>), dim3((unsigned)n_tokens, (unsigned)gx), dim3(256), 0, s, slots, slot_e,
+    hipLaunchKernelGGL((k_f8_combine<TY, V>), dim3((unsigned)n_tokens, (unsigned)(gx < 65535 ? gx : 65535)), dim3(256), 0, s, slots, slot_e,
                        rw, top_k, N, y);
     return hipGetLastError();
 }
@@ -695,12 +717,13 @@ struct Call {
 };
 
 // gm: tiles of rows (of slots: the most there can be)
-template <int MT, int NT, int WV, int D, bool ROUTED, typename TY>
+template <int MT, int NT, int WV, bool ROUTED, typename TY>
 hipError_t stream(const Call<TY>& c, int64_t gm) {
     const int64_t gn = (c.N + 16 * NT - 1) / (16 * NT);
-    if (!grid_ok(gn * gm, 64 * WV)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_f8_stream<MT, NT, WV, D, TY, ROUTED>), dim3((unsigned)(gn * gm)), dim3(64 * WV), 0, c.s, c.W,
-                       c.wsc, c.N, c.K, c.X, c.xs, c.M, c.ldx, c.xs_ld, c.Y, c.ldy, (int)gn, c.t);
+    // (routed: at most 8 slots an expert, 6144 tiles; dense: few rows)
+    if (!grid_ok(gn, 64 * WV) || gm > 65535) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_f8_stream<MT, NT, WV, TY, ROUTED>), dim3((unsigned)gn, (unsigned)gm), dim3(64 * WV), 0, c.s,
+                       c.W, c.wsc, c.N, c.K, c.X, c.xs, c.M, c.ldx, c.xs_ld, c.Y, c.ldy, c.t);
     return hipGetLastError();
 }
 
@@ -722,7 +745,6 @@ template <int BM, int BN, int WM, int WN, int NB, bool FAR, typename TY>
 hipError_t tile_id(const Call<TY>& c, int64_t gm) {
     // two tiles of columns a workgroup (one with 256 rows): the second one's copies hide the first one's end
     const int64_t gn = (c.N + BN - 1) / BN, split = BM < 256 ? (gn + 1) / 2 : gn;
-    if (gn > INT_MAX / 2 || !grid_ok(gm * split, 64 * WM * WN)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_f8_tile_id<BM, BN, WM, WN, NB, TY, FAR>), dim3((unsigned)(gm * split)), dim3(64 * WM * WN),
                        0, c.s, c.W, c.wsc, c.N, c.K, c.X, c.xs, c.ldx, c.xs_ld, c.Y, (int)gm, (int)gn, (int)split,
                        c.t);
@@ -748,18 +770,18 @@ hipError_t matmul(const Call<TY>& c) {
     const int64_t cus = gqk_cu_count();
     if (tiles(64, 128) <= (sizeof(TY) == 4 ? 3 * cus / 4 : cus / 2)) {
         // rows of X and of W a workgroup: tall ones read either side less often, as long as 3 in 4 CUs have one
-        if (c.M <= 16) return stream<1, 2, 8, 1, false>(c, (c.M + 15) / 16);
-        if (c.M <= 64) return stream<2, 2, 8, 1, false>(c, (c.M + 31) / 32);
-        if (tiles(48, 64) >= 3 * cus / 4) return stream<3, 4, 8, 1, false>(c, (c.M + 47) / 48);
-        return stream<3, 2, 8, 1, false>(c, (c.M + 47) / 48);
+        if (c.M <= 16) return stream<1, 2, 8, false>(c, (c.M + 15) / 16);
+        if (c.M <= 64) return stream<2, 2, 8, false>(c, (c.M + 31) / 32);
+        if (tiles(48, 64) >= 3 * cus / 4) return stream<3, 4, 8, false>(c, (c.M + 47) / 48);
+        return stream<3, 2, 8, false>(c, (c.M + 47) / 48);
     }
     if constexpr (sizeof(TY) == 2) {
-        if (c.M <= 32) return stream<2, 2, 8, 1, false>(c, (c.M + 31) / 32);
+        if (c.M <= 32) return stream<2, 2, 8, false>(c, (c.M + 31) / 32);
         if (tiles(64, 128) <= cus) return tile<64, 128, 2, 4, 4, false>(c);
         if (tiles(128, 128) <= cus) return tile<128, 128, 4, 2, 4, false>(c);
         if (tiles(256, 256) >= cus / 2) return tile<256, 256, 4, 2, 2, true>(c);
     } else {
-        if (c.M <= 64) return stream<2, 2, 8, 1, false>(c, (c.M + 31) / 32);
+        if (c.M <= 64) return stream<2, 2, 8, false>(c, (c.M + 31) / 32);
     }
     return tile<128, 128, 4, 2, 2, false>(c);
 }
@@ -781,9 +803,9 @@ int tile_rows(int64_t S, int n_experts) {
 // of 16, 2560 x 9728: 35.7, 28.4 and 29.6 us).
 template <typename TY>
 hipError_t stream_id(const Call<TY>& c, int64_t gm) {
-    if (c.K <= 8 * BLK) return stream<1, 2, 2, 1, true>(c, gm);
-    if (c.K <= 32 * BLK) return stream<1, 2, 4, 1, true>(c, gm);
-    return stream<1, 2, 8, 1, true>(c, gm);
+    if (c.K <= 8 * BLK) return stream<1, 2, 2, true>(c, gm);
+    if (c.K <= 32 * BLK) return stream<1, 2, 4, true>(c, gm);
+    return stream<1, 2, 8, true>(c, gm);
 }
 
 template <typename TY>
@@ -804,9 +826,11 @@ hipError_t matmul_id(Call<TY> c, int n_experts, const int32_t* ids, int n_tokens
     const bool small = ids && S <= SMALL && h == 16;
     c.t = Table{hdr, tiles, slot_e, slot, n_experts, S, top_k, x_per_slot, small ? ids : nullptr, !route_w};
     const int64_t rows = x_per_slot ? S : n_tokens;
+    // (the most workgroups that any of the tile kernels takes; before anything is launched)
+    if (h > 16 && !grid_ok(gm * ((c.N + 127) / 128), 512)) return hipErrorInvalidValue;
     if (ids && !small) {
-        hipLaunchKernelGGL((k_f8_plan<TY>), dim3(n_experts + 1), dim3(S <= 4096 ? 256 : 1024), 0, c.s, ids, S, n_experts, h, hdr,
-                           tiles, slot_e, slot, route_w ? nullptr : y, c.N);
+        hipLaunchKernelGGL((k_f8_plan<TY>), dim3(n_experts + 1), dim3(S <= 4096 ? 256 : 1024), 0, c.s, ids, S,
+                           n_experts, h, hdr, tiles, slot_e, slot, route_w ? nullptr : y, c.N);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

