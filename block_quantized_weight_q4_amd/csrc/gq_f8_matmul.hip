@@ -295,7 +295,8 @@ struct Tile {
     static constexpr int XI = BM / 8 / WV, WI = BN / 8 / WV;  // copies of a wavefront and block
     static constexpr int SX = (BM + BN) * BLK, STAGE = SX + WV * 256;
     static constexpr int LOADS = XI + WI + 1;
-    static constexpr bool MANY = ROUTED && BM < 256;  // (with the 256 x 256 tile's registers the longer loop does not fit)
+    // (with the 256 x 256 tile's registers the longer loop does not fit)
+    static constexpr bool MANY = ROUTED && BM < 256;
     static_assert(BM % (8 * WV) == 0 && BN % (8 * WV) == 0 && WV > BM / 64 && BN / WN <= BLK, "tile shape");
 
     // swizzle of W's rows: (r / 2 % 2, r / 8 % 4), the rows of one operand read
@@ -365,7 +366,8 @@ struct Tile {
             const int k = ck * BLK;
             const int left = (int)K - k, wleft = cn < n_end ? left : 0;  // (W past the last tile: zeros)
             const uint32_t wo = within(woff, (int)wchunk, wleft);
-            const int xk = k + ((int)xchunk < left ? (int)xchunk : -k);  // (FAR: past K the row's first chunk, times zeros)
+            // (FAR: past K the row's first chunk, times zeros)
+            const int xk = k + ((int)xchunk < left ? (int)xchunk : -k);
             const Rsrc wr = make_rsrc(W + cn * K, cn < N ? (N - cn < BN ? N - cn : BN) * K : 0);
 #pragma unroll
             for (int u = 0; u < XI; ++u) {
@@ -595,6 +597,135 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_tile_id(const uint8_t* __re
     T::run(W, wsc, N, K, X, xs, ldx, xs_ld, Y, N, 0, (int64_t)first * BN, rows, start, end - first, t, smem);
 }
 
+// Routed, bf16 results, short rows (at most KB <= 6 blocks of 128): a wavefront
+// keeps its 32 rows of X in registers, for all of K, and only W goes through LDS,
+// in panels of 32 columns and all of K.  Beside half the copies, a panel is one
+// piece of memory, read in whole lines (blocks of 128 inputs of rows of 704 bytes
+// are not).  The panels are copied two ahead; a row of one is CHP = 8 KB + 1
+// chunks of 16 bytes, odd, so that 16 rows at one chunk cover all banks, and its
+// rows lie in the order of the operands (see Tile: a lane ends up with eight
+// neighbouring columns).  A panel's results are stored behind the next barrier,
+// ahead of the next copies, so that no wait is for a store just made.
+// 3015 x 8 slots of 128 experts, 2816 x 704: 115 us (128 x 128 tiles: 148 us); of
+// that the copies alone 68, the stores 23, products and stores without copies 86.
+constexpr int PANELS = 3;
+
+template <int KB, int WV>
+__global__ __launch_bounds__(64 * WV, 2) void k_f8_short_id(const uint8_t* __restrict__ W,
+                                                            const float* __restrict__ wsc, int64_t N, int64_t K,
+                                                            const uint8_t* __restrict__ X,
+                                                            const float* __restrict__ xs, int64_t ldx, int64_t xs_ld,
+                                                            uint16_t* __restrict__ Y, int gm, int gn, int split,
+                                                            Table t) {
+    // copies of a panel, and of a wavefront; those past the panel's go to the last KB of LDS
+    constexpr int CHP = 8 * KB + 1, NI = (32 * CHP + 63) / 64, CI = (NI + WV - 1) / WV;
+    __shared__ __align__(16) uint8_t smem[(PANELS * NI + 1) * 1024];
+    const int tiles = t.hdr[1], real = (tiles < gm ? tiles : gm) * split;
+    if ((int)blockIdx.x >= real) return;
+    const int id = xcd_order(blockIdx.x, real), tm = id / split, part = id % split;
+    const int first = (int)((int64_t)gn * part / split), end = (int)((int64_t)gn * (part + 1) / split);
+    int e, start, rows;
+    if (!tile_of(t, tm, 32 * WV, e, start, rows)) return;
+    const int kbs = (int)((K + BLK - 1) / BLK);
+    W += (int64_t)e * N * K;
+    wsc += (int64_t)e * ((N + BLK - 1) / BLK) * kbs;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int fr = lane & 15, fq = lane >> 4, wm = 32 * wave;
+    auto slot_of = [&](int i) -> int64_t {
+        const unsigned s = (unsigned)t.slot[start + (i < rows ? i : rows - 1)];
+        return s < (unsigned)t.S ? (int64_t)s : t.S - 1;
+    };
+
+    // copies: position 64 (wave + WV u) + lane of a panel is chunk c of its row r
+    uint32_t off[CI];
+#pragma unroll
+    for (int u = 0; u < CI; ++u) {
+        const int p = 64 * (wave + WV * u) + lane, r = p / CHP, c = p - r * CHP;
+        const int row = 8 * ((r & 15) >> 2) + 4 * (r >> 4) + (r & 3);
+        off[u] = r < 32 && 16 * c < K ? (uint32_t)(row * K + 16 * c) : NOWHERE;
+    }
+    auto load = [&](int panel, int buf) {
+        const int64_t n = (int64_t)panel * 32;
+        const Rsrc r = make_rsrc(W + n * K, panel < end ? (N - n < 32 ? N - n : 32) * K : 0);
+#pragma unroll
+        for (int u = 0; u < CI; ++u) {
+            const int i = wave + WV * u;
+            copy16(r, off[u], smem + 1024 * (i < NI ? buf * NI + i : PANELS * NI));
+        }
+    };
+    load(first, 0);
+    load(first + 1, 1);
+
+    int64_t x_row[2];
+    uint16_t* y_row[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int64_t s = slot_of(wm + 16 * j + fr);
+        x_row[j] = t.per_slot ? s : s / t.top_k;
+        y_row[j] = Y + s * N;
+    }
+    const Rsrc xr = make_rsrc(X, (t.per_slot ? t.S : t.S / t.top_k) * ldx);
+    i32x8 x[KB][2];
+    float sx[KB][2], f[KB][2];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int k = kb * BLK + 16 * fq;
+            const uint32_t o = (uint32_t)(x_row[j] * ldx) + k;
+            x[kb][j] = join(bld16(xr, within(o, k, (int)K)), bld16(xr, within(o + 64, k + 64, (int)K)));
+            sx[kb][j] = kb < kbs ? xs[kb * xs_ld + x_row[j]] : 0.0f;
+        }
+    const bool idle = wm >= rows, vec = (N & 7) == 0;  // (idle: none of this wavefront's rows is used)
+    const int at0 = fr * CHP + fq, at1 = at0 + 16 * CHP;
+    f32x4 acc[2][2];
+    auto store = [&](int panel) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (wm + 16 * j + fr < rows) store8(y_row[j], (int64_t)panel * 32 + 8 * fq, N, vec, acc[0][j], acc[1][j]);
+    };
+    int buf = 0;
+    for (int p = first; p < end; ++p) {
+        wait_copies<CI>();
+        gqd::lds_barrier();
+        if (p > first) store(p - 1);
+        load(p + 2, buf == 0 ? 2 : buf - 1);
+        if (!idle) {
+            if (p == first || (p & 3) == 0) {
+                const float* s = wsc + (int64_t)(p >> 2) * kbs;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    const float w = s[kb < kbs ? kb : 0];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) f[kb][j] = w * sx[kb][j];
+                }
+            }
+            const u32x4* d = reinterpret_cast<const u32x4*>(smem + buf * (NI * 1024));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const i32x8 a[2] = {join(d[at0 + 8 * kb], d[at0 + 8 * kb + 4]),
+                                    join(d[at1 + 8 * kb], d[at1 + 8 * kb + 4])};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const f32x4 q = mfma8(a[i], x[kb][j]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(q[r], f[kb][j], acc[i][j][r]);
+                    }
+            }
+        }
+        buf = buf == 2 ? 0 : buf + 1;
+    }
+    if (end > first) store(end - 1);
+    wait_copies<0>();
+}
+
 // A few rows: the stream kernel, 16 MT rows of X and 16 NT of W a workgroup.
 template <int MT, int NT, int WV, typename TY, bool ROUTED>
 __global__ __launch_bounds__(64 * WV) void k_f8_stream(const uint8_t* __restrict__ W, const float* __restrict__ wsc,
@@ -696,8 +827,8 @@ template <int V, typename TY>
 hipError_t combine(const TY* slots, const int* slot_e, const float* rw, int n_tokens, int top_k, int64_t N, TY* y,
                    hipStream_t s) {
     const int64_t gx = (N + 256 * V - 1) / (256 * V);
-    hipLaunchKernelGGL((k_f8_combine<TY, V>), dim3((unsigned)n_tokens, (unsigned)(gx < 65535 ? gx : 65535)), dim3(256), 0, s, slots, slot_e,
-                       rw, top_k, N, y);
+    const dim3 grid((unsigned)n_tokens, (unsigned)(gx < 65535 ? gx : 65535));
+    hipLaunchKernelGGL((k_f8_combine<TY, V>), grid, dim3(256), 0, s, slots, slot_e, rw, top_k, N, y);
     return hipGetLastError();
 }
 
@@ -750,6 +881,30 @@ hipError_t tile_id(const Call<TY>& c, int64_t gm) {
                        c.t);
     return hipGetLastError();
 }
+
+// n_tiles: the tiles that are likely.  About 4 workgroups of four wavefronts a CU
+// (two run at once), or one of eight; each loads its rows of X first, which pays
+// from 3 panels on (2816 x 704, 188 slots for each of 128 experts: 149, 150 and
+// 155 us with 1000, 2000 and 500 workgroups; 2816 x 768, 754 for each of 16: 61
+// and 67 us with 200 and 400 of eight).
+template <int KB, int WV>
+hipError_t short_id(const Call<uint16_t>& c, int64_t gm, int64_t n_tiles) {
+    const int64_t gn = (c.N + 31) / 32, groups = gqk_cu_count() * (WV == 4 ? 4 : 1);
+    const int64_t want = groups > n_tiles ? groups / n_tiles : 1, most = (gn + 2) / 3;
+    const int64_t split = want < most ? want : most;
+    hipLaunchKernelGGL((k_f8_short_id<KB, WV>), dim3((unsigned)(gm * split)), dim3(64 * WV), 0, c.s, c.W, c.wsc, c.N,
+                       c.K, c.X, c.xs, c.ldx, c.xs_ld, c.Y, (int)gm, (int)gn, (int)split, c.t);
+    return hipGetLastError();
+}
+
+// (K padded to 2, 4 or 6 blocks: constants, so that the operands are read ahead)
+template <int WV>
+hipError_t short_id(const Call<uint16_t>& c, int64_t gm, int64_t n_tiles) {
+    if (c.K > 4 * BLK) return short_id<6, WV>(c, gm, n_tiles);
+    if (c.K > 2 * BLK) return short_id<4, WV>(c, gm, n_tiles);
+    return short_id<2, WV>(c, gm, n_tiles);
+}
+
 
 // Which kernel: measured at N x K of 1024 x 2560, 5120 x 5120, 2560 x 9728 and
 // 17408 x 5120, 16 to 2048 rows.  What decides is how many tiles there are for
@@ -808,6 +963,22 @@ hipError_t stream_id(const Call<TY>& c, int64_t gm) {
     return stream<1, 2, 8, true>(c, gm);
 }
 
+// Many slots an expert: tiles of h = 128 or 256 slots.  Short rows: from 3 in 4
+// down to 9 in 10 of the tile kernels' time (500 tokens x 2 of 8 experts, 400 x
+// 400: 12.1 against 18.7 us; 3015 x 4 of 16, 2816 x 768: 61.4 against 68.6 us).
+hipError_t many_id(const Call<uint16_t>& c, int64_t gm, int h, int n_experts) {
+    if (c.K > 0 && c.K <= 6 * BLK) {
+        const int64_t n_tiles = (c.M + h - 1) / h + n_experts / 2;  // (an expert's last is half full)
+        return h == 128 ? short_id<4>(c, gm, n_tiles) : short_id<8>(c, gm, n_tiles);
+    }
+    if (h == 128) return tile_id<128, 128, 2, 2, 2, false>(c, gm);
+    return tile_id<256, 256, 4, 2, 2, false>(c, gm);
+}
+hipError_t many_id(const Call<float>& c, int64_t gm, int h, int) {
+    if (h == 128) return tile_id<128, 128, 2, 2, 2, false>(c, gm);
+    return tile_id<256, 128, 4, 2, 2, false>(c, gm);
+}
+
 template <typename TY>
 hipError_t matmul_id(Call<TY> c, int n_experts, const int32_t* ids, int n_tokens, int top_k, int x_per_slot,
                      const float* route_w, int y_dtype, void* ws) {
@@ -838,9 +1009,7 @@ hipError_t matmul_id(Call<TY> c, int n_experts, const int32_t* ids, int n_tokens
     if (h == 16) e = stream_id(c, gm);
     else if (rows * c.ldx >= INT_MAX) e = tile_id<256, 128, 4, 2, 2, true>(c, gm);
     else if (h == 64) e = tile_id<64, 128, 1, 4, 2, false>(c, gm);
-    else if (h == 128) e = tile_id<128, 128, 2, 2, 2, false>(c, gm);
-    else if constexpr (sizeof(TY) == 2) e = tile_id<256, 256, 4, 2, 2, false>(c, gm);
-    else e = tile_id<256, 128, 4, 2, 2, false>(c, gm);
+    else e = many_id(c, gm, h, n_experts);
     if (e != hipSuccess || !route_w) return e;
     constexpr int V = 16 / sizeof(TY);
     if (c.N % V == 0) return combine<V>(c.Y, slot_e, route_w, n_tokens, top_k, c.N, y, c.s);

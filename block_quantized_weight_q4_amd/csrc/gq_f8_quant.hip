@@ -11,9 +11,9 @@
 // Bound by HBM: each input is read once and each byte written once; 3015 x 5120
 // bf16 take 9.3 us (5.0 TB/s, a 1 GiB copy reaches 5.1), the gated unit of 3015
 // x 17408 55.9 us (4.7 TB/s; 60.9 us with expf, tanhf and a division, when the
-// vector unit took as long as the memory).  Eight lanes share a group: each holds 16 inputs (two or four 16-byte loads, one
-// 16-byte store) and three DPP / xor steps give the group's maximum.  The
-// maximum is taken over the magnitudes' bit patterns, where infinities and
+// vector unit took as long as the memory).  Eight lanes share a group: each holds
+// 16 inputs (two or four 16-byte loads, one 16-byte store) and three DPP / xor
+// steps give the group's maximum.  The maximum is taken over the magnitudes' bit patterns, where infinities and
 // NaNs sort above every number and so cannot be lost.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

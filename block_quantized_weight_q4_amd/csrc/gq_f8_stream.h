@@ -31,6 +31,11 @@ enum { X_E4M3 = 0, X_BF16 = 1, X_F32 = 2 };
 __device__ __forceinline__ int pos128(int r, int c) { return r * 8 + (c ^ ((r >> 1) & 7)); }
 __device__ __forceinline__ int pos_wide(int r, int c, int chunks) { return r * chunks + (c ^ (r & 15)); }
 
+// What an fp32 value's upper 16 bits leave of it.
+__device__ __forceinline__ uint32_t minus_upper(uint32_t u) {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u) - __builtin_bit_cast(float, u & 0xffff0000u));
+}
+
 // Eight fp32 values as three bf16 operands whose sum they are: the upper 16
 // bits, those of what is left, and the rest (8 + 8 + 8 bits of the mantissa:
 // exact while the last is a normal number).
@@ -42,8 +47,8 @@ __device__ __forceinline__ void split8(const u32x4& p, const u32x4& q, bf16x8 (&
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
             part[c][i] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);  // the upper halves of both
-            u0 = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u0) - __builtin_bit_cast(float, u0 & 0xffff0000u));
-            u1 = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u1) - __builtin_bit_cast(float, u1 & 0xffff0000u));
+            u0 = minus_upper(u0);
+            u1 = minus_upper(u1);
         }
     }
 #pragma unroll

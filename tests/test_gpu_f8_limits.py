@@ -66,6 +66,29 @@ def test_table_of_few_slots_reused(gq):
         assert torch.equal(got.view(torch.int32), want.view(torch.int32))
 
 
+@pytest.mark.parametrize("per_slot", [False, True])
+@pytest.mark.parametrize("E,T,k,N,K", [(3, 200, 1, 33, 16), (4, 130, 2, 257, 128), (2, 330, 2, 700, 272),
+                                       (5, 210, 2, 95, 512), (2, 1000, 1, 130, 640), (3, 700, 2, 416, 768),
+                                       (3, 200, 1, 64, 784), (1, 500, 1, 31, 96), (9, 300, 3, 200, 704)])
+def test_short_rows_of_many_slots(gq, E, T, k, N, K, per_slot):
+    """Rows on both sides of what a wavefront keeps in registers, columns that end inside a panel, experts with few
+    slots beside full ones."""
+    r = Routed(E, T, k, N, K, per_slot, "bf16", skew=0.5)
+    r.ids[T // 2] = -1
+    for weighted in (False, True):
+        Y, ws = r.check(gq, weighted)
+        again, _ = r.call(gq, weighted, ids=(T, k), ws=ws, Y=Y.clone())
+        assert torch.equal(again.view(torch.int16), Y.view(torch.int16))
+
+
+def test_a_nan_weight_reaches_its_column_only(gq):
+    """Short rows that end inside a block of 128: what is padded is not multiplied by a neighbour's NaN."""
+    r = Routed(1, 300, 1, 100, 144, False, "bf16")
+    r.q[0, 41, :] = 0x7F
+    Y, _ = r.call(gq, False)
+    assert torch.isnan(Y[..., 41]).all() and torch.isfinite(Y[..., :41]).all() and torch.isfinite(Y[..., 42:]).all()
+
+
 def wide(N, K):
     g = torch.Generator(device="cuda").manual_seed(N)
     W = torch.randint(0, 0x7F, (N, K), dtype=torch.uint8, device="cuda", generator=g)
