@@ -446,15 +446,11 @@ def _raw_stream(index: int) -> int:
 
 # the same handle without building a Stream object, where torch offers it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _f8_blocks(n: int) -> int:
     return (n + 127) // 128
-
-
-def _ld(t: torch.Tensor) -> int:
-    """Elements from one row to the next (of a single row: its length)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _f8_rows(name: str, t: torch.Tensor) -> None:
@@ -475,7 +471,7 @@ def _launch(fn: str, f, index: int, stream, *args) -> None:
     else:
         _need(stream.device.index == index, "stream belongs to %s, the tensors to cuda:%d" % (stream.device, index))
         s = stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = f(*args, s)
     else:
         with torch.cuda.device(index):
@@ -519,17 +515,18 @@ def gq_f8_quant(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, pow2: bo
     """q, scales of x [M][K] (fp32 / bf16 / fp16): e4m3 bytes [M][K] and one
     fp32 scale for 128 inputs of a row, [ceil(K / 128)][M]."""
     try:
-        (M, K), d = x.shape, x.get_device()
+        (M, K), d, G = x.shape, x.get_device(), scales.shape[0]
+        (ldx, x1), (ldq, q1), (s_ld, s1) = x.stride(), q.stride(), scales.stride()
         ok = (d >= 0 and d == q.get_device() == scales.get_device() and x.dtype in _HALF_OR_F32 and
               q.dtype in _F8 and scales.dtype is _f32 and q.shape == (M, K) and
-              scales.shape == ((K + 127) // 128, M) and x.stride(1) == q.stride(1) == 1 and
-              (scales.stride(1) == 1 or M == 1))
+              scales.shape == ((K + 127) // 128, M) and x1 == q1 == 1 and (s1 == 1 or M == 1))
     except (AttributeError, ValueError):
         ok = False
     if not ok:
         _check_quant(x, q, scales)
-    _launch("gq_f8_quant", _lib.gq_f8_quant, d, stream, x.data_ptr(), _DTYPES[x.dtype], M, K, _ld(x), pow2,
-            q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales))
+    one = M <= 1  # (a single row's stride says nothing)
+    _launch("gq_f8_quant", _lib.gq_f8_quant, d, stream, x.data_ptr(), _DTYPES[x.dtype], M, K, K if one else ldx, pow2,
+            q.data_ptr(), K if one else ldq, scales.data_ptr(), s_ld if G > 1 else M)
     return q, scales
 
 
@@ -537,19 +534,22 @@ def gq_f8_glu_quant(g: torch.Tensor, u: torch.Tensor, act: str, q: torch.Tensor,
                     pow2: bool = False, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """gq_f8_quant of act(g) * u; g, u [M][K] of one type (fp32 / bf16 / fp16)."""
     try:
-        (M, K), d = g.shape, g.get_device()
+        (M, K), d, G = g.shape, g.get_device(), scales.shape[0]
+        (ldg, g1), (ldu, u1), (ldq, q1), (s_ld, s1) = g.stride(), u.stride(), q.stride(), scales.stride()
         ok = (d >= 0 and d == u.get_device() == q.get_device() == scales.get_device() and
               g.dtype in _HALF_OR_F32 and u.dtype is g.dtype and q.dtype in _F8 and scales.dtype is _f32 and
               u.shape == q.shape == (M, K) and scales.shape == ((K + 127) // 128, M) and act in ACTS and
-              g.stride(1) == u.stride(1) == q.stride(1) == 1 and (scales.stride(1) == 1 or M == 1))
+              g1 == u1 == q1 == 1 and (s1 == 1 or M == 1))
     except (AttributeError, ValueError):
         ok = False
     if not ok:
         _need(act in ACTS, "act must be one of %s" % sorted(ACTS))
         _tensor("u", u, _HALF_OR_F32)
         _check_quant(g, q, scales, u=u)
+    one = M <= 1
     _launch("gq_f8_glu_quant", _lib.gq_f8_glu_quant, d, stream, g.data_ptr(), u.data_ptr(), _DTYPES[g.dtype], M, K,
-            _ld(g), _ld(u), ACTS[act], pow2, q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales))
+            K if one else ldg, K if one else ldu, ACTS[act], pow2, q.data_ptr(), K if one else ldq, scales.data_ptr(),
+            s_ld if G > 1 else M)
     return q, scales
 
 
@@ -617,20 +617,23 @@ def gq_f8_matmul(W: torch.Tensor, wscales: torch.Tensor, X: torch.Tensor, xscale
     """Y [M][N] (fp32 / bf16) = X [M][K] e4m3 with xscales [ceil(K / 128)][M]
     times the weights W [N][K] with wscales [ceil(N / 128)][ceil(K / 128)]."""
     try:
-        (N, K), d, M = W.shape, W.get_device(), X.shape[0]
+        (N, K), d, M, G = W.shape, W.get_device(), X.shape[0], xscales.shape[0]
+        (ldx, x1), (xs_ld, s1), (ldy, y1) = X.stride(), xscales.stride(), Y.stride()
         ok = (d >= 0 and
               d == wscales.get_device() == X.get_device() == xscales.get_device() == Y.get_device() and
               W.dtype in _F8 and X.dtype in _F8 and wscales.dtype is _f32 and xscales.dtype is _f32 and
               Y.dtype in _ACT and wscales.shape == ((N + 127) // 128, (K + 127) // 128) and X.shape == (M, K) and
               xscales.shape == ((K + 127) // 128, M) and Y.shape == (M, N) and
               W.is_contiguous() and wscales.is_contiguous() and
-              X.stride(1) == Y.stride(1) == 1 and (xscales.stride(1) == 1 or M == 1))
+              x1 == y1 == 1 and (s1 == 1 or M == 1))
     except (AttributeError, ValueError, IndexError):
         ok = False
     if not ok:
         _check_matmul(W, wscales, X, xscales, Y)
+    one = M <= 1
     _launch("gq_f8_matmul", _lib.gq_f8_matmul, d, stream, W.data_ptr(), wscales.data_ptr(), N, K, X.data_ptr(),
-            xscales.data_ptr(), M, _ld(X), _ld(xscales), Y.data_ptr(), _DTYPES[Y.dtype], _ld(Y))
+            xscales.data_ptr(), M, K if one else ldx, xs_ld if G > 1 else M, Y.data_ptr(), _DTYPES[Y.dtype],
+            N if one else ldy)
     return Y
 
 
@@ -675,8 +678,9 @@ def gq_f8_matmul_id(W: torch.Tensor, wscales: torch.Tensor, ids, X: torch.Tensor
     (n_tokens, top_k) tuple: the table already in ws is used."""
     reuse = isinstance(ids, tuple)
     try:
-        (n_experts, N, K), d, rows = W.shape, W.get_device(), X.shape[0]
+        (n_experts, N, K), d, rows, G = W.shape, W.get_device(), X.shape[0], xscales.shape[0]
         n_tokens, top_k = ids if reuse else ids.shape
+        (ldx, x1), (xs_ld, s1) = X.stride(), xscales.stride()
         ok = (d >= 0 and d == wscales.get_device() == X.get_device() == xscales.get_device() ==
               Y.get_device() == ws.get_device() and W.dtype in _F8 and X.dtype in _F8 and wscales.dtype is _f32 and
               xscales.dtype is _f32 and Y.dtype in _ACT and ws.dtype is _u8 and
@@ -686,15 +690,15 @@ def gq_f8_matmul_id(W: torch.Tensor, wscales: torch.Tensor, ids, X: torch.Tensor
               (Y.shape == (n_tokens, top_k, N) if route_w is None else
                Y.shape == (n_tokens, N) and route_w.shape == (n_tokens, top_k) and route_w.dtype is _f32 and
                route_w.get_device() == d and route_w.is_contiguous()) and
-              X.stride(1) == 1 and (xscales.stride(1) == 1 or rows == 1) and W.is_contiguous() and wscales.is_contiguous() and
+              x1 == 1 and (s1 == 1 or rows == 1) and W.is_contiguous() and wscales.is_contiguous() and
               Y.is_contiguous() and ws.is_contiguous())
     except (AttributeError, ValueError, IndexError):
         ok = False
     if not ok:
         _check_matmul_id(W, wscales, ids, X, xscales, Y, ws, route_w)
     _launch("gq_f8_matmul_id", _lib.gq_f8_matmul_id, d, stream, W.data_ptr(), wscales.data_ptr(), n_experts, N, K,
-            None if reuse else ids.data_ptr(), n_tokens, top_k, X.data_ptr(), xscales.data_ptr(), _ld(X),
-            _ld(xscales), rows != n_tokens, None if route_w is None else route_w.data_ptr(), Y.data_ptr(),
+            None if reuse else ids.data_ptr(), n_tokens, top_k, X.data_ptr(), xscales.data_ptr(),
+            K if rows <= 1 else ldx, xs_ld if G > 1 else rows, rows != n_tokens, None if route_w is None else route_w.data_ptr(), Y.data_ptr(),
             _DTYPES[Y.dtype], ws.data_ptr(), ws.numel())
     return Y
 
