@@ -13,15 +13,17 @@
 // One wavefront per token.  Lane l holds the experts l NI .. l NI + NI - 1
 // (blocked, so that the lowest lane that holds the largest value also holds
 // the lowest expert id among equals) as order-preserving 64-bit images of c;
-// a wave maximum by DPP moves, a ballot and a readlane find each place.
+// a wave maximum of the images' upper halves by DPP, a ballot and a readlane find
+// each place, the lower halves only where the upper ones are equal.  The scores
+// wait in LDS for the places that take them.
 // Bound by latency: T x E logits are a few megabytes at most.  Measured: one
-// token of 256 experts in 8 groups 6.1 us, 3015 tokens of 128 experts 7.4 us.
+// token of 256 experts in 8 groups 5.2 us, 3015 tokens of 128 experts 6.1 us (6.2
+// and 8.1 with 64-bit maxima and the chosen scores computed again).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "gq_device.h"
 #include "gq_f8_internal.h"
-#include "gq_route_core.h"
 
 namespace {
 
@@ -46,6 +48,36 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
     return v;
+}
+
+// Largest value of the wave, in every lane: each step is one instruction (0,
+// which lanes without a source get, is the smallest value).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t max_of(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+    return o > v ? o : v;
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = max_of<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8: each row's maximum in its last lane
+    v = max_of<0x112, 0xF>(v);
+    v = max_of<0x114, 0xF>(v);
+    v = max_of<0x118, 0xF>(v);
+    v = max_of<0x142, 0xA>(v);  // row_bcast15 into rows 1 and 3
+    v = max_of<0x143, 0xC>(v);  // row_bcast31 into rows 2 and 3
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// The lowest lane that holds the largest key: by the upper halves, and by the
+// lower ones where those are equal.
+__device__ __forceinline__ int wave_argmax_u64(uint64_t v) {
+    const uint32_t hi = (uint32_t)(v >> 32), top = wave_max_u32(hi);
+    uint64_t at = __ballot(hi == top);
+    if (at & (at - 1)) {
+        const uint32_t lo = hi == top ? (uint32_t)v : 0u;
+        const uint32_t low = wave_max_u32(lo);
+        at &= __ballot(lo == low);
+    }
+    return __builtin_ctzll(at);
 }
 
 template <typename T>
@@ -77,7 +109,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_route_scored(const T* __restrict
     float v[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) v[i] = load_logit(l + (e0 + i < n_experts ? e0 + i : n_experts - 1));
-    double m = 0.0, total = 1.0;
+    float b[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) b[i] = bias ? bias[e0 + i < n_experts ? e0 + i : n_experts - 1] : 0.0f;
+    double m = 0.0;
     if (score != SCORE_SIGMOID) {
         float mx = v[0];  // (a clamped index repeats a real logit)
 #pragma unroll
@@ -86,30 +121,29 @@ __global__ __launch_bounds__(64 * WAVES) void k_route_scored(const T* __restrict
         for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
         m = mx;
     }
-    double c[NI];
+    double s[NI];
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        c[i] = score_of(score, v[i], m);
-        sum += e0 + i < n_experts ? c[i] : 0.0;
+        s[i] = score_of(score, v[i], m);
+        sum += e0 + i < n_experts ? s[i] : 0.0;
     }
     if (score != SCORE_SIGMOID) {
-        total = wave_sum_f64(sum);
+        const double total = wave_sum_f64(sum);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) c[i] = c[i] == 0.0 ? 0.0 : c[i] / total;
-    }
-    if (bias) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) c[i] += (double)bias[e0 + i < n_experts ? e0 + i : n_experts - 1];
+        for (int i = 0; i < NI; ++i) s[i] = s[i] == 0.0 ? 0.0 : s[i] / total;
     }
     uint64_t key[NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) key[i] = e0 + i < n_experts ? order_key64(c[i]) : 0ull;
+    for (int i = 0; i < NI; ++i) key[i] = e0 + i < n_experts ? order_key64(s[i] + (double)b[i]) : 0ull;
 
     if (n_groups > 1) {
         const int gs = n_experts / n_groups;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) lds[wave][e0 + i] = c[i] != c[i] ? -__builtin_inf() : c[i];
+        for (int i = 0; i < NI; ++i) {
+            const double c = s[i] + (double)b[i];
+            lds[wave][e0 + i] = c != c ? -__builtin_inf() : c;
+        }
         wave_lds_fence();
         // P lanes per group find its two largest values
         const int P = 1 << (31 - __builtin_clz(64 / n_groups));
@@ -147,6 +181,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_route_scored(const T* __restrict
         }
     }
 
+    // the scores, for whichever lane's place takes them
+    wave_lds_fence();
+#pragma unroll
+    for (int i = 0; i < NI; ++i) lds[wave][e0 + i] = s[i];
+    wave_lds_fence();
+
     int my_id = 0;
     for (int j = 0; j < top_k; ++j) {
         uint64_t best = key[0];
@@ -157,8 +197,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_route_scored(const T* __restrict
                 best = key[i];
                 bi = i;
             }
-        const uint64_t win = gqr::wave_max_u64(best);
-        const int owner = __builtin_ctzll(__ballot(best == win));
+        const int owner = wave_argmax_u64(best);
         const int e = owner * NI + __builtin_amdgcn_readlane(bi, owner);
 #pragma unroll
         for (int i = 0; i < NI; ++i)
@@ -166,16 +205,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_route_scored(const T* __restrict
         if (lane == j) my_id = e;
     }
     if (my_id >= n_experts) my_id = n_experts - 1;  // (cannot happen: enough experts stay)
-    // the chosen experts' scores again, from their logits: lane j holds place j's
-    double s = 0.0;
-    if (lane < top_k) {
-        s = score_of(score, load_logit(l + my_id), m);
-        if (score != SCORE_SIGMOID) s = s == 0.0 ? 0.0 : s / total;
-    }
-    double w = s;
+    const double chosen_s = lane < top_k ? lds[wave][my_id] : 0.0;
+    double w = chosen_s;
     if (renorm) {
-        const double chosen = wave_sum_f64(s);
-        w = chosen == 0.0 ? 0.0 : s / chosen;
+        const double chosen = wave_sum_f64(chosen_s);
+        w = chosen == 0.0 ? 0.0 : chosen_s / chosen;
     }
     if (lane < top_k) {
         ids[(int64_t)t * top_k + lane] = my_id;
