@@ -606,14 +606,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_tile_id(const uint8_t* __re
 // Routed, bf16 results, short rows (at most KB <= 6 blocks of 128): a wavefront
 // keeps its 32 rows of X in registers, for all of K, and only W goes through LDS,
 // in panels of 32 columns and all of K.  Beside half the copies, a panel is one
-// piece of memory, read in whole lines (blocks of 128 inputs of rows of 704 bytes
-// are not).  The panels are copied two ahead; a row of one is CHP = 8 KB + 1
-// chunks of 16 bytes, odd, so that 16 rows at one chunk cover all banks, and its
-// rows lie in the order of the operands (see Tile: a lane ends up with eight
-// neighbouring columns).  A panel's results are stored behind the next barrier,
-// ahead of the next copies, so that no wait is for a store just made.
-// 3015 x 8 slots of 128 experts, 2816 x 704: 115 us (128 x 128 tiles: 148 us); of
-// that the copies alone 68, the stores 23, products and stores without copies 86.
+// piece of memory whose lines are read at one time (blocks of 128 inputs of rows
+// of 704 bytes share lines).  The panels are copied two ahead, block by block,
+// their rows in the operands' order (see Tile: a lane ends up with eight
+// neighbouring columns), the chunks swizzled as there.  A panel's results are
+// stored behind the next barrier, ahead of the next copies, so that no wait is for
+// a store just made.
+// 3015 x 8 slots of 128 experts, 2816 x 704: 112 us (128 x 128 tiles: 148 us); 82
+// without the copies, 90 without the stores, and 22 for two starts one after the
+// other.  X through LDS in whole lines starts sooner but holds the panels up (146
+// against 147 us a call, other shapes 8% less to 6% more); whole rows of a panel
+// one after another, of odd stride, have bank conflicts (147 against 146 us).
 constexpr int PANELS = 3;
 
 template <int KB, int WV>
@@ -623,9 +626,10 @@ __global__ __launch_bounds__(64 * WV, 2) void k_f8_short_id(const uint8_t* __res
                                                             const float* __restrict__ xs, int64_t ldx, int64_t xs_ld,
                                                             uint16_t* __restrict__ Y, int gm, int gn, int split,
                                                             Table t) {
-    // copies of a panel, and of a wavefront; those past the panel's go to the last KB of LDS
-    constexpr int CHP = 8 * KB + 1, NI = (32 * CHP + 63) / 64, CI = (NI + WV - 1) / WV;
-    __shared__ __align__(16) uint8_t smem[(PANELS * NI + 1) * 1024];
+    // copies of a panel, and of a wavefront
+    constexpr int NI = 4 * KB, CI = NI / WV;
+    static_assert(NI % WV == 0, "whole copies");
+    __shared__ __align__(16) uint8_t smem[PANELS * NI * 1024];
     const int tiles = t.hdr[1], real = (tiles < gm ? tiles : gm) * split;
     if ((int)blockIdx.x >= real) return;
     const int id = xcd_order(blockIdx.x, real), tm = id / split, part = id % split;
@@ -643,22 +647,19 @@ __global__ __launch_bounds__(64 * WV, 2) void k_f8_short_id(const uint8_t* __res
         return s < (unsigned)t.S ? (int64_t)s : t.S - 1;
     };
 
-    // copies: position 64 (wave + WV u) + lane of a panel is chunk c of its row r
+    // copy i of a panel: of block i / 4 the rows 8 (i % 4) .. + 7, in the operands' order
     uint32_t off[CI];
 #pragma unroll
     for (int u = 0; u < CI; ++u) {
-        const int p = 64 * (wave + WV * u) + lane, r = p / CHP, c = p - r * CHP;
+        const int i = wave + WV * u, r = 8 * (i & 3) + (lane >> 3), c = 8 * (i >> 2) + ((lane & 7) ^ ((r >> 1) & 7));
         const int row = 8 * ((r & 15) >> 2) + 4 * (r >> 4) + (r & 3);
-        off[u] = r < 32 && 16 * c < K ? (uint32_t)(row * K + 16 * c) : NOWHERE;
+        off[u] = 16 * c < K ? (uint32_t)(row * K + 16 * c) : NOWHERE;
     }
     auto load = [&](int panel, int buf) {
         const int64_t n = (int64_t)panel * 32;
         const Rsrc r = make_rsrc(W + n * K, panel < end ? (N - n < 32 ? N - n : 32) * K : 0);
 #pragma unroll
-        for (int u = 0; u < CI; ++u) {
-            const int i = wave + WV * u;
-            copy16(r, off[u], smem + 1024 * (i < NI ? buf * NI + i : PANELS * NI));
-        }
+        for (int u = 0; u < CI; ++u) copy16(r, off[u], smem + 1024 * (buf * NI + wave + WV * u));
     };
     load(first, 0);
     load(first + 1, 1);
@@ -684,7 +685,7 @@ __global__ __launch_bounds__(64 * WV, 2) void k_f8_short_id(const uint8_t* __res
             sx[kb][j] = kb < kbs ? xs[kb * xs_ld + x_row[j]] : 0.0f;
         }
     const bool idle = wm >= rows, vec = (N & 7) == 0;  // (idle: none of this wavefront's rows is used)
-    const int at0 = fr * CHP + fq, at1 = at0 + 16 * CHP;
+    const int at0 = pos128(fr, fq), at1 = pos128(fr, 4 + fq);  // (16 rows further: 128 positions)
     f32x4 acc[2][2];
     auto store = [&](int panel) {
 #pragma unroll
@@ -714,8 +715,8 @@ __global__ __launch_bounds__(64 * WV, 2) void k_f8_short_id(const uint8_t* __res
                 for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                const i32x8 a[2] = {join(d[at0 + 8 * kb], d[at0 + 8 * kb + 4]),
-                                    join(d[at1 + 8 * kb], d[at1 + 8 * kb + 4])};
+                const i32x8 a[2] = {join(d[256 * kb + at0], d[256 * kb + at1]),
+                                    join(d[256 * kb + 128 + at0], d[256 * kb + 128 + at1])};
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
