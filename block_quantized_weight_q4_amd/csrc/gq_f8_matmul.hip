@@ -890,10 +890,11 @@ hipError_t tile_id(const Call<TY>& c, int64_t gm) {
 }
 
 // n_tiles: the tiles that are likely.  About 4 workgroups of four wavefronts a CU
-// (two run at once), or one of eight; each loads its rows of X first, which pays
-// from 3 panels on (2816 x 704, 188 slots for each of 128 experts: 149, 150 and
-// 155 us with 1000, 2000 and 500 workgroups; 2816 x 768, 754 for each of 16: 61
-// and 67 us with 200 and 400 of eight).
+// (two run at once), or one of eight; each loads its rows of X first, so none has
+// fewer than 3 panels (2816 x 704, 188 slots for each of 128 experts: 154, 156 and
+// 161 us with 1000, 2000 and 500 workgroups; 2816 x 768, 754 for each of 16: 61
+// and 67 us with 200 and 400 of eight; 704 x 640, 377 for each of 16: 20 and 24 us
+// with 3 and 6 panels each).
 template <int KB, int WV>
 hipError_t short_id(const Call<uint16_t>& c, int64_t gm, int64_t n_tiles) {
     const int64_t gn = (c.N + 31) / 32, groups = gqk_cu_count() * (WV == 4 ? 4 : 1);
@@ -970,9 +971,10 @@ hipError_t stream_id(const Call<TY>& c, int64_t gm) {
     return stream<1, 2, 8, true>(c, gm);
 }
 
-// Many slots an expert: tiles of h = 128 or 256 slots.  Short rows: from 3 in 4
-// down to 9 in 10 of the tile kernels' time (500 tokens x 2 of 8 experts, 400 x
-// 400: 12.1 against 18.7 us; 3015 x 4 of 16, 2816 x 768: 61.4 against 68.6 us).
+// Many slots an expert: tiles of h = 128 or 256 slots.  Short rows take 0.6 to
+// 0.92 of the tile kernels' time (500 tokens x 2 of 8 experts, 400 x 400: 11.2
+// against 18.7 us; 3015 x 4 of 16, 2816 x 768: 59.9 against 68.6 us; 3015 x 2 of
+// 4, 2100 x 256: 43.4 against 47.0 us).
 hipError_t many_id(const Call<uint16_t>& c, int64_t gm, int h, int n_experts) {
     if (c.K > 0 && c.K <= 6 * BLK) {
         const int64_t n_tiles = (c.M + h - 1) / h + n_experts / 2;  // (an expert's last is half full)
