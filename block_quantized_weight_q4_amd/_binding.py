@@ -520,7 +520,7 @@ def gq_f8_quant(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, pow2: bo
         ok = (d >= 0 and d == q.get_device() == scales.get_device() and x.dtype in _HALF_OR_F32 and
               q.dtype in _F8 and scales.dtype is _f32 and q.shape == (M, K) and
               scales.shape == ((K + 127) // 128, M) and x1 == q1 == 1 and (s1 == 1 or M == 1))
-    except (AttributeError, ValueError):
+    except (AttributeError, ValueError, IndexError):
         ok = False
     if not ok:
         _check_quant(x, q, scales)
@@ -540,7 +540,7 @@ def gq_f8_glu_quant(g: torch.Tensor, u: torch.Tensor, act: str, q: torch.Tensor,
               g.dtype in _HALF_OR_F32 and u.dtype is g.dtype and q.dtype in _F8 and scales.dtype is _f32 and
               u.shape == q.shape == (M, K) and scales.shape == ((K + 127) // 128, M) and act in ACTS and
               g1 == u1 == q1 == 1 and (s1 == 1 or M == 1))
-    except (AttributeError, ValueError):
+    except (AttributeError, ValueError, IndexError):
         ok = False
     if not ok:
         _need(act in ACTS, "act must be one of %s" % sorted(ACTS))

@@ -280,3 +280,10 @@ def test_sizes_past_a_launch_are_refused(lib):
                   [A, A, 1, 64, 16, A, 1, 1, A, A, 16, 1, 0, None, A, F32, A, 1 << 40, None])(N=n) == SHAPE
     assert caller(lib.gq_route_scored, "l d T E k score bias G top rank renorm scale ids w st".split(),
                   [A, F32, 8, 8, 8, 1, None, 1, 1, 0, 1, 1.0, A, A, None])(T=(1 << 25) + 1) == SHAPE
+
+
+@pytest.mark.parametrize("shape", [(), (2,), (1, 2, 4)])
+def test_binding_names_scales_that_are_not_2d(lib, shape):
+    import block_quantized_weight_q4_amd as gq
+    refuses("scales must be", gq.gq_f8_quant, t(4, 256), t(4, 256, dt=U8), t(*shape))
+    refuses("scales must be", gq.gq_f8_glu_quant, t(4, 256), t(4, 256), "silu", t(4, 256, dt=U8), t(*shape))
