@@ -285,5 +285,5 @@ def test_sizes_past_a_launch_are_refused(lib):
 @pytest.mark.parametrize("shape", [(), (2,), (1, 2, 4)])
 def test_binding_names_scales_that_are_not_2d(lib, shape):
     import block_quantized_weight_q4_amd as gq
-    refuses("scales must be", gq.gq_f8_quant, t(4, 256), t(4, 256, dt=U8), t(*shape))
-    refuses("scales must be", gq.gq_f8_glu_quant, t(4, 256), t(4, 256), "silu", t(4, 256, dt=U8), t(*shape))
+    refuses("scales must be", gq.gq_f8_quant, t(4, 256), t(4, 256, dt=U8), torch.zeros(shape))
+    refuses("scales must be", gq.gq_f8_glu_quant, t(4, 256), t(4, 256), "silu", t(4, 256, dt=U8), torch.zeros(shape))
