@@ -19,7 +19,8 @@ __all__ = [
 
 def __getattr__(name):
     if name in __all__:
-        from . import _binding
-        globals()[name] = value = getattr(_binding, name)  # found directly from now on
-        return value
+        module = globals().get("_binding")  # (the import statement costs more than the rest of this)
+        if module is None:
+            from . import _binding as module
+        return getattr(module, name)
     raise AttributeError(name)

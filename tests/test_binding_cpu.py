@@ -130,3 +130,15 @@ def test_dequant_and_route_checks():
         gq.gq_route_topk(host(4, 16, dtype=bf16), 2, host(4, 2, dtype=i32), host(4, 2))
     with pytest.raises(TypeError, match="GPU tensor"):
         gq.gq_matvec_id_check(host(256, dtype=u8))
+
+
+def test_the_package_looks_entry_points_up_in_the_binding(monkeypatch):
+    """A replaced entry point (a wrapper that times or records calls) is the one that the package gives, every time."""
+    import block_quantized_weight_q4_amd as package
+    for name in ("gq_matvec", "gq_f8_quant"):
+        was = getattr(gq, name)
+        assert getattr(package, name) is was
+        monkeypatch.setattr(gq, name, lambda *a: "replaced")
+        assert getattr(package, name)() == "replaced"
+        monkeypatch.undo()
+        assert getattr(package, name) is was
