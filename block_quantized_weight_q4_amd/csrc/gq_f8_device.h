@@ -128,7 +128,9 @@ __device__ __forceinline__ u32x4 bld16(Rsrc r, uint32_t off) {
 typedef __attribute__((address_space(3))) void* LdsPtr;
 typedef const __attribute__((address_space(1))) void* GlobalPtr;
 
-// (base: the same for the whole wavefront, off + base below 2^31)
+// (base: the same for the whole wavefront, off + base below 2^31; whether the
+// range check counts base is left open: where off is within the resource, off +
+// base must be too)
 __device__ __forceinline__ void copy16(Rsrc r, uint32_t off, uint8_t* lds, uint32_t base = 0) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)lds, 16, (int)off, (int)base, 0, 0);
 }

@@ -344,7 +344,15 @@ struct Tile {
             else xoff[u] = (uint32_t)(lr * ldx) + xchunk;
         }
         const int64_t x_rows = t.per_slot ? t.S : t.S / (t.top_k > 0 ? t.top_k : 1);
-        const Rsrc xr = ROUTED ? make_rsrc(X, FAR ? 0 : x_rows * ldx) : make_rsrc(X + m0 * ldx, (int64_t)rows * ldx);
+        const Rsrc xr = make_rsrc(X, ROUTED && !FAR ? x_rows * ldx : 0);
+        // Rows 8 WV u and on of `rows` rows of `width` bytes from p: each copy has a
+        // resource of its own, so that no row past the last one is read whether or
+        // not the range check counts the scalar offset (an offset of k is within
+        // the lane's row).
+        auto rows_from = [](const uint8_t* p, int u, int rows, int64_t width) {
+            const int n = rows - 8 * WV * u;
+            return make_rsrc(p + 8 * WV * u * width, (n > 0 ? n : 0) * (int)width);
+        };
         // one copy of 64 scales: wavefronts below BM / 64 those of X, the others
         // W's (lane w: of wavefront w's columns), from sbase[slane + ck * sstep];
         // a tile further (routed), W's lie snext on, as far as the last row of blocks
@@ -371,20 +379,20 @@ struct Tile {
             cg = cg + 1 == NB ? 0 : cg + 1;
             const int k = ck * BLK;
             const int left = (int)K - k, wleft = cn < n_end ? left : 0;  // (W past the last tile: zeros)
+            const int w_rows = N - cn < BN ? (int)(N - cn) : BN;
             const uint32_t wo = within(woff, (int)wchunk, wleft);
             // (FAR: past K the row's first chunk, times zeros)
             const int xk = k + ((int)xchunk < left ? (int)xchunk : -k);
-            const Rsrc wr = make_rsrc(W + cn * K, cn < N ? (N - cn < BN ? N - cn : BN) * K : 0);
 #pragma unroll
             for (int u = 0; u < XI; ++u) {
                 uint8_t* l = d + (wave + WV * u) * 1024;
                 if constexpr (FAR) copy16(xp[u] + xk, l);
                 else if constexpr (ROUTED) copy16(xr, within(xoff[u], (int)xchunk, left), l, (uint32_t)k);
-                else copy16(xr, within(xoff[0], (int)xchunk, left), l, (uint32_t)(8 * WV * u * ldx + k));
+                else copy16(rows_from(X + m0 * ldx, u, rows, ldx), within(xoff[0], (int)xchunk, left), l, (uint32_t)k);
             }
 #pragma unroll
             for (int u = 0; u < WI; ++u)
-                copy16(wr, wo, d + BM * BLK + (wave + WV * u) * 1024, (uint32_t)(8 * WV * u * K + k));
+                copy16(rows_from(W + cn * K, u, w_rows, K), wo, d + BM * BLK + (wave + WV * u) * 1024, (uint32_t)k);
             copy4(sbase + (slane + (ck < KB ? ck : KB - 1) * sstep), d + SX + wave * 256);
             ++ck;
             if constexpr (MANY) {
