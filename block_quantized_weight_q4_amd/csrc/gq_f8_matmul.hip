@@ -889,8 +889,10 @@ hipError_t tile(const Call<TY>& c) {
 
 template <int BM, int BN, int WM, int WN, int NB, bool FAR, typename TY>
 hipError_t tile_id(const Call<TY>& c, int64_t gm) {
-    // two tiles of columns a workgroup (one with 256 rows): the second one's copies hide the first one's end
-    const int64_t gn = (c.N + BN - 1) / BN, split = BM < 256 ? (gn + 1) / 2 : gn;
+    // two tiles of columns a workgroup (one with 256 rows): the second one's copies hide the first one's end;
+    // more where a launch would have too many workgroups (at most 20,480 tiles of slots: at least one each)
+    const int64_t gn = (c.N + BN - 1) / BN, most = (((int64_t)1 << 32) - 1) / (64 * WM * WN) / gm;
+    const int64_t split = BM < 256 ? ((gn + 1) / 2 < most ? (gn + 1) / 2 : most) : gn;
     hipLaunchKernelGGL((k_f8_tile_id<BM, BN, WM, WN, NB, TY, FAR>), dim3((unsigned)(gm * split)), dim3(64 * WM * WN),
                        0, c.s, c.W, c.wsc, c.N, c.K, c.X, c.xs, c.ldx, c.xs_ld, c.Y, (int)gm, (int)gn, (int)split,
                        c.t);
@@ -957,6 +959,23 @@ hipError_t matmul(const Call<TY>& c) {
     return tile<128, 128, 4, 2, 2, false>(c);
 }
 
+// A launch has fewer than 2^23 workgroups of eight wavefronts, the last round's
+// quarters among them: more rows than that many tiles of 128 x 128 have are
+// multiplied by several.
+template <typename TY>
+hipError_t matmul_rows(Call<TY> c) {
+    const int64_t M = c.M, most = ((1 << 23) - 1024) / ((c.N + 127) / 128) * 128;
+    for (int64_t m = 0; m < M; m += most) {
+        c.M = M - m < most ? M - m : most;
+        const hipError_t e = matmul(c);
+        if (e != hipSuccess) return e;
+        c.X += most * c.ldx;
+        c.xs += most;
+        c.Y += most * c.ldy;
+    }
+    return hipSuccess;
+}
+
 // Measured at 64 experts of 1408 x 2816 and 2816 x 704 by the slots an expert
 // has on average: 16 slots a tile up to 8 (4 each: 45 us against 56 us with
 // 64), 64 up to 48 (24 each: 63 against 77 and 65 us with 16 and 128),
@@ -996,6 +1015,21 @@ hipError_t many_id(const Call<float>& c, int64_t gm, int h, int) {
     return tile_id<256, 128, 4, 2, 2, false>(c, gm);
 }
 
+// Rows of X that lie 2^31 bytes and more apart: the tile kernels again, with
+// pointers.  Where there are few tiles, eight wavefronts and one tile of columns
+// a workgroup take the shorter tiles too: 33 and 132 slots for each of 32 and 8
+// experts of 768 x 2816, 32.8 and 35.3 us (two tiles a workgroup: 41.1 and 50.7
+// us), fp32 46.1 and 49.9 (47.5 and 70); from 517 tiles on the other way round:
+// 62 slots for each of 32 of 1408 x 2816 59.8 us (64.8), of 64 of 768 x 2816 62.6
+// (69.7), fp32 80.0 (97.1), 31 for each of 256 of 1408 x 2816 247 us (360).
+template <typename TY>
+hipError_t far_id(const Call<TY>& c, int64_t gm, int h) {
+    const bool few = 2 * gm * ((c.N + 127) / 128) <= 3 * (int64_t)gqk_cu_count();
+    if (h == 64 && !few) return tile_id<64, 128, 1, 4, 2, true>(c, gm);
+    if (h == 128 && !few) return tile_id<128, 128, 2, 2, 2, true>(c, gm);
+    return tile_id<256, 128, 4, 2, 2, true>(c, gm);
+}
+
 template <typename TY>
 hipError_t matmul_id(Call<TY> c, int n_experts, const int32_t* ids, int n_tokens, int top_k, int x_per_slot,
                      const float* route_w, int y_dtype, void* ws) {
@@ -1014,8 +1048,9 @@ hipError_t matmul_id(Call<TY> c, int n_experts, const int32_t* ids, int n_tokens
     const bool small = ids && S <= SMALL && h == 16;
     c.t = Table{hdr, tiles, slot_e, slot, n_experts, S, top_k, x_per_slot, small ? ids : nullptr, !route_w};
     const int64_t rows = x_per_slot ? S : n_tokens;
-    // (the most workgroups that any of the tile kernels takes; before anything is launched)
-    if (h > 16 && !grid_ok(gm * ((c.N + 127) / 128), 512)) return hipErrorInvalidValue;
+    // (one tile of columns a workgroup: more than 320 slots for each expert, so a Y of 600 GB; before anything is
+    // launched)
+    if (h == 256 && !grid_ok(gm * ((c.N + 127) / 128), 512)) return hipErrorInvalidValue;
     if (ids && !small) {
         hipLaunchKernelGGL((k_f8_plan<TY>), dim3(n_experts + 1), dim3(S <= 4096 ? 256 : 1024), 0, c.s, ids, S,
                            n_experts, h, hdr, tiles, slot_e, slot, route_w ? nullptr : y, c.N);
@@ -1024,7 +1059,7 @@ hipError_t matmul_id(Call<TY> c, int n_experts, const int32_t* ids, int n_tokens
     }
     hipError_t e;
     if (h == 16) e = stream_id(c, gm);
-    else if (rows * c.ldx >= INT_MAX) e = tile_id<256, 128, 4, 2, 2, true>(c, gm);
+    else if (rows * c.ldx >= INT_MAX) e = far_id(c, gm, h);
     else if (h == 64) e = tile_id<64, 128, 1, 4, 2, false>(c, gm);
     else e = many_id(c, gm, h, n_experts);
     if (e != hipSuccess || !route_w) return e;
@@ -1038,8 +1073,8 @@ hipError_t matmul_id(Call<TY> c, int n_experts, const int32_t* ids, int n_tokens
 hipError_t gqk_f8_matmul(const uint8_t* W, const float* ws, int64_t N, int64_t K, const uint8_t* X, const float* xs,
                          int64_t M, int64_t ldx, int64_t xs_ld, void* Y, int y_dtype, int64_t ldy, hipStream_t s) {
     if (y_dtype == gqd::DT_F32)
-        return matmul(Call<float>{W, ws, N, K, X, xs, M, ldx, xs_ld, static_cast<float*>(Y), ldy, Table{}, s});
-    return matmul(Call<uint16_t>{W, ws, N, K, X, xs, M, ldx, xs_ld, static_cast<uint16_t*>(Y), ldy, Table{}, s});
+        return matmul_rows(Call<float>{W, ws, N, K, X, xs, M, ldx, xs_ld, static_cast<float*>(Y), ldy, Table{}, s});
+    return matmul_rows(Call<uint16_t>{W, ws, N, K, X, xs, M, ldx, xs_ld, static_cast<uint16_t*>(Y), ldy, Table{}, s});
 }
 
 size_t gqk_f8_matmul_id_ws_bytes(int n_experts, int n_tokens, int top_k, int64_t N, int y_dtype, int weighted) {

@@ -163,3 +163,72 @@ def test_matvec_without_inputs(gq, batch):
     y = torch.full((batch, 70), 3.0, device="cuda")
     gq.gq_f8_matvec(W, torch.zeros(1, 0, device="cuda"), torch.zeros(batch, 0, device="cuda"), y)
     assert (y == 0).all()
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_more_rows_than_a_launch_counts(gq, out):
+    """More than 2^30 rows of X: 2^23 tiles of 128, in several launches."""
+    M, N, K = (1 << 30) + 300, 3, 16
+    q, s = P.weights(np.random.default_rng(5), N, K)
+    xq = torch.randint(0, 0x7F, (M, K), dtype=torch.uint8, device="cuda",
+                       generator=torch.Generator(device="cuda").manual_seed(1))
+    xs = torch.ones(1, M, device="cuda")
+    xs[:, ::3] = 0.5
+    Y = torch.full((M, N), float("nan"), dtype=DT[out], device="cuda")
+    gq.gq_f8_matmul(dev(q), dev(s), xq, xs, Y)
+    seam = ((1 << 23) - 1024) * 128
+    for lo in (0, seam - 70, M - 100):
+        hi = min(lo + 140, M)
+        near(Y[lo:hi], *matmul_ref(q, s, xq[lo:hi].cpu().numpy(), xs[:, lo:hi].cpu().numpy(), out))
+    for lo in range(0, M, 1 << 28):
+        assert torch.isfinite(Y[lo:lo + (1 << 28)]).all()
+    del xq, xs, Y
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("out,N", [("f32", 233_100), ("bf16", 1_000_100)])
+def test_many_experts_of_very_many_rows(gq, out, N):
+    """More tiles than a launch counts, at one tile of columns a workgroup and at two."""
+    E, T, k, K = 4096, 8194, 4, 16
+    W, s = wide(N, K)
+    W = W[None].expand(E, N, K).contiguous()
+    W[1::2] ^= 0x80  # every other expert's weights have the other sign
+    s = s[None].expand(E, -1, 1).contiguous()
+    xq, xs = P.activations(np.random.default_rng(2), 50, K)
+    again = np.arange(T) % 50
+    ids = torch.arange(T * k, device="cuda", dtype=torch.int32).view(T, k) * 7 % E
+    ws = torch.full((gq.gq_f8_matmul_id_workspace(E, T, k, N, DT[out], False),), 0xAB, dtype=torch.uint8,
+                    device="cuda")
+    Y = torch.full((T, k, N), float("nan"), dtype=DT[out], device="cuda")
+    gq.gq_f8_matmul_id(W, s, ids, dev(xq[again]), dev(xs[:, again]), Y, ws)
+    lo = N - N % 128 - 128
+    for at in (0, N // 2 - N // 2 % 128, lo):
+        hi = min(at + 300, N)
+        ref, tol = matmul_ref(W[0, at:hi].cpu().numpy(), s[0, at // 128:(hi + 127) // 128].cpu().numpy(), xq, xs, out)
+        rows = np.array([0, 1, 51, T // 2, T - 1])
+        sign = np.where(ids[torch.from_numpy(rows)].cpu().numpy() % 2, -1.0, 1.0)[:, :, None]
+        near(Y[torch.from_numpy(rows).cuda(), :, at:hi], ref[again[rows]][:, None] * sign,
+             np.repeat(tol[again[rows]][:, None], k, 1))
+    for t in range(0, T, 1024):
+        assert torch.isfinite(Y[t:t + 1024]).all()
+    del W, Y
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("E,T,k,N,per_slot", [(32, 530, 2, 200, False), (9, 300, 2, 200, True), (2, 700, 2, 200, False),
+                                              (90, 700, 4, 400, False), (90, 1500, 4, 400, False)])
+def test_far_rows_at_every_tile_height(gq, E, T, k, N, per_slot, out):
+    """Rows of X 4 MB apart, more than 2^31 bytes in all; 33, 67, 700, 31 and 67 slots for each expert, the last two
+    with more tiles than CUs."""
+    ld, K = 1 << 22, 272
+    r = Routed(E, T, k, N, K, per_slot, out)
+    X = torch.empty(len(r.xq), ld, dtype=torch.uint8, device="cuda")[:, :K]
+    X.copy_(dev(r.xq))
+    ws = torch.full((gq.gq_f8_matmul_id_workspace(E, T, k, N, DT[out], False),), 0xAB, dtype=torch.uint8,
+                    device="cuda")
+    Y = torch.full((T, k, N), float("nan"), dtype=DT[out], device="cuda")
+    gq.gq_f8_matmul_id(dev(r.q), dev(r.s), dev(r.ids), X, dev(r.xs), Y, ws)
+    near(Y, *r.ref())
+    del X
+    torch.cuda.empty_cache()
