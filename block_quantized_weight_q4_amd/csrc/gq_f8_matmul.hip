@@ -925,18 +925,30 @@ hipError_t short_id(const Call<uint16_t>& c, int64_t gm, int64_t n_tiles) {
 
 
 // Which kernel: measured at N x K of 1024 x 2560, 5120 x 5120, 2560 x 9728 and
-// 17408 x 5120, 16 to 2048 rows.  What decides is how many tiles there are for
-// the CUs.  Few 64 x 128 tiles: the stream kernel, which splits K (256 rows of
-// 2560 x 9728: 15.8 us against 31.6 us in tiles).  Up to one a CU: those tiles,
-// eight wavefronts each and four blocks ahead (2048 rows of 1024 x 2560: 12.1
-// against 14.8 us two blocks ahead, 19.9 us streamed); up to one 128 x 128 tile
-// a CU: those in the same way (512 rows of 5120 x 5120: 28.8 against 32.6 us);
-// then two of these a CU, two blocks ahead (2048 rows of 2560 x 9728: 74.1
-// against 93.1 us), until 256 x 256 tiles fill half of the CUs (2048 rows of
-// 5120 x 5120: 71.0 against 73.2 us, of 17408 x 5120: 225 against 243 us).  An
-// fp32 result's products run at half the rate, which favours the stream kernel
-// longer (512 rows of 2560 x 9728: 37.3 against 53.8 us) and leaves 256 x 256
-// without registers.
+// 17408 x 5120, 16 to 2048 rows, and at N of 20,480 to 151,936, 17 to 769 rows.
+// What decides is how many tiles there are for the CUs.  Few 64 x 128 tiles: the
+// stream kernel, which splits K (256 rows of 2560 x 9728: 15.8 us against 31.6 us
+// in tiles).  Up to one a CU: those tiles, eight wavefronts each and four blocks
+// ahead (2048 rows of 1024 x 2560: 11.6 against 14.8 us two blocks ahead, 19.9 us
+// streamed); up to one 128 x 128 tile a CU: those in the same way (512 rows of
+// 5120 x 5120: 28.8 against 32.6 us); then two of these a CU, two blocks ahead
+// (2048 rows of 2560 x 9728: 72.3 against 93.1 us).
+// 256 x 256 tiles where they fill half of the CUs (2048 rows of 5120 x 5120: 70.3
+// against 73.2 us, of 17408 x 5120: 225 against 243 us), 128 x 128 ones take more
+// than one round (256 rows of 32768 x 5120: 93.0 against 73.9 us) and at most a
+// quarter of what they cover is padding that smaller ones do not have (257 rows of
+// 17408 x 5120: 69.5 against 46.7 us, 128 of 34816 x 5120 74.4 against 72.4, 60000
+// of 64 x 5120 86 against 72; 513 rows of 17408 x 5120 on the other side: 71.4
+// against 81.7 us).
+// Up to 64 rows leave half of a taller tile empty: one 64 x 128 tile a CU, and past
+// that two, two blocks ahead (40 rows of 34816 x 5120: 53.4 us, 54.5 in 128 x 128
+// and 69 in 256 x 256 tiles; 64 of 151,936 x 5120: 165, 185 and 220 us); up to 32
+// the stream kernel, which reads W once for them (32 of 34816 x 5120: 44.9 against
+// 51.0 us).
+// An fp32 result's products run at half the rate, which favours the stream kernel
+// longer (512 rows of 2560 x 9728: 37.3 against 53.8 us; not with 33 to 64 rows, for
+// which it reads W twice: 64 of 151,936 x 5120 356 against 196 us) and leaves 256 x
+// 256 without registers.
 template <typename TY>
 hipError_t matmul(const Call<TY>& c) {
     auto tiles = [&](int64_t h, int64_t w) { return ((c.M + h - 1) / h) * ((c.N + w - 1) / w); };
@@ -948,13 +960,13 @@ hipError_t matmul(const Call<TY>& c) {
         if (tiles(48, 64) >= 3 * cus / 4) return stream<3, 4, 8, false>(c, (c.M + 47) / 48);
         return stream<3, 2, 8, false>(c, (c.M + 47) / 48);
     }
+    if (c.M <= 32) return stream<2, 2, 8, false>(c, (c.M + 31) / 32);
+    if (tiles(64, 128) <= cus && (sizeof(TY) == 2 || c.M <= 64)) return tile<64, 128, 2, 4, 4, false>(c);
+    if (c.M <= 64) return tile<64, 128, 2, 4, 2, false>(c);
     if constexpr (sizeof(TY) == 2) {
-        if (c.M <= 32) return stream<2, 2, 8, false>(c, (c.M + 31) / 32);
-        if (tiles(64, 128) <= cus) return tile<64, 128, 2, 4, 4, false>(c);
-        if (tiles(128, 128) <= cus) return tile<128, 128, 4, 2, 4, false>(c);
-        if (tiles(256, 256) >= cus / 2) return tile<256, 256, 4, 2, 2, true>(c);
-    } else {
-        if (c.M <= 64) return stream<2, 2, 8, false>(c, (c.M + 31) / 32);
+        const int64_t small = tiles(128, 128), large = tiles(256, 256);
+        if (small <= cus) return tile<128, 128, 4, 2, 4, false>(c);
+        if (large >= cus / 2 && small > 2 * cus && 3 * large < small) return tile<256, 256, 4, 2, 2, true>(c);
     }
     return tile<128, 128, 4, 2, 2, false>(c);
 }

@@ -356,3 +356,12 @@ def test_matmul_id_tile_heights(gq, E, T, k, N, K, out):
 def test_matmul_every_kernel(gq, M, N, K, out):
     """Sizes on both sides of the rules that choose a kernel, the split last round of tiles among them."""
     matmul_case(gq, M, N, K, out)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(M, N, 144) for M in (17, 33, 40, 64, 65, 128, 129, 257) for N in (30000, 34816)] +
+                         [(40, 151936, 128), (65, 151936, 128), (257, 17408, 272), (256, 32768, 128), (513, 17410, 128),
+                          (33000, 64, 144), (33000, 130, 128)])
+def test_matmul_few_rows_of_wide_weights(gq, M, N, K, out):
+    """Tiles that the rows, or the columns, fill in part, on both sides of each rule."""
+    matmul_case(gq, M, N, K, out)
