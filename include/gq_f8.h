@@ -18,9 +18,20 @@
  * neighbouring rows are neighbours in memory.  gq_f8_quant and
  * gq_f8_glu_quant write this form.
  *
- * K is a multiple of 16 (rows of bytes start 16-byte aligned) and at most
- * 4,194,304 everywhere, N at most 268,435,200.  A NaN weight, activation or scale makes the outputs
- * that read it NaN; nothing else is affected by it.
+ * Sizes.  K is a multiple of 16 (rows of bytes start 16-byte aligned) and at
+ * most 4,194,304 everywhere, as is the row stride ldx of the products of two
+ * 8-bit operands; N at most 268,435,200; rows (M) at most 2,147,483,392; an
+ * operand at most 2^40 elements (GQ_ERR_SHAPE beyond).
+ *
+ * Range.  The sum over a block of 128 inputs is formed before its scales meet
+ * it, and the two scales of a product are multiplied first, in fp32.  The
+ * accuracies below hold for vectors (gq_f8_matvec) of zeros and values from
+ * 2^-94 up to below 2^112, and for pairs of scales whose product is a normal
+ * fp32 number; beyond, a result may be an infinity, NaN or zero where the exact
+ * one is a number.
+ *
+ * A NaN weight, activation or scale makes the outputs that read it NaN; nothing
+ * else is affected by it.
  */
 #ifndef GQ_F8_H
 #define GQ_F8_H
@@ -48,8 +59,8 @@ gq_status gq_f8_quant(const void* x, gq_dtype x_dtype, int64_t M, int64_t K, int
 /* The gated unit's elementwise step straight to 8 bits: gq_f8_quant of
  *   h[m][k] = act(g[m][k]) * u[m][k]
  * computed in fp32 and not rounded in between (act as gq_matvec_glu's; h within
- * 2^-20 |h| + 2^-125 |g u|, with the tanh form within 2^-20 (|h| + |g u|)).  g, u: [M][ldg],
- * [M][ldu] of dtype (the halves of one gate|up product, or two). */
+ * 2^-20 |h| + 2^-125 |g u|, with the tanh form within 2^-20 (|h| + |g u|)).
+ * g, u: [M][ldg], [M][ldu] of dtype (the halves of one gate|up product, or two). */
 gq_status gq_f8_glu_quant(const void* g, const void* u, gq_dtype dtype, int64_t M, int64_t K, int64_t ldg,
                           int64_t ldu, gq_act act, int32_t pow2, void* q, int64_t ldq, float* scales, int64_t s_ld,
                           hipStream_t stream);
@@ -58,12 +69,11 @@ gq_status gq_f8_glu_quant(const void* g, const void* u, gq_dtype dtype, int64_t 
  * vectors (GQ_ERR_UNSUPPORTED above).  x: [batch][K] of x_dtype (GQ_F32 or
  * GQ_BF16), not quantised; y: [batch][N] of y_dtype (GQ_F32 or GQ_BF16).
  * N == 0 is a no-op; K == 0 writes zeros.
- * Accuracy: weights and activations enter exactly (fp32 ones as three bf16
- * parts; what of a value lies below 2^-126 is lost), products are exact and
- * sums fp32: within (K / 128 + 162) * 2^-23 times sum |w x| (fp32 vectors:
- * K / 128 + 418, their parts being three sums), then y_dtype's rounding.  An
- * infinite activation gives NaN or an infinity.  Each vector's result does not
- * depend on the other vectors' values. */
+ * Accuracy: weights and activations enter exactly (fp32 ones, from two vectors
+ * on, as three bf16 parts), products are exact and sums fp32: within (K / 128 +
+ * 162) * 2^-23 times sum |w x| (fp32 vectors: K / 128 + 418, their parts being
+ * three sums), then y_dtype's rounding.  An infinite activation gives NaN or an
+ * infinity.  Each vector's result does not depend on the other vectors' values. */
 gq_status gq_f8_matvec(const void* W, const float* wscales, int64_t N, int64_t K, const void* x, gq_dtype x_dtype,
                        int32_t batch, void* y, gq_dtype y_dtype, hipStream_t stream);
 

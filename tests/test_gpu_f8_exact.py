@@ -185,3 +185,39 @@ def test_gated_rows_past_4_gib(gq):
         gated_near("gelu_tanh", g[rows], u[rows], q[rows], s[:, rows])
     del g, u, q, s
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("xdt", ["f32", "bf16"])
+def test_vectors_at_the_ends_of_their_range(gq, xdt):
+    """Vectors just below 2^112 and from 2^-94 on, with scales that bring them back."""
+    g = np.random.default_rng(11)
+    N, K = 130, 400
+    for B in (1, 3, 16):
+        q, s = P.weights(g, N, K)
+        for e in (111, -94):
+            x = dev(((1 + 0.999 * g.random((B, K))) * 2.0 ** e).astype(np.float32))
+            x = x.to(DT[xdt]).clamp(max=2.0 ** (e + 1) * (1 - 2.0 ** -8))
+            se = (s * 2.0 ** -e).astype(np.float32)
+            y = torch.full((B, N), float("nan"), device="cuda")
+            gq.gq_f8_matvec(dev(q), dev(se), x, y)
+            ref, mag = P.product(x.double().cpu().numpy(), P.wide_w(q, se))
+            tol = P.bound(ref, mag, K, torch.float32, 256 * 2.0 ** -23 if xdt == "f32" else 0.0)
+            assert (np.abs(y.double().cpu().numpy() - ref) <= tol).all(), (B, e)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(5, 130, 400), (150, 17000, 144), (300, 9000, 256)])
+def test_scales_at_the_ends_of_their_range(gq, M, N, K, out):
+    """Pairs of scales whose product is the smallest normal number, and 2^100 of very different factors."""
+    q, s, xq, xs = exact_case(np.random.default_rng([M, N]), M, N, K)
+    for ew, ex in ((-62, -62), (120, -20), (-20, 120)):
+        sw, sx = (s * 2.0 ** ew).astype(np.float32), (xs * 2.0 ** ex).astype(np.float32)
+        Y = torch.full((M, N), float("nan"), dtype=DT[out], device="cuda")
+        gq.gq_f8_matmul(dev(q), dev(sw), dev(xq), dev(sx), Y)
+        x, w = P.wide_x(xq, sx), P.wide_w(q, sw)
+        ref, mag = P.product(x, w)
+        if out == "f32":  # (as without the factors)
+            assert np.array_equal(Y.double().cpu().numpy(), ref)
+        else:
+            tol = P.bound8(ref, mag, P.floored(xq, x) @ P.floored(q, w).T, K, DT[out])
+            assert (np.abs(Y.double().cpu().numpy() - ref) <= tol).all()
