@@ -289,7 +289,8 @@ __device__ __forceinline__ int xcd_order(int id, int total) {
 // 5120, three whole rounds, 248 us): the copies alone take 228 us (8.8 TB/s from
 // the L2s; 150 us if all of them hit), the products with the scaling 192 us,
 // the matrix instructions alone 154 us.  Reading each line ahead into the L2
-// cost more than it gave (262-285 us).  Measured: 3015 x 17408 x 5120 in 262-271
+// cost more than it gave (262-285 us).  The L2s fetch 4.4 times the operands'
+// bytes for 3015 x 17408 x 5120.  Measured: that in 262-271
 // us (1.98-2.05 PFLOP/s; a vendor's product with one scale for each operand
 // takes 268-276 us), 8100 x 8192 x 8192 in 482 us (2.26 PFLOP/s).
 //
@@ -620,11 +621,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_tile_id(const uint8_t* __re
 // neighbouring columns), the chunks swizzled as there.  A panel's results are
 // stored behind the next barrier, ahead of the next copies, so that no wait is for
 // a store just made.
-// 3015 x 8 slots of 128 experts, 2816 x 704: 112 us (128 x 128 tiles: 148 us); 82
-// without the copies, 90 without the stores, and 22 for two starts one after the
-// other.  X through LDS in whole lines starts sooner but holds the panels up (146
-// against 147 us a call, other shapes 8% less to 6% more); whole rows of a panel
-// one after another, of odd stride, have bank conflicts (147 against 146 us).
+// 3015 x 8 slots of 128 experts, 2816 x 704: 117 us in the median of a trace, 113
+// at least (128 x 128 tiles: 148 us); of these 113, 82 are left without the copies,
+// 90 without the stores, and 22 are two starts one after the other.  It fetches 1.2
+// times its operands' bytes.  X through LDS in whole lines starts sooner but holds
+// the panels up (146 against 147 us a call, other shapes 8% less to 6% more); whole
+// rows of a panel one after another, of odd stride, have bank conflicts (147 against
+// 146 us).  6 blocks take 208 registers and 72 KB of LDS, so that two workgroups run
+// on a CU; 8 would take 96 KB and more than 256 registers.
 constexpr int PANELS = 3;
 
 template <int KB, int WV>
@@ -796,7 +800,8 @@ __global__ __launch_bounds__(64 * WV) void k_f8_stream(const uint8_t* __restrict
 // 8 slots of 2816 bf16 in 23 us (6.6 TB/s, part of it still in the caches; 125
 // us one element a thread).  Slots are held in the result's type: with bf16
 // each is rounded once before the sum, which adds to the result's own rounding
-// (together 1.35 times its error), and halves the bytes that bound this.
+// (together 1.41 times its error: 0.0023 against 0.0017 of the result's size), and
+// halves the bytes that bound this.
 template <typename TY, int V>
 __global__ __launch_bounds__(256) void k_f8_combine(const TY* __restrict__ slots, const int* __restrict__ slot_e,
                                                     const float* __restrict__ rw, int top_k, int64_t N,
@@ -901,10 +906,10 @@ hipError_t tile_id(const Call<TY>& c, int64_t gm) {
 
 // n_tiles: the tiles that are likely.  About 4 workgroups of four wavefronts a CU
 // (two run at once), or one of eight; each loads its rows of X first, so none has
-// fewer than 3 panels (2816 x 704, 188 slots for each of 128 experts: 154, 156 and
-// 161 us with 1000, 2000 and 500 workgroups; 2816 x 768, 754 for each of 16: 61
-// and 67 us with 200 and 400 of eight; 704 x 640, 377 for each of 16: 20 and 24 us
-// with 3 and 6 panels each).
+// fewer than 3 panels (weighted 2816 x 704, 188 slots for each of 128 experts: 154,
+// 146 and 146 us with 500, 1000 and 2000 workgroups; 2816 x 768, 754 for each of
+// 16: 85, 61 and 64 us with 130, 260 and 510 of eight; 704 x 640, 377 for each of
+// 16: 23.4 and 24.0 us with at least 3 and 6 panels each).
 template <int KB, int WV>
 hipError_t short_id(const Call<uint16_t>& c, int64_t gm, int64_t n_tiles) {
     const int64_t gn = (c.N + 31) / 32, groups = gqk_cu_count() * (WV == 4 ? 4 : 1);
@@ -927,14 +932,14 @@ hipError_t short_id(const Call<uint16_t>& c, int64_t gm, int64_t n_tiles) {
 // Which kernel: measured at N x K of 1024 x 2560, 5120 x 5120, 2560 x 9728 and
 // 17408 x 5120, 16 to 2048 rows, and at N of 20,480 to 151,936, 17 to 769 rows.
 // What decides is how many tiles there are for the CUs.  Few 64 x 128 tiles: the
-// stream kernel, which splits K (256 rows of 2560 x 9728: 15.8 us against 31.6 us
+// stream kernel, which splits K (256 rows of 2560 x 9728: 15.4 us against 30.6 us
 // in tiles).  Up to one a CU: those tiles, eight wavefronts each and four blocks
-// ahead (2048 rows of 1024 x 2560: 11.6 against 14.8 us two blocks ahead, 19.9 us
+// ahead (2048 rows of 1024 x 2560: 11.6 against 14.6 us two blocks ahead, 19.6 us
 // streamed); up to one 128 x 128 tile a CU: those in the same way (512 rows of
-// 5120 x 5120: 28.8 against 32.6 us); then two of these a CU, two blocks ahead
-// (2048 rows of 2560 x 9728: 72.3 against 93.1 us).
+// 5120 x 5120: 28.9 against 32.5 us); then two of these a CU, two blocks ahead
+// (2048 rows of 2560 x 9728: 72.4 against 93.0 us).
 // 256 x 256 tiles where they fill half of the CUs (2048 rows of 5120 x 5120: 70.3
-// against 73.2 us, of 17408 x 5120: 225 against 243 us), 128 x 128 ones take more
+// against 72.7 us, of 17408 x 5120: 190 against 242 us), 128 x 128 ones take more
 // than one round (256 rows of 32768 x 5120: 93.0 against 73.9 us) and at most a
 // quarter of what they cover is padding that smaller ones do not have (257 rows of
 // 17408 x 5120: 69.5 against 46.7 us, 128 of 34816 x 5120 74.4 against 72.4, 60000
@@ -946,7 +951,7 @@ hipError_t short_id(const Call<uint16_t>& c, int64_t gm, int64_t n_tiles) {
 // the stream kernel, which reads W once for them (32 of 34816 x 5120: 44.9 against
 // 51.0 us).
 // An fp32 result's products run at half the rate, which favours the stream kernel
-// longer (512 rows of 2560 x 9728: 37.3 against 53.8 us; not with 33 to 64 rows, for
+// longer (512 rows of 2560 x 9728: 35.9 against 53.9 us; not with 33 to 64 rows, for
 // which it reads W twice: 64 of 151,936 x 5120 356 against 196 us) and leaves 256 x
 // 256 without registers.
 template <typename TY>
@@ -988,11 +993,20 @@ hipError_t matmul_rows(Call<TY> c) {
     return hipSuccess;
 }
 
-// Measured at 64 experts of 1408 x 2816 and 2816 x 704 by the slots an expert
-// has on average: 16 slots a tile up to 8 (4 each: 45 us against 56 us with
-// 64), 64 up to 48 (24 each: 63 against 77 and 65 us with 16 and 128),
-// 128 up to 320 (256 each: 134 against 160 and 137 us with 64 and 256), 256
-// above (375 each: 158 against 184 us).
+// The slots of a tile, by those that an expert has on average (the experts'
+// popularity as of normal logits); the table serves every product of a layer, so N,
+// K and the type do not count.  us a call at 16, 64, 128 and 256 slots a tile, bf16:
+//   64 experts        1408 x 2816              2816 x 704
+//     8 slots each     45   43   44   73        27   28   33   35
+//    24                66   48   57   77        39   33   34   41
+//    48                92   67   61   81        59   40   38   55
+//   128               215  107  113   96       123   54   47   71
+//   320               480  192  179  151       278  107   74   84
+//   400               587  230  197  186       375  149  111  154
+//   750              1056  388  323  284       733  266  213  194
+// The borders are compromises: 320 slots of long rows would take 256 to a tile, 400
+// of short ones 128, and an fp32 result, whose tiles of 256 have 128 columns, 128
+// throughout (64 experts of 1408 x 2816, 400 slots: 285 against 304 us).
 int tile_rows(int64_t S, int n_experts) {
     const int64_t E = n_experts;
     return S <= 8 * E ? 16 : S <= 48 * E ? 64 : S <= 320 * E ? 128 : 256;

@@ -18,7 +18,9 @@
 // wait in LDS for the places that take them.
 // Bound by latency: T x E logits are a few megabytes at most.  Measured: one
 // token of 256 experts in 8 groups 5.2 us, 3015 tokens of 128 experts 6.1 us (6.2
-// and 8.1 with 64-bit maxima and the chosen scores computed again).
+// and 8.1 with 64-bit maxima and the chosen scores computed again).  Above 1024
+// experts a lane holds 64, whose scores fill the registers of a SIMD: one wavefront
+// each, one token of 2048 experts 35 us, 3015 of them 122 us (1024: 10.5 and 25 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
