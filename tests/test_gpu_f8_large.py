@@ -99,3 +99,59 @@ def test_quantised_rows(gq):
         # every row but the last three is the first one
         assert torch.equal(q[:-3], q[:1].expand(M - 3, K)) and torch.equal(s[:, :-3], s[:, :1].expand(-1, M - 3))
         assert torch.equal(q[-1], q[-2]) and torch.equal(s[:, -1], s[:, -3]) and (s[:, -1] > s[:, 0]).all()
+
+
+def chosen(W, s, X, xs, n, m):
+    """Plain products of rows m of X and rows n of W."""
+    q, xq = W[n].cpu().numpy(), X[m].cpu().numpy()
+    w = P.decode(q) * np.repeat(s[torch.as_tensor(n, device=s.device) // 128].double().cpu().numpy(), 128, 1)[:, :q.shape[1]]
+    if xs is None:
+        return P.product(xq.astype(np.float64), w)
+    x = P.wide_x(xq, xs[:, m].cpu().numpy())
+    return (*P.product(x, w), P.floored(xq, x) @ P.floored(q, w).T)
+
+
+def test_longest_rows(gq):
+    """K of 4,194,304, the most there may be: every kind of kernel, at its last rows and columns."""
+    K, N = 1 << 22, 300
+    W = bytes_of(N, K)
+    s = torch.rand(3, K // 128, device="cuda") * 1e-3
+    n = [0, 127, 128, 255, 257, 299]
+    r = torch.Generator(device="cuda").manual_seed(3)
+    for xdt, B in (("f32", 1), ("bf16", 1), ("f32", 5), ("bf16", 16)):
+        x = torch.randn(B, K, device="cuda", generator=r).to(DT[xdt])
+        y = torch.full((B, N), float("nan"), device="cuda")
+        gq.gq_f8_matvec(W, s, x, y)
+        ref, mag = chosen(W, s, x.float(), None, n, [0, B - 1])
+        near(y[[0, B - 1]][:, n], ref, P.bound(ref, mag, K, torch.float32, 256 * 2.0 ** -23 if xdt == "f32" else 0.0))
+        assert torch.isfinite(y).all()
+    X = bytes_of(520, K)
+    xs = torch.rand(K // 128, 520, device="cuda", generator=r) * 1e-3
+    for M, out in ((7, "f32"), (40, "bf16"), (520, "bf16"), (300, "f32")):
+        Y = torch.full((M, N), float("nan"), dtype=DT[out], device="cuda")
+        gq.gq_f8_matmul(W, s, X[:M], xs[:, :M], Y)
+        m = [0, M // 2, M - 1]
+        ref, mag, mag8 = chosen(W, s, X, xs, n, m)
+        near(Y[m][:, n], ref, P.bound8(ref, mag, mag8, K, DT[out]))
+        assert torch.isfinite(Y).all()
+    # one expert; few slots, tiles of 64 and 128, and rows that span more than 2^31 bytes
+    for T, out in ((5, "f32"), (40, "bf16"), (300, "f32"), (520, "bf16")):
+        ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+        ws = torch.full((gq.gq_f8_matmul_id_workspace(1, T, 1, N, DT[out], False),), 0xAB, dtype=torch.uint8,
+                        device="cuda")
+        Y = torch.full((T, 1, N), float("nan"), dtype=DT[out], device="cuda")
+        gq.gq_f8_matmul_id(W[None], s[None], ids, X[:T], xs[:, :T], Y, ws)
+        m = [0, T // 2, T - 1]
+        ref, mag, mag8 = chosen(W, s, X, xs, n, m)
+        near(Y[m][:, 0, n], ref, P.bound8(ref, mag, mag8, K, DT[out]))
+        assert torch.isfinite(Y).all()
+    # tiles of columns by the hundred, few rows
+    del W, s
+    N = 17_000
+    W, s = bytes_of(N, K), torch.rand((N + 127) // 128, K // 128, device="cuda", generator=r) * 1e-3
+    Y = torch.full((520, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    gq.gq_f8_matmul(W, s, X, xs, Y)
+    n, m = [0, 8191, N - 1], [0, 511, 519]
+    ref, mag, mag8 = chosen(W, s, X, xs, n, m)
+    near(Y[m][:, n], ref, P.bound8(ref, mag, mag8, K, torch.bfloat16))
+    assert torch.isfinite(Y).all()
