@@ -155,3 +155,38 @@ def test_longest_rows(gq):
     ref, mag, mag8 = chosen(W, s, X, xs, n, m)
     near(Y[m][:, n], ref, P.bound8(ref, mag, mag8, K, torch.bfloat16))
     assert torch.isfinite(Y).all()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_more_rows_than_the_quantisers_grid(gq, gated):
+    """Nine million rows of 48: a workgroup comes round to a second set of rows."""
+    M, K = 9_000_001, 48
+    x = torch.empty(M, K, dtype=torch.float16, device="cuda")
+    x.copy_(torch.randn(997, K, device="cuda", generator=torch.Generator(device="cuda").manual_seed(4)).half()
+            .repeat(M // 997 + 1, 1)[:M])
+    q, s = torch.zeros(M, K, dtype=torch.uint8, device="cuda"), torch.zeros(1, M, device="cuda")
+    if gated:
+        gq.gq_f8_glu_quant(x, x, "silu", q, s)
+    else:
+        gq.gq_f8_quant(x, q, s)
+        rq, rs = P.quant(x[:997].float().cpu().numpy(), False)
+        assert np.array_equal(s[:, :997].cpu().numpy(), rs)
+        assert np.array_equal(P.decode(q[:997].cpu().numpy()), P.decode(rq))
+    whole = M // 997 * 997  # every 997 rows are the first 997 again
+    assert torch.equal(q[:whole].view(-1, 997, K), q[:997].expand(whole // 997, 997, K))
+    assert torch.equal(s[0, :whole].view(-1, 997), s[:, :997].expand(whole // 997, 997))
+    assert torch.equal(q[whole:], q[:M - whole]) and torch.equal(s[:, whole:], s[:, :M - whole])
+    assert (s > 0).all()
+
+
+def test_the_most_tokens_of_the_router(gq):
+    T, E = 1 << 25, 5
+    l = torch.randn(T, E, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    ids = torch.full((T, 1), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, 1), -7.0, device="cuda")
+    gq.gq_route_scored(l, 1, ids, w, renorm=False)
+    assert (ids >= 0).all() and (ids < E).all()
+    assert torch.equal(l.gather(1, ids.long()), l.amax(1, keepdim=True))
+    some = slice(T - 1000, T)
+    want = torch.softmax(l[some].double(), 1).amax(1, keepdim=True)
+    assert ((w[some].double() - want).abs() <= (2.0 ** -24 + 2.0 ** -40) * want).all()
