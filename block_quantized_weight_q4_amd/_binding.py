@@ -62,6 +62,16 @@ if hasattr(_lib, "gq_f8_quant"):  # gq_f8.h
     _lib.gq_f8_matmul_id_check.argtypes = [P, P, ctypes.POINTER(I32)]
     _lib.gq_route_scored.argtypes = [P, ctypes.c_int, I32, I32, I32, ctypes.c_int, P, I32, I32, ctypes.c_int, I32,
                                      ctypes.c_float, P, P, P]
+if hasattr(_lib, "gq_g4_matvec"):  # gq_g4.h
+    _lib.gq_g4_matvec.argtypes = [P, P, ctypes.c_int, P, I32, I64, I64, P, ctypes.c_int, I32, P, ctypes.c_int, P]
+    _lib.gq_g4_matmul.argtypes = [P, P, ctypes.c_int, P, I32, I64, I64, P, ctypes.c_int, I64, I64, P, ctypes.c_int, I64,
+                                  I32, P, P]
+    _lib.gq_g4_matmul_dx.argtypes = [P, P, ctypes.c_int, P, I32, I64, I64, P, ctypes.c_int, I64, I64, P, I64, I32, P, P]
+if hasattr(_lib, "gq_expert_sort"):  # gq_expert.h
+    _lib.gq_expert_sort.argtypes = [P, I32, I32, I32, P, P, P]
+    _lib.gq_expert_gather.argtypes = [P, ctypes.c_int, I32, I32, I64, I64, P, P, I64, P]
+    _lib.gq_expert_combine.argtypes = [P, ctypes.c_int, I32, I32, I64, I64, P, P, P, ctypes.c_int, I64, P]
+    _lib.gq_expert_combine_grad.argtypes = [P, ctypes.c_int, I32, I32, I64, I64, P, I64, P, P, P, I64, P, P]
 ACTS = {"silu": 0, "gelu_tanh": 1}
 SCORES = {"softmax": 0, "sigmoid": 1}
 GROUP_RANKS = {"max": 0, "top2": 1}
@@ -69,7 +79,8 @@ for _f in ("gq_block_info", "gq_dequant", "gq_matvec", "gq_matvec_id_workspace",
            "gq_matvec_id_check", "gq_matmul", "gq_route_topk", "gq_route_topk_plan", "gq_matvec_glu",
            "gq_matvec_id_glu", "gq_route_matvec_id_glu", "gq_f8_quant", "gq_f8_glu_quant", "gq_f8_matvec",
            "gq_f8_matmul", "gq_f8_matmul_id_workspace", "gq_f8_matmul_id", "gq_f8_matmul_id_check",
-           "gq_route_scored"):
+           "gq_route_scored", "gq_g4_matvec", "gq_g4_matmul", "gq_g4_matmul_dx", "gq_expert_sort",
+           "gq_expert_gather", "gq_expert_combine", "gq_expert_combine_grad"):
     if hasattr(_lib, _f):
         getattr(_lib, _f).restype = ctypes.c_int
 
@@ -755,6 +766,284 @@ def gq_route_scored(logits: torch.Tensor, top_k: int, ids: torch.Tensor, weights
             n_experts, top_k, SCORES[score], None if bias is None else bias.data_ptr(), n_groups, top_groups,
             GROUP_RANKS[group_rank], renorm, scale, ids.data_ptr(), weights.data_ptr())
     return ids, weights
+
+
+# --- products with 4-bit weights and group scales (gq_g4.h) -------------------
+# As above: sizes from the shapes, one short test first.
+
+_HALF = (torch.bfloat16, torch.float16)
+_GROUPS = (32, 64, 128)
+
+
+def _check_g4_weights(W, scales, zeros, group: int, dims: int) -> None:
+    _tensor("W", W, _U8)
+    _need(W.dim() == dims, "W must be %d-D" % dims)
+    _need(group in _GROUPS, "group must be one of %s" % list(_GROUPS))
+    *lead, half = W.shape
+    _tensor("scales", scales, _HALF)
+    _shape("scales", scales, *lead, (2 * half + group - 1) // group)
+    if zeros is not None:
+        _tensor("zeros", zeros, _U8)
+        _shape("zeros", zeros, *scales.shape)
+        _contig("zeros", zeros)
+    _contig("W", W)
+    _contig("scales", scales)
+
+
+def _check_g4_matvec(W, scales, x, y, zeros, group) -> None:
+    _check_g4_weights(W, scales, zeros, group, 2)
+    N, half = W.shape
+    _tensor("x", x, _HALF_OR_F32)
+    _tensor("y", y, _HALF_OR_F32)
+    _need(x.dim() == 2 and x.shape[1] == 2 * half, "x must be [batch][%d]" % (2 * half))
+    _shape("y", y, x.shape[0], N)
+    _contig("x", x)
+    _contig("y", y)
+    _one_device(W=W, scales=scales, zeros=zeros, x=x, y=y)
+
+
+def gq_g4_matvec(W: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
+                 zeros: torch.Tensor | None = None, group: int = 128, stream=None) -> torch.Tensor:
+    """y [batch][N] = x [batch][K] (each fp32 / bf16 / fp16) times the 4-bit
+    weights W [N][K / 2] (uint8) with scales [N][ceil(K / group)] (bf16 / fp16)
+    and zero points of the same shape (uint8; None: 8)."""
+    try:
+        (N, half), d, batch = W.shape, W.get_device(), x.shape[0]
+        K = 2 * half
+        ok = (d >= 0 and d == scales.get_device() == x.get_device() == y.get_device() and W.dtype is _u8 and
+              scales.dtype in _HALF and x.dtype in _HALF_OR_F32 and y.dtype in _HALF_OR_F32 and group in _GROUPS and
+              scales.shape == (N, (K + group - 1) // group) and x.shape == (batch, K) and y.shape == (batch, N) and
+              W.is_contiguous() and scales.is_contiguous() and x.is_contiguous() and y.is_contiguous() and
+              (zeros is None or (zeros.dtype is _u8 and zeros.get_device() == d and zeros.shape == scales.shape and
+                                 zeros.is_contiguous())))
+    except (AttributeError, ValueError, IndexError, TypeError):
+        ok = False
+    if not ok:
+        _check_g4_matvec(W, scales, x, y, zeros, group)
+    _launch("gq_g4_matvec", _lib.gq_g4_matvec, d, stream, W.data_ptr(), scales.data_ptr(), _DTYPES[scales.dtype],
+            None if zeros is None else zeros.data_ptr(), group, N, K, x.data_ptr(), _DTYPES[x.dtype], batch,
+            y.data_ptr(), _DTYPES[y.dtype])
+    return y
+
+
+def _check_g4_rows(W, scales, zeros, group, offsets, x_name, x, x_width, y_name, y, y_width, y_dtypes) -> None:
+    _check_g4_weights(W, scales, zeros, group, 2 if offsets is None else 3)
+    if offsets is not None:
+        _tensor("offsets", offsets, _I32)
+        _shape("offsets", offsets, W.shape[0] + 1)
+        _contig("offsets", offsets)
+    _tensor(x_name, x, _HALF)
+    _f8_rows(x_name, x)
+    _need(x.shape[1] == x_width(), "%s must have rows of %d" % (x_name, x_width()))
+    _tensor(y_name, y, y_dtypes(x.dtype))
+    _f8_rows(y_name, y)
+    _shape(y_name, y, x.shape[0], y_width())
+    _one_device(**{"W": W, "scales": scales, "zeros": zeros, "offsets": offsets, x_name: x, y_name: y})
+
+
+def _g4_rows(fn, W, scales, x, y, zeros, group, offsets, grad, stream) -> torch.Tensor:
+    """gq_g4_matmul, or with grad gq_g4_matmul_dx."""
+    try:
+        lead, d, M = W.shape[:-2], W.get_device(), x.shape[0]
+        N, K = W.shape[-2], 2 * W.shape[-1]
+        x_width, y_width = (N, K) if grad else (K, N)
+        (ldx, x1), (ldy, y1) = x.stride(), y.stride()
+        ok = (d >= 0 and d == scales.get_device() == x.get_device() == y.get_device() and W.dtype is _u8 and
+              scales.dtype in _HALF and x.dtype in _HALF and
+              (y.dtype is x.dtype or (not grad and y.dtype is _f32)) and group in _GROUPS and
+              scales.shape == (*lead, N, (K + group - 1) // group) and x.shape == (M, x_width) and
+              y.shape == (M, y_width) and x1 == y1 == 1 and W.is_contiguous() and scales.is_contiguous() and
+              (len(lead) == 0 if offsets is None else
+               len(lead) == 1 and offsets.dtype is _i32 and offsets.shape == (lead[0] + 1,) and
+               offsets.get_device() == d and offsets.is_contiguous()) and
+              (zeros is None or (zeros.dtype is _u8 and zeros.get_device() == d and zeros.shape == scales.shape and
+                                 zeros.is_contiguous())))
+    except (AttributeError, ValueError, IndexError, TypeError):
+        ok = False
+    if not ok:
+        _check_g4_rows(W, scales, zeros, group, offsets, "dY" if grad else "X", x,
+                       lambda: W.shape[-2] if grad else 2 * W.shape[-1], "dX" if grad else "Y", y,
+                       lambda: 2 * W.shape[-1] if grad else W.shape[-2],
+                       lambda t: (t,) if grad else (torch.float32, t))
+    one = M <= 1  # (a single row's stride says nothing)
+    tail = (y.data_ptr(), K if one else ldy) if grad else (y.data_ptr(), _DTYPES[y.dtype], N if one else ldy)
+    _launch(fn, getattr(_lib, fn), d, stream, W.data_ptr(), scales.data_ptr(), _DTYPES[scales.dtype],
+            None if zeros is None else zeros.data_ptr(), group, N, K, x.data_ptr(), _DTYPES[x.dtype], M,
+            x_width if one else ldx, *tail, lead[0] if lead else 1, None if offsets is None else offsets.data_ptr())
+    return y
+
+
+def gq_g4_matmul(W: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, Y: torch.Tensor,
+                 zeros: torch.Tensor | None = None, group: int = 128, offsets: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Y [M][N] (fp32 or X's type) = X [M][K] (bf16 / fp16) times the weights of
+    gq_g4_matvec; with offsets (int32 [E + 1]) W is [E][N][K / 2], and the rows
+    offsets[e] .. offsets[e + 1] - 1 of X meet the weights of expert e."""
+    return _g4_rows("gq_g4_matmul", W, scales, X, Y, zeros, group, offsets, False, stream)
+
+
+def gq_g4_matmul_dx(W: torch.Tensor, scales: torch.Tensor, dY: torch.Tensor, dX: torch.Tensor,
+                    zeros: torch.Tensor | None = None, group: int = 128, offsets: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """dX [M][K] of dY [M][N] (both bf16 or both fp16): the gradient of
+    gq_g4_matmul with respect to X."""
+    return _g4_rows("gq_g4_matmul_dx", W, scales, dY, dX, zeros, group, offsets, True, stream)
+
+
+# --- tokens sorted by expert and back (gq_expert.h) ---------------------------
+
+def _check_expert_sort(ids, n_experts, offsets, place) -> None:
+    T, k = _ids(ids)
+    _tensor("offsets", offsets, _I32)
+    _shape("offsets", offsets, n_experts + 1)
+    _contig("offsets", offsets)
+    _tensor("place", place, _I32)
+    _shape("place", place, T, k)
+    _contig("place", place)
+    _one_device(ids=ids, offsets=offsets, place=place)
+
+
+def gq_expert_sort(ids: torch.Tensor, n_experts: int, offsets: torch.Tensor, place: torch.Tensor,
+                   stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """offsets [n_experts + 1] and place [n_tokens][top_k] (int32) of ids
+    [n_tokens][top_k]: the slots ordered by expert; place -1 for an invalid id."""
+    try:
+        (T, k), d = ids.shape, ids.get_device()
+        ok = (d >= 0 and d == offsets.get_device() == place.get_device() and ids.dtype is _i32 and
+              offsets.dtype is _i32 and place.dtype is _i32 and offsets.shape == (n_experts + 1,) and
+              place.shape == (T, k) and ids.is_contiguous() and offsets.is_contiguous() and place.is_contiguous())
+    except (AttributeError, ValueError, TypeError):
+        ok = False
+    if not ok:
+        _check_expert_sort(ids, n_experts, offsets, place)
+    _launch("gq_expert_sort", _lib.gq_expert_sort, d, stream, ids.data_ptr(), T, k, n_experts, offsets.data_ptr(),
+            place.data_ptr())
+    return offsets, place
+
+
+def _check_place(place) -> tuple[int, int]:
+    _tensor("place", place, _I32)
+    _need(place.dim() == 2, "place must be [n_tokens][top_k]")
+    _contig("place", place)
+    return place.shape[0], place.shape[1]
+
+
+def _check_expert_weights(name, w, T, k) -> None:
+    if w is not None:
+        _tensor(name, w, _F32)
+        _shape(name, w, T, k)
+        _contig(name, w)
+
+
+def _check_expert_rows(name, t, dtypes, rows, D) -> None:
+    _tensor(name, t, dtypes)
+    _f8_rows(name, t)
+    _shape(name, t, rows, D)
+
+
+def _check_expert_gather(x, place, xs) -> None:
+    T, k = _check_place(place)
+    _tensor("x", x, _HALF_OR_F32)
+    _f8_rows("x", x)
+    _need(x.shape[0] == T, "x must have n_tokens = %d rows" % T)
+    _check_expert_rows("xs", xs, (x.dtype,), T * k, x.shape[1])
+    _one_device(x=x, place=place, xs=xs)
+
+
+def gq_expert_gather(x: torch.Tensor, place: torch.Tensor, xs: torch.Tensor, stream=None) -> torch.Tensor:
+    """xs[place[t][j]] = x[t]: x [n_tokens][D], xs [n_tokens * top_k][D] of one
+    type; rows of xs that no slot has are left as they were."""
+    try:
+        (T, k), D, d = place.shape, x.shape[1], place.get_device()
+        (ldx, x1), (ldxs, xs1) = x.stride(), xs.stride()
+        ok = (d >= 0 and d == x.get_device() == xs.get_device() and place.dtype is _i32 and
+              x.dtype in _HALF_OR_F32 and xs.dtype is x.dtype and x.shape == (T, D) and xs.shape == (T * k, D) and
+              x1 == xs1 == 1 and place.is_contiguous())
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _check_expert_gather(x, place, xs)
+    _launch("gq_expert_gather", _lib.gq_expert_gather, d, stream, x.data_ptr(), _DTYPES[x.dtype], T, k, D,
+            D if T <= 1 else ldx, place.data_ptr(), xs.data_ptr(), D if T * k <= 1 else ldxs)
+    return xs
+
+
+def _check_expert_combine(ys, place, y, weights) -> None:
+    T, k = _check_place(place)
+    _tensor("ys", ys, _HALF_OR_F32)
+    _f8_rows("ys", ys)
+    _need(ys.shape[0] == T * k, "ys must have n_tokens * top_k = %d rows" % (T * k))
+    _check_expert_rows("y", y, (torch.float32, ys.dtype), T, ys.shape[1])
+    _check_expert_weights("weights", weights, T, k)
+    _one_device(ys=ys, place=place, y=y, weights=weights)
+
+
+def gq_expert_combine(ys: torch.Tensor, place: torch.Tensor, y: torch.Tensor, weights: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """y[t] = sum_j weights[t][j] * ys[place[t][j]]: ys [n_tokens * top_k][D], y
+    [n_tokens][D] (fp32 or ys' type); weights None: 1 (gq_expert_gather's gradient)."""
+    try:
+        (T, k), D, d = place.shape, ys.shape[1], place.get_device()
+        (ldys, ys1), (ldy, y1) = ys.stride(), y.stride()
+        ok = (d >= 0 and d == ys.get_device() == y.get_device() and place.dtype is _i32 and
+              ys.dtype in _HALF_OR_F32 and (y.dtype is ys.dtype or y.dtype is _f32) and ys.shape == (T * k, D) and
+              y.shape == (T, D) and ys1 == y1 == 1 and place.is_contiguous() and
+              (weights is None or (weights.dtype is _f32 and weights.shape == (T, k) and
+                                   weights.get_device() == d and weights.is_contiguous())))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _check_expert_combine(ys, place, y, weights)
+    _launch("gq_expert_combine", _lib.gq_expert_combine, d, stream, ys.data_ptr(), _DTYPES[ys.dtype], T, k, D,
+            D if T * k <= 1 else ldys, place.data_ptr(), None if weights is None else weights.data_ptr(),
+            y.data_ptr(), _DTYPES[y.dtype], D if T <= 1 else ldy)
+    return y
+
+
+def _check_expert_combine_grad(dy, ys, place, dys, dweights, weights) -> None:
+    T, k = _check_place(place)
+    _tensor("dy", dy, _HALF_OR_F32)
+    _f8_rows("dy", dy)
+    _need(dy.shape[0] == T, "dy must have n_tokens = %d rows" % T)
+    for name, t in (("ys", ys), ("dys", dys)):
+        if t is not None:
+            _check_expert_rows(name, t, (dy.dtype,), T * k, dy.shape[1])
+    _need(dweights is None or ys is not None, "dweights needs ys")
+    _check_expert_weights("weights", weights, T, k)
+    _check_expert_weights("dweights", dweights, T, k)
+    _one_device(dy=dy, ys=ys, place=place, dys=dys, dweights=dweights, weights=weights)
+
+
+def gq_expert_combine_grad(dy: torch.Tensor, ys: torch.Tensor | None, place: torch.Tensor,
+                           dys: torch.Tensor | None, dweights: torch.Tensor | None,
+                           weights: torch.Tensor | None = None,
+                           stream=None) -> tuple[torch.Tensor | None, torch.Tensor | None]:
+    """dys[place[t][j]] = weights[t][j] * dy[t], dweights[t][j] = <dy[t],
+    ys[place[t][j]]> (fp32; 0 without a place): dy [n_tokens][D], ys and dys
+    [n_tokens * top_k][D] of one type; dys or dweights (with ys) may be None, and
+    dys may be ys."""
+    try:
+        (T, k), D, d = place.shape, dy.shape[1], place.get_device()
+        (lddy, s1), (ldys, s2) = dy.stride(), (D, 1) if ys is None else ys.stride()
+        lddys, s3 = (D, 1) if dys is None else dys.stride()
+        ok = (d >= 0 and d == dy.get_device() and place.dtype is _i32 and dy.dtype in _HALF_OR_F32 and
+              dy.shape == (T, D) and s1 == s2 == s3 == 1 and place.is_contiguous() and
+              (ys is None or (ys.dtype is dy.dtype and ys.shape == (T * k, D) and ys.get_device() == d)) and
+              (dys is None or (dys.dtype is dy.dtype and dys.shape == (T * k, D) and dys.get_device() == d)) and
+              (dweights is None or (ys is not None and dweights.dtype is _f32 and dweights.shape == (T, k) and
+                                    dweights.get_device() == d and dweights.is_contiguous())) and
+              (weights is None or (weights.dtype is _f32 and weights.shape == (T, k) and
+                                   weights.get_device() == d and weights.is_contiguous())))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _check_expert_combine_grad(dy, ys, place, dys, dweights, weights)
+    many = T * k > 1
+    _launch("gq_expert_combine_grad", _lib.gq_expert_combine_grad, d, stream, dy.data_ptr(), _DTYPES[dy.dtype], T, k, D,
+            lddy if T > 1 else D, None if ys is None else ys.data_ptr(), ldys if many else D, place.data_ptr(),
+            None if weights is None else weights.data_ptr(), None if dys is None else dys.data_ptr(),
+            lddys if many else D, None if dweights is None else dweights.data_ptr())
+    return dys, dweights
 
 
 # raw handle for the tests that check the exported symbols

@@ -1,0 +1,102 @@
+// gq_g4.hip -- products with 4-bit weights and group scales (gfx950): one
+// thread an output, sums over a group in fp32 before its scale meets them.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gq_device.h"
+#include "gq_g4_internal.h"
+
+namespace {
+
+__device__ __forceinline__ float to_f32(const void* p, int64_t i, int dtype) {
+    if (dtype == gqd::DT_F32) return static_cast<const float*>(p)[i];
+    const uint16_t u = static_cast<const uint16_t*>(p)[i];
+    return dtype == gqd::DT_BF16 ? gqd::bf2f(u) : gqd::h2f(u);
+}
+
+__device__ __forceinline__ void store_f32(void* p, int64_t i, int dtype, float v) {
+    if (dtype == gqd::DT_F32) static_cast<float*>(p)[i] = v;
+    else static_cast<uint16_t*>(p)[i] = dtype == gqd::DT_BF16 ? gqd::f2bf(v) : gqd::f2h(v);
+}
+
+__device__ __forceinline__ float scale_of(const G4Weights& w, int64_t i) {
+    return w.s_f16 ? gqd::h2f(w.scales[i]) : gqd::bf2f(w.scales[i]);
+}
+
+// Expert of row m, -1 if it has none; every index stays in range whatever offsets hold.
+__device__ __forceinline__ int expert_of(const int32_t* offsets, int n_experts, int64_t m) {
+    if (!offsets) return 0;
+    int lo = 0, hi = n_experts;  // the first e with offsets[e + 1] > m
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (offsets[mid + 1] > m) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo < n_experts && offsets[lo] <= m ? lo : -1;
+}
+
+__global__ __launch_bounds__(256) void k_g4_rows(G4Weights w, const void* __restrict__ X, int x_dtype, int64_t M,
+                                                 int64_t ldx, void* __restrict__ Y, int y_dtype, int64_t ldy,
+                                                 int n_experts, const int32_t* __restrict__ offsets) {
+    const int64_t groups = (w.K + w.group - 1) / w.group;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < M * w.N; i += gridDim.x * 256ll) {
+        const int64_t m = i / w.N, n = i % w.N;
+        const int e = expert_of(offsets, n_experts, m);
+        if (e < 0) continue;
+        const int64_t row = e * w.N + n;
+        float acc = 0.0f;
+        for (int64_t b = 0; b < groups; ++b) {
+            const int z = w.zeros ? w.zeros[row * groups + b] & 15 : 8;
+            float sum = 0.0f;
+            const int64_t end = (b + 1) * w.group < w.K ? (b + 1) * w.group : w.K;
+            for (int64_t k = b * w.group; k < end; ++k) {
+                const int q = (w.W[row * (w.K / 2) + k / 2] >> (4 * (k & 1))) & 15;
+                sum = __builtin_fmaf((float)(q - z), to_f32(X, m * ldx + k, x_dtype), sum);
+            }
+            acc = __builtin_fmaf(scale_of(w, row * groups + b), sum, acc);
+        }
+        store_f32(Y, m * ldy + n, y_dtype, acc);
+    }
+}
+
+__global__ __launch_bounds__(256) void k_g4_dx(G4Weights w, const void* __restrict__ dY, int dtype, int64_t M,
+                                               int64_t lddy, void* __restrict__ dX, int64_t lddx, int n_experts,
+                                               const int32_t* __restrict__ offsets) {
+    const int64_t groups = (w.K + w.group - 1) / w.group;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < M * w.K; i += gridDim.x * 256ll) {
+        const int64_t m = i / w.K, k = i % w.K, b = k / w.group;
+        const int e = expert_of(offsets, n_experts, m);
+        if (e < 0) continue;
+        float acc = 0.0f;
+        for (int64_t n = 0; n < w.N; ++n) {
+            const int64_t row = e * w.N + n;
+            const int z = w.zeros ? w.zeros[row * groups + b] & 15 : 8;
+            const int q = (w.W[row * (w.K / 2) + k / 2] >> (4 * (k & 1))) & 15;
+            acc = __builtin_fmaf(scale_of(w, row * groups + b) * (float)(q - z), to_f32(dY, m * lddy + n, dtype), acc);
+        }
+        store_f32(dX, m * lddx + k, dtype, acc);
+    }
+}
+
+dim3 grid_for(int64_t n) { return dim3((unsigned)((n + 255) / 256 < 65536 ? (n + 255) / 256 : 65536)); }
+
+}  // namespace
+
+hipError_t gqk_g4_matmul(const G4Weights& w, const void* X, int x_dtype, int64_t M, int64_t ldx, void* Y, int y_dtype,
+                         int64_t ldy, int n_experts, const int32_t* offsets, hipStream_t s) {
+    hipLaunchKernelGGL(k_g4_rows, grid_for(M * w.N), dim3(256), 0, s, w, X, x_dtype, M, ldx, Y, y_dtype, ldy, n_experts,
+                       offsets);
+    return hipGetLastError();
+}
+
+hipError_t gqk_g4_matvec(const G4Weights& w, const void* x, int x_dtype, int batch, void* y, int y_dtype,
+                         hipStream_t s) {
+    return gqk_g4_matmul(w, x, x_dtype, batch, w.K, y, y_dtype, w.N, 1, nullptr, s);
+}
+
+hipError_t gqk_g4_matmul_dx(const G4Weights& w, const void* dY, int dtype, int64_t M, int64_t lddy, void* dX,
+                            int64_t lddx, int n_experts, const int32_t* offsets, hipStream_t s) {
+    hipLaunchKernelGGL(k_g4_dx, grid_for(M * w.K), dim3(256), 0, s, w, dY, dtype, M, lddy, dX, lddx, n_experts,
+                       offsets);
+    return hipGetLastError();
+}
