@@ -89,11 +89,6 @@ hipError_t gqk_g4_matmul(const G4Weights& w, const void* X, int x_dtype, int64_t
     return hipGetLastError();
 }
 
-hipError_t gqk_g4_matvec(const G4Weights& w, const void* x, int x_dtype, int batch, void* y, int y_dtype,
-                         hipStream_t s) {
-    return gqk_g4_matmul(w, x, x_dtype, batch, w.K, y, y_dtype, w.N, 1, nullptr, s);
-}
-
 hipError_t gqk_g4_matmul_dx(const G4Weights& w, const void* dY, int dtype, int64_t M, int64_t lddy, void* dX,
                             int64_t lddx, int n_experts, const int32_t* offsets, hipStream_t s) {
     hipLaunchKernelGGL(k_g4_dx, grid_for(M * w.K), dim3(256), 0, s, w, dY, dtype, M, lddy, dX, lddx, n_experts,
