@@ -1,5 +1,5 @@
-// gq_g4.hip -- products with 4-bit weights and group scales (gfx950): one
-// thread an output, sums over a group in fp32 before its scale meets them.
+// gq_g4_dx.hip -- gradient of the products with 4-bit weights with respect to X
+// (gfx950): one thread an output.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -35,30 +35,6 @@ __device__ __forceinline__ int expert_of(const int32_t* offsets, int n_experts, 
     return lo < n_experts && offsets[lo] <= m ? lo : -1;
 }
 
-__global__ __launch_bounds__(256) void k_g4_rows(G4Weights w, const void* __restrict__ X, int x_dtype, int64_t M,
-                                                 int64_t ldx, void* __restrict__ Y, int y_dtype, int64_t ldy,
-                                                 int n_experts, const int32_t* __restrict__ offsets) {
-    const int64_t groups = (w.K + w.group - 1) / w.group;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < M * w.N; i += gridDim.x * 256ll) {
-        const int64_t m = i / w.N, n = i % w.N;
-        const int e = expert_of(offsets, n_experts, m);
-        if (e < 0) continue;
-        const int64_t row = e * w.N + n;
-        float acc = 0.0f;
-        for (int64_t b = 0; b < groups; ++b) {
-            const int z = w.zeros ? w.zeros[row * groups + b] & 15 : 8;
-            float sum = 0.0f;
-            const int64_t end = (b + 1) * w.group < w.K ? (b + 1) * w.group : w.K;
-            for (int64_t k = b * w.group; k < end; ++k) {
-                const int q = (w.W[row * (w.K / 2) + k / 2] >> (4 * (k & 1))) & 15;
-                sum = __builtin_fmaf((float)(q - z), to_f32(X, m * ldx + k, x_dtype), sum);
-            }
-            acc = __builtin_fmaf(scale_of(w, row * groups + b), sum, acc);
-        }
-        store_f32(Y, m * ldy + n, y_dtype, acc);
-    }
-}
-
 __global__ __launch_bounds__(256) void k_g4_dx(G4Weights w, const void* __restrict__ dY, int dtype, int64_t M,
                                                int64_t lddy, void* __restrict__ dX, int64_t lddx, int n_experts,
                                                const int32_t* __restrict__ offsets) {
@@ -81,13 +57,6 @@ __global__ __launch_bounds__(256) void k_g4_dx(G4Weights w, const void* __restri
 dim3 grid_for(int64_t n) { return dim3((unsigned)((n + 255) / 256 < 65536 ? (n + 255) / 256 : 65536)); }
 
 }  // namespace
-
-hipError_t gqk_g4_matmul(const G4Weights& w, const void* X, int x_dtype, int64_t M, int64_t ldx, void* Y, int y_dtype,
-                         int64_t ldy, int n_experts, const int32_t* offsets, hipStream_t s) {
-    hipLaunchKernelGGL(k_g4_rows, grid_for(M * w.N), dim3(256), 0, s, w, X, x_dtype, M, ldx, Y, y_dtype, ldy, n_experts,
-                       offsets);
-    return hipGetLastError();
-}
 
 hipError_t gqk_g4_matmul_dx(const G4Weights& w, const void* dY, int dtype, int64_t M, int64_t lddy, void* dX,
                             int64_t lddx, int n_experts, const int32_t* offsets, hipStream_t s) {

@@ -148,8 +148,8 @@ hipError_t dot(const G4Weights& w, const void* x, int x_dtype, void* y, int y_dt
 template <typename X, bool ZP, int G, int NT, int W, int XR>
 __global__ __launch_bounds__(64 * W) void k_g4_vectors(G4Weights wt, const void* __restrict__ x, int batch,
                                                        void* __restrict__ y, int y_dtype) {
-    constexpr int RING = W * StreamSize<X, NT, XR>::BYTES, JOIN = W * NT * 1024;
-    __shared__ __align__(16) uint8_t smem[RING > JOIN ? RING : JOIN];
+    using S = StreamSize<X, NT, XR>;
+    __shared__ __align__(16) uint8_t smem[W * (S::BYTES > S::JOIN ? S::BYTES : S::JOIN)];
     stream_tile<X, ZP, G, NT, W, XR>(wt, (int64_t)blockIdx.x * (16 * NT), x, wt.K, batch, smem,
                                      [&](int i, int64_t n, float v) { store_as(y, i * wt.N + n, y_dtype, v); });
 }

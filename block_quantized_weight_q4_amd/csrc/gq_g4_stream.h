@@ -1,6 +1,6 @@
-// gq_g4_stream.h -- the product of at most 16 rows of X with 4-bit weights, bound
-// by the stream of weights (gfx950, wave64): decode vectors, and the few rows
-// that each of many experts has.
+// gq_g4_stream.h -- the product of a few rows of X with 4-bit weights, bound by the
+// stream of weights (gfx950, wave64): decode vectors, short prompts, and the few
+// rows that each of many experts has.
 //
 // y[m][n] = sum over groups g of s[n][g] * sum_{k in g} (q[n][k] - z[n][g]) x[m][k]:
 // the inner sums are matrix instructions on exact integers, scaled into the fp32
@@ -44,11 +44,13 @@ struct StreamSize {
     static constexpr int ROW = BLK * X::SIZE;          // bytes of a row of X
     static constexpr int XI = XR * ROW / 1024;         // copies of X
     static constexpr int BYTES = 1024 * (WI + XI);
+    static constexpr int MT = XR > 16 ? XR / 16 : 1;   // operands of rows of X
+    static constexpr int JOIN = 1024 * NT * MT;
     static_assert(XR * ROW % 1024 == 0, "whole copies");
 };
 
 // Rows [row0, row0 + rows) of X (1 <= rows <= XR; rows past them repeat the
-// last), the 16 NT rows of W from n0.  smem: W * BYTES bytes, at least W * NT KB.
+// last), the 16 NT rows of W from n0.  smem: W * max(BYTES, JOIN) bytes.
 // store(i, n, v): element (row i < rows, n < N).
 template <typename X, bool ZP, int G, int NT, int W, int XR, typename Store>
 __device__ __forceinline__ void stream_tile(const G4Weights& wt, int64_t n0, const void* __restrict__ Xp,
@@ -57,7 +59,7 @@ __device__ __forceinline__ void stream_tile(const G4Weights& wt, int64_t n0, con
     constexpr int GPB = BLK / G;                // groups of a block
     constexpr int MPG = G / 32;                 // matrix instructions of a group (dwords of a lane)
     constexpr int CH = S::ROW / 16;             // 16-byte chunks of a row of X
-    constexpr int RPI = 64 / CH > 0 ? 64 / CH : 1;  // rows of one copy of X
+    constexpr int MT = S::MT;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, fq = lane >> 4;
@@ -129,13 +131,15 @@ __device__ __forceinline__ void stream_tile(const G4Weights& wt, int64_t n0, con
             }
         }
     };
-    f32x4 acc[NT];
+    f32x4 acc[NT][MT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = f32x4{};
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{};
 
     // one block: operands from LDS, the next one's copies, the products
     constexpr int PARTS = X::SIZE == 4 ? 3 : 1;
-    const int xrow = fr & (XR - 1);
+    const int xrow = XR < 16 ? fr & (XR - 1) : fr;
     auto step = [&](int kb) {
         // group g: MPG dwords of this lane's row, from byte (G / 2) g + 4 MPG fq
         uint32_t a[NT][GPB][MPG];
@@ -148,17 +152,18 @@ __device__ __forceinline__ void stream_tile(const G4Weights& wt, int64_t n0, con
                 __builtin_memcpy(a[i][g], __builtin_assume_aligned(p, 4 * MPG), 4 * MPG);
             }
         const u32x4* xd = reinterpret_cast<const u32x4*>(mine + 1024 * S::WI);
-        typename X::x8 v[GPB][MPG][PARTS];
-        u32x4 raw[GPB][MPG][X::SIZE / 2];
+        u32x4 raw[MT][GPB][MPG][X::SIZE / 2];
 #pragma unroll
-        for (int g = 0; g < GPB; ++g)
+        for (int j = 0; j < MT; ++j)
 #pragma unroll
-            for (int m = 0; m < MPG; ++m)
+            for (int g = 0; g < GPB; ++g)
 #pragma unroll
-                for (int c = 0; c < X::SIZE / 2; ++c) {
-                    const int eight = g * (G / 8) + MPG * fq + m;  // which eight inputs of the block
-                    raw[g][m][c] = xd[gqf8::pos_wide(xrow, (X::SIZE / 2) * eight + c, CH)];
-                }
+                for (int m = 0; m < MPG; ++m)
+#pragma unroll
+                    for (int c = 0; c < X::SIZE / 2; ++c) {
+                        const int eight = g * (G / 8) + MPG * fq + m;  // which eight inputs of the block
+                        raw[j][g][m][c] = xd[gqf8::pos_wide(16 * j + xrow, (X::SIZE / 2) * eight + c, CH)];
+                    }
         float s[NT][GPB];
         uint32_t z4[NT][GPB];
 #pragma unroll
@@ -171,26 +176,34 @@ __device__ __forceinline__ void stream_tile(const G4Weights& wt, int64_t n0, con
         wait_reads();
         load(kb + W);
 #pragma unroll
-        for (int g = 0; g < GPB; ++g)
+        for (int g = 0; g < GPB; ++g) {
+            typename X::x8 v[MT][MPG][PARTS];
 #pragma unroll
-            for (int m = 0; m < MPG; ++m) {
-                if constexpr (PARTS == 3) gqf8::split8(raw[g][m][0], raw[g][m][1], v[g][m]);
-                else v[g][m][0] = __builtin_bit_cast(typename X::x8, raw[g][m][0]);
-            }
+            for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+                for (int m = 0; m < MPG; ++m) {
+                    if constexpr (PARTS == 3) gqf8::split8(raw[j][g][m][0], raw[j][g][m][1], v[j][m]);
+                    else v[j][m][0] = __builtin_bit_cast(typename X::x8, raw[j][g][m][0]);
+                }
 #pragma unroll
-            for (int g = 0; g < GPB; ++g) {
-                f32x4 p{};
+            for (int i = 0; i < NT; ++i) {
+                f32x4 p[MT];
+#pragma unroll
+                for (int j = 0; j < MT; ++j) p[j] = f32x4{};
 #pragma unroll
                 for (int m = 0; m < MPG; ++m) {
                     const typename X::x8 b = operand<X, ZP>(a[i][g][m], z4[i][g]);
 #pragma unroll
-                    for (int e = PARTS - 1; e >= 0; --e) p = X::mfma(v[g][m][e], b, p);
+                    for (int j = 0; j < MT; ++j)
+#pragma unroll
+                        for (int e = PARTS - 1; e >= 0; --e) p[j] = X::mfma(v[j][m][e], b, p[j]);
                 }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(s[i][g], p[r], acc[i][r]);
+                for (int j = 0; j < MT; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(s[i][g], p[j][r], acc[i][j][r]);
             }
+        }
     };
     if (wave < KB) {
         load(wave);
@@ -202,22 +215,26 @@ __device__ __forceinline__ void stream_tile(const G4Weights& wt, int64_t n0, con
     wait_copies<0>();
     __syncthreads();
     // the join: partial sums of every wavefront, added in their order
+    constexpr int TILES = NT * MT;
     f32x4* part = reinterpret_cast<f32x4*>(smem);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) part[(wave * NT + i) * 64 + lane] = acc[i];
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) part[(wave * TILES + i * MT + j) * 64 + lane] = acc[i][j];
     __syncthreads();
-    for (int i = wave; i < NT; i += W) {
-        f32x4 v = part[i * 64 + lane];
+    for (int c = wave; c < TILES; c += W) {
+        f32x4 v = part[c * 64 + lane];
 #pragma unroll
         for (int w = 1; w < W; ++w) {
-            const f32x4 o = part[(w * NT + i) * 64 + lane];
+            const f32x4 o = part[(w * TILES + c) * 64 + lane];
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] += o[r];
         }
-        const int64_t n = n0 + 16 * i + fr;
+        const int64_t n = n0 + 16 * (c / MT) + fr;
+        const int row = 16 * (c % MT) + 4 * fq;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            if (4 * fq + r < rows && n < N) store(4 * fq + r, n, v[r]);
+            if (row + r < rows && n < N) store(row + r, n, v[r]);
     }
 }
 
