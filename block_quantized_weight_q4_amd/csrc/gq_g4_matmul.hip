@@ -25,14 +25,6 @@ struct Rows {
     const int32_t* offsets;
 };
 
-__device__ __forceinline__ G4Weights of_expert(G4Weights w, int e) {
-    const int64_t KG = (w.K + w.group - 1) / w.group;
-    w.W += (int64_t)e * w.N * (w.K / 2);
-    w.scales += (int64_t)e * w.N * KG;
-    if (w.zeros) w.zeros += (int64_t)e * w.N * KG;
-    return w;
-}
-
 // ------------------------------------------------------------- few rows ----
 
 template <typename X, bool ZP, int G, int NT, int W, int XR>

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "gq_g4_device.h"
+#include "gq_g4_internal.h"
 
 namespace gqg4 {
 
@@ -67,6 +68,15 @@ __device__ __forceinline__ bool tile_of(const int32_t* __restrict__ offsets, int
         left -= tiles;
     }
     return false;
+}
+
+// Weights of expert e.
+__device__ __forceinline__ G4Weights of_expert(G4Weights w, int e) {
+    const int64_t KG = (w.K + w.group - 1) / w.group;
+    w.W += (int64_t)e * w.N * (w.K / 2);
+    w.scales += (int64_t)e * w.N * KG;
+    if (w.zeros) w.zeros += (int64_t)e * w.N * KG;
+    return w;
 }
 
 // Most tiles there can be: every expert ends with a partial one.
