@@ -1,148 +1,357 @@
-// gq_expert.hip -- tokens sorted by expert and back (gfx950): a counting sort by
-// one workgroup; one workgroup a token for the rows.
+// gq_expert.hip -- tokens sorted by expert and back, and their gradients
+// (gfx950).  All are bound by HBM where there are many rows, and by the launch
+// where there are few.
 #include <hip/hip_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "gq_device.h"
 #include "gq_expert_internal.h"
 
+using gqd::u32x4;
+
 namespace {
 
 constexpr int MAX_E = 4096;
 
-__global__ __launch_bounds__(1024) void k_sort(const int32_t* __restrict__ ids, int S, int E,
-                                               int32_t* __restrict__ offsets, int32_t* __restrict__ place) {
-    __shared__ int count[MAX_E];
+// ------------------------------------------------------------------ sort ----
+
+// Workgroup b places the slots [b * chunk, (b + 1) * chunk) (chunk a multiple of
+// 64).  Each counts all the slots by itself, those before its own apart from the
+// others, so that no workgroup waits for another and one launch does it: the ids
+// are few bytes and come from the caches.  Then it scans the experts, and its
+// wavefronts place their slots one after another: equal ids of a wavefront find
+// each other by a ballot for each bit of the id.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void k_sort(const int32_t* __restrict__ ids, int S, int E, int chunk,
+                                                  int32_t* __restrict__ offsets, int32_t* __restrict__ place) {
+    constexpr int WAVES = THREADS / 64;
+    __shared__ int before[MAX_E], rest[MAX_E];  // slots before this workgroup's, the others; then places
+    __shared__ int wave_sum[WAVES];
     const int tid = threadIdx.x, lane = tid & 63;
-    for (int e = tid; e < E; e += 1024) count[e] = 0;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int first = blockIdx.x * chunk;
+    for (int e = tid; e < E; e += THREADS) before[e] = rest[e] = 0;
     __syncthreads();
-    for (int s = tid; s < S; s += 1024) {
-        const int id = ids[s];
-        if (id >= 0 && id < E) atomicAdd(&count[id], 1);
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int sum = 0;
-        for (int e = 0; e < E; ++e) {
-            const int c = count[e];
-            offsets[e] = count[e] = sum;
-            sum += c;
+    constexpr int U = 8;  // loads on their way at once
+    for (int s0 = 0; s0 < S; s0 += U * 4 * THREADS) {
+        int4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + (u * THREADS + tid) * 4;
+            v[u] = make_int4(-1, -1, -1, -1);
+            if (s + 4 <= S) {
+                v[u] = *reinterpret_cast<const int4*>(ids + s);  // (ids are 16-byte aligned)
+            } else {
+                if (s < S) v[u].x = ids[s];
+                if (s + 1 < S) v[u].y = ids[s + 1];
+                if (s + 2 < S) v[u].z = ids[s + 2];
+            }
         }
-        offsets[E] = sum;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + (u * THREADS + tid) * 4;
+            if (s0 + u * THREADS * 4 >= S) break;
+            int* count = s < first ? before : rest;  // (first is a multiple of 4)
+            if ((unsigned)v[u].x < (unsigned)E) atomicAdd(&count[v[u].x], 1);
+            if ((unsigned)v[u].y < (unsigned)E) atomicAdd(&count[v[u].y], 1);
+            if ((unsigned)v[u].z < (unsigned)E) atomicAdd(&count[v[u].z], 1);
+            if ((unsigned)v[u].w < (unsigned)E) atomicAdd(&count[v[u].w], 1);
+        }
     }
     __syncthreads();
-    // the first wavefront places 64 slots at a time, in their order
-    if (tid >= 64) return;
-    for (int s0 = 0; s0 < S; s0 += 64) {
-        const int s = s0 + lane, id = s < S ? ids[s] : -1;
-        const bool ok = id >= 0 && id < E;
+    // exclusive sums over the experts, a thread a run of them
+    const int per = (E + THREADS - 1) / THREADS;
+    const int lo = tid * per < E ? tid * per : E, hi = lo + per < E ? lo + per : E;
+    int n = 0;
+    for (int e = lo; e < hi; ++e) n += before[e] + rest[e];
+    int incl = n;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(incl, off, 64);
+        if (lane >= off) incl += v;
+    }
+    if (lane == 63) wave_sum[wave] = incl;
+    __syncthreads();
+    int sum = incl - n;
+    for (int w = 0; w < wave; ++w) sum += wave_sum[w];
+    for (int e = lo; e < hi; ++e) {
+        const int here = before[e] + rest[e];
+        if (blockIdx.x == 0) offsets[e] = sum;
+        before[e] += sum;  // the place of this workgroup's first slot of e
+        sum += here;
+    }
+    if (blockIdx.x == 0 && tid == THREADS - 1) offsets[E] = sum;
+    __syncthreads();
+    const int last = first + chunk < S ? first + chunk : S;
+    for (int s0 = first; s0 < last; s0 += THREADS) {
+        const int s = s0 + tid, id = s < last ? ids[s] : -1;
+        const bool ok = (unsigned)id < (unsigned)E;
         uint64_t same = __ballot(ok);
+#pragma unroll
         for (int b = 0; b < 12; ++b) {  // (E <= 4096)
             const uint64_t m = __ballot((id >> b) & 1);
             same &= (id >> b) & 1 ? m : ~m;
         }
-        const int rank = __popcll(same & ((1ull << lane) - 1));
-        const int base = ok ? count[id] : 0;
-        __builtin_amdgcn_wave_barrier();
-        if (ok && rank == 0) count[id] = base + __popcll(same);
-        if (s < S) place[s] = ok ? base + rank : -1;
+        const int rank = __popcll(same & ((1ull << lane) - 1)), count = __popcll(same);
+        const int waves = (last - s0 + 63) / 64 < WAVES ? (last - s0 + 63) / 64 : WAVES;
+        for (int w = 0; w < waves; ++w) {
+            if (wave == w) {
+                const int base = ok ? before[id] : 0;
+                if (ok && rank == count - 1) before[id] = base + count;  // (behind the reads of the others)
+                if (s < last) place[s] = ok ? base + rank : -1;
+            }
+            __syncthreads();
+        }
     }
 }
 
-__device__ __forceinline__ float to_f32(const void* p, int64_t i, int dtype) {
-    if (dtype == gqd::DT_F32) return static_cast<const float*>(p)[i];
-    const uint16_t u = static_cast<const uint16_t*>(p)[i];
-    return dtype == gqd::DT_BF16 ? gqd::bf2f(u) : gqd::h2f(u);
+// ------------------------------------------------------------------ rows ----
+
+// Element types of rows, and 16 bytes of them.
+struct F32 {
+    static constexpr int V = 4;
+    typedef float elem;
+    static __device__ __forceinline__ float wide(float v) { return v; }
+    static __device__ __forceinline__ float narrow(float v) { return v; }
+};
+struct Bf16 {
+    static constexpr int V = 8;
+    typedef uint16_t elem;
+    static __device__ __forceinline__ float wide(uint16_t v) { return gqd::bf2f(v); }
+    static __device__ __forceinline__ uint16_t narrow(float v) { return gqd::f2bf(v); }
+};
+struct F16 {
+    static constexpr int V = 8;
+    typedef uint16_t elem;
+    static __device__ __forceinline__ float wide(uint16_t v) { return gqd::h2f(v); }
+    static __device__ __forceinline__ uint16_t narrow(float v) { return gqd::f2h(v); }
+};
+
+// N elements from p, of which the first `left` are a row's (the others zeros, not
+// read); rows start at any element, which vector memory instructions allow.
+template <int N, typename E>
+__device__ __forceinline__ void read(const E* p, int64_t left, E (&v)[N]) {
+    if (left >= N) {
+        __builtin_memcpy(v, p, sizeof(v));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = i < left ? p[i] : E(0);
+    }
+}
+template <int N, typename E>
+__device__ __forceinline__ void write(E* p, int64_t left, const E (&v)[N]) {
+    if (left >= N) {
+        __builtin_memcpy(p, v, sizeof(v));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < left) p[i] = v[i];
+    }
 }
 
-__device__ __forceinline__ void store_f32(void* p, int64_t i, int dtype, float v) {
-    if (dtype == gqd::DT_F32) static_cast<float*>(p)[i] = v;
-    else static_cast<uint16_t*>(p)[i] = dtype == gqd::DT_BF16 ? gqd::f2bf(v) : gqd::f2h(v);
+// The row of slot s, -1 if it has none.
+__device__ __forceinline__ int64_t row_of(const int32_t* __restrict__ place, int64_t s, int64_t S) {
+    const int64_t p = place[s];
+    return p >= 0 && p < S ? p : -1;
+}
+
+// A wavefront copies 1 KB of one token's row to its slots' places.  pieces: of a
+// row.
+template <typename T>
+__global__ __launch_bounds__(256) void k_gather(const typename T::elem* __restrict__ x, int n_tokens, int top_k,
+                                                int64_t D, int64_t ldx, const int32_t* __restrict__ place,
+                                                typename T::elem* __restrict__ xs, int64_t ldxs, int64_t pieces) {
+    const int64_t i = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = i / pieces, d = ((i - t * pieces) * 64 + (threadIdx.x & 63)) * T::V;
+    if (t >= n_tokens || d >= D) return;
+    const int64_t S = (int64_t)n_tokens * top_k;
+    typename T::elem v[T::V];
+    read(x + t * ldx + d, D - d, v);
+#pragma unroll 8
+    for (int j = 0; j < top_k; ++j) {
+        const int64_t p = row_of(place, t * top_k + j, S);
+        if (p >= 0) write(xs + p * ldxs + d, D - d, v);
+    }
+}
+
+// A wavefront adds up 1 KB of one token's slots' rows, in their order.
+template <typename T, typename Y>
+__global__ __launch_bounds__(256) void k_combine(const typename T::elem* __restrict__ ys, int n_tokens, int top_k,
+                                                 int64_t D, int64_t ldys, const int32_t* __restrict__ place,
+                                                 const float* __restrict__ w, typename Y::elem* __restrict__ y,
+                                                 int64_t ldy, int64_t pieces) {
+    const int64_t i = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = i / pieces, d = ((i - t * pieces) * 64 + (threadIdx.x & 63)) * T::V;
+    if (t >= n_tokens || d >= D) return;
+    const int64_t S = (int64_t)n_tokens * top_k;
+    float sum[T::V];
+#pragma unroll
+    for (int e = 0; e < T::V; ++e) sum[e] = 0.0f;
+    constexpr int U = 8;  // rows on their way at once
+    for (int j0 = 0; j0 < top_k; j0 += U) {
+        typename T::elem v[U][T::V];
+        float f[U];
+        bool ok[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u < top_k ? j0 + u : top_k - 1;
+            const int64_t p = row_of(place, t * top_k + j, S);
+            ok[u] = p >= 0 && j0 + u < top_k;
+            f[u] = w ? w[t * top_k + j] : 1.0f;
+            if (ok[u]) read(ys + p * ldys + d, D - d, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (ok[u]) {
+#pragma unroll
+                for (int e = 0; e < T::V; ++e) sum[e] = __builtin_fmaf(f[u], T::wide(v[u][e]), sum[e]);
+            }
+    }
+    typename Y::elem out[T::V];
+#pragma unroll
+    for (int e = 0; e < T::V; ++e) out[e] = Y::narrow(sum[e]);
+    write(y + t * ldy + d, D - d, out);
+}
+
+// A workgroup has one token, its four wavefronts 1 KB pieces of the row in turn.
+// (dys may be ys: no __restrict__, and a piece is read before it is written)
+template <typename T>
+__global__ __launch_bounds__(256) void k_combine_grad(const typename T::elem* __restrict__ dy, int n_tokens,
+                                                      int top_k, int64_t D, int64_t lddy, const typename T::elem* ys,
+                                                      int64_t ldys, const int32_t* __restrict__ place,
+                                                      const float* __restrict__ w, typename T::elem* dys,
+                                                      int64_t lddys, float* __restrict__ dw) {
+    constexpr int U = 8;  // slots at a time
+    __shared__ float part[4][U];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = blockIdx.x, S = (int64_t)n_tokens * top_k;
+    for (int j0 = 0; j0 < top_k; j0 += U) {
+        int64_t p[U];
+        float f[U], sum[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u < top_k ? j0 + u : top_k - 1;
+            p[u] = j0 + u < top_k ? row_of(place, t * top_k + j, S) : -1;
+            f[u] = w ? w[t * top_k + j] : 1.0f;
+            sum[u] = 0.0f;
+        }
+        for (int64_t d = ((int64_t)wave * 64 + lane) * T::V; d < D; d += 256 * T::V) {
+            typename T::elem g[T::V], v[U][T::V];
+            read(dy + t * lddy + d, D - d, g);
+            if (dw) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (p[u] >= 0) read(ys + p[u] * ldys + d, D - d, v[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (p[u] < 0) continue;
+                if (dw) {
+#pragma unroll
+                    for (int e = 0; e < T::V; ++e) sum[u] = __builtin_fmaf(T::wide(g[e]), T::wide(v[u][e]), sum[u]);
+                }
+                if (dys) {
+                    typename T::elem out[T::V];
+#pragma unroll
+                    for (int e = 0; e < T::V; ++e) out[e] = w ? T::narrow(f[u] * T::wide(g[e])) : g[e];
+                    write(dys + p[u] * lddys + d, D - d, out);
+                }
+            }
+        }
+        if (!dw) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int off = 32; off >= 1; off >>= 1) sum[u] += __shfl_xor(sum[u], off, 64);
+            if (lane == 0) part[wave][u] = sum[u];
+        }
+        __syncthreads();
+        const int u = threadIdx.x;
+        if (u < U && j0 + u < top_k)
+            dw[t * top_k + j0 + u] = (part[0][u] + part[1][u]) + (part[2][u] + part[3][u]);
+        __syncthreads();
+    }
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void k_gather(const T* __restrict__ x, int64_t top_k, int64_t D, int64_t ldx,
-                                                const int32_t* __restrict__ place, T* __restrict__ xs, int64_t ldxs) {
-    const int64_t t = blockIdx.x, S = gridDim.x * top_k;
-    for (int64_t d = threadIdx.x; d < D; d += 256) {
-        const T v = x[t * ldx + d];
-        for (int64_t j = 0; j < top_k; ++j) {
-            const int64_t p = place[t * top_k + j];
-            if (p >= 0 && p < S) xs[p * ldxs + d] = v;
-        }
-    }
+int64_t pieces_of(int64_t D) {
+    return (D + 64 * T::V - 1) / (64 * T::V);
 }
 
-__global__ __launch_bounds__(256) void k_combine(const void* __restrict__ ys, int dtype, int64_t top_k, int64_t D,
-                                                 int64_t ldys, const int32_t* __restrict__ place,
-                                                 const float* __restrict__ w, void* __restrict__ y, int y_dtype,
-                                                 int64_t ldy) {
-    const int64_t t = blockIdx.x, S = gridDim.x * top_k;
-    for (int64_t d = threadIdx.x; d < D; d += 256) {
-        float sum = 0.0f;
-        for (int64_t j = 0; j < top_k; ++j) {
-            const int64_t p = place[t * top_k + j];
-            if (p >= 0 && p < S)
-                sum = __builtin_fmaf(w ? w[t * top_k + j] : 1.0f, to_f32(ys, p * ldys + d, dtype), sum);
-        }
-        store_f32(y, t * ldy + d, y_dtype, sum);
-    }
+// (a launch has at most 2^32 threads: 2^40 elements are at most 2^31 pieces of 512)
+dim3 grid_of(int64_t pieces) { return dim3((unsigned)((pieces + 3) / 4)); }
+
+template <typename T>
+hipError_t gather(const void* x, int n_tokens, int top_k, int64_t D, int64_t ldx, const int32_t* place, void* xs,
+                  int64_t ldxs, hipStream_t s) {
+    using E = typename T::elem;
+    const int64_t pieces = pieces_of<T>(D);
+    hipLaunchKernelGGL(k_gather<T>, grid_of(pieces * n_tokens), dim3(256), 0, s, static_cast<const E*>(x), n_tokens,
+                       top_k, D, ldx, place, static_cast<E*>(xs), ldxs, pieces);
+    return hipGetLastError();
 }
 
-// One workgroup a slot.  (dys may be ys: no __restrict__)
-__global__ __launch_bounds__(256) void k_combine_grad(const void* dy, int dtype, int64_t top_k, int64_t D,
-                                                      int64_t lddy, const void* ys, int64_t ldys,
-                                                      const int32_t* __restrict__ place, const float* __restrict__ w,
-                                                      void* dys, int64_t lddys, float* __restrict__ dw) {
-    __shared__ float part[4];
-    const int64_t slot = blockIdx.x, t = slot / top_k, S = gridDim.x, p = place[slot];
-    const bool ok = p >= 0 && p < S;
-    float sum = 0.0f;
-    if (ok) {
-        const float f = w ? w[slot] : 1.0f;
-        for (int64_t d = threadIdx.x; d < D; d += 256) {
-            const float g = to_f32(dy, t * lddy + d, dtype);
-            if (dw) sum = __builtin_fmaf(g, to_f32(ys, p * ldys + d, dtype), sum);
-            if (dys) store_f32(dys, p * lddys + d, dtype, f * g);
-        }
-    }
-    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
-    __syncthreads();
-    if (dw && threadIdx.x == 0) dw[slot] = (part[0] + part[1]) + (part[2] + part[3]);
+template <typename T, typename Y>
+hipError_t combine(const void* ys, int n_tokens, int top_k, int64_t D, int64_t ldys, const int32_t* place,
+                   const float* w, void* y, int64_t ldy, hipStream_t s) {
+    const int64_t pieces = pieces_of<T>(D);
+    hipLaunchKernelGGL((k_combine<T, Y>), grid_of(pieces * n_tokens), dim3(256), 0, s,
+                       static_cast<const typename T::elem*>(ys), n_tokens, top_k, D, ldys, place, w,
+                       static_cast<typename Y::elem*>(y), ldy, pieces);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t combine_grad(const void* dy, int n_tokens, int top_k, int64_t D, int64_t lddy, const void* ys,
+                        int64_t ldys, const int32_t* place, const float* w, void* dys, int64_t lddys, float* dw,
+                        hipStream_t s) {
+    using E = typename T::elem;
+    hipLaunchKernelGGL(k_combine_grad<T>, dim3(n_tokens), dim3(256), 0, s, static_cast<const E*>(dy), n_tokens, top_k,
+                       D, lddy, static_cast<const E*>(ys), ldys, place, w, static_cast<E*>(dys), lddys, dw);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t gqk_expert_sort(const int32_t* ids, int n_tokens, int top_k, int n_experts, int32_t* offsets,
                            int32_t* place, hipStream_t s) {
-    hipLaunchKernelGGL(k_sort, dim3(1), dim3(1024), 0, s, ids, n_tokens * top_k, n_experts, offsets, place);
+    const int S = n_tokens * top_k;
+    if (S <= 1024) {
+        hipLaunchKernelGGL(k_sort<256>, dim3(1), dim3(256), 0, s, ids, S, n_experts, 1024, offsets, place);
+        return hipGetLastError();
+    }
+    int chunk = (S / 256 + 63) / 64 * 64;  // about a workgroup a CU
+    if (chunk < 256) chunk = 256;
+    hipLaunchKernelGGL(k_sort<1024>, dim3((S + chunk - 1) / chunk), dim3(1024), 0, s, ids, S, n_experts, chunk, offsets,
+                       place);
     return hipGetLastError();
 }
 
 hipError_t gqk_expert_gather(const void* x, int dtype, int n_tokens, int top_k, int64_t D, int64_t ldx,
                              const int32_t* place, void* xs, int64_t ldxs, hipStream_t s) {
-    if (dtype == gqd::DT_F32)
-        hipLaunchKernelGGL(k_gather<uint32_t>, dim3(n_tokens), dim3(256), 0, s, static_cast<const uint32_t*>(x), top_k,
-                           D, ldx, place, static_cast<uint32_t*>(xs), ldxs);
-    else
-        hipLaunchKernelGGL(k_gather<uint16_t>, dim3(n_tokens), dim3(256), 0, s, static_cast<const uint16_t*>(x), top_k,
-                           D, ldx, place, static_cast<uint16_t*>(xs), ldxs);
-    return hipGetLastError();
+    if (dtype == gqd::DT_F32) return gather<F32>(x, n_tokens, top_k, D, ldx, place, xs, ldxs, s);
+    return gather<Bf16>(x, n_tokens, top_k, D, ldx, place, xs, ldxs, s);  // (a copy: any 16 bits)
 }
 
 hipError_t gqk_expert_combine(const void* ys, int dtype, int n_tokens, int top_k, int64_t D, int64_t ldys,
                               const int32_t* place, const float* w, void* y, int y_dtype, int64_t ldy,
                               hipStream_t s) {
-    hipLaunchKernelGGL(k_combine, dim3(n_tokens), dim3(256), 0, s, ys, dtype, top_k, D, ldys, place, w, y, y_dtype,
-                       ldy);
-    return hipGetLastError();
+    if (dtype == gqd::DT_F32) return combine<F32, F32>(ys, n_tokens, top_k, D, ldys, place, w, y, ldy, s);
+    if (dtype == gqd::DT_BF16)
+        return y_dtype == gqd::DT_F32 ? combine<Bf16, F32>(ys, n_tokens, top_k, D, ldys, place, w, y, ldy, s)
+                                      : combine<Bf16, Bf16>(ys, n_tokens, top_k, D, ldys, place, w, y, ldy, s);
+    return y_dtype == gqd::DT_F32 ? combine<F16, F32>(ys, n_tokens, top_k, D, ldys, place, w, y, ldy, s)
+                                  : combine<F16, F16>(ys, n_tokens, top_k, D, ldys, place, w, y, ldy, s);
 }
 
 hipError_t gqk_expert_combine_grad(const void* dy, int dtype, int n_tokens, int top_k, int64_t D, int64_t lddy,
                                    const void* ys, int64_t ldys, const int32_t* place, const float* w, void* dys,
                                    int64_t lddys, float* dw, hipStream_t s) {
-    hipLaunchKernelGGL(k_combine_grad, dim3(n_tokens * top_k), dim3(256), 0, s, dy, dtype, top_k, D, lddy, ys, ldys,
-                       place, w, dys, lddys, dw);
-    return hipGetLastError();
+    if (dtype == gqd::DT_F32)
+        return combine_grad<F32>(dy, n_tokens, top_k, D, lddy, ys, ldys, place, w, dys, lddys, dw, s);
+    if (dtype == gqd::DT_BF16)
+        return combine_grad<Bf16>(dy, n_tokens, top_k, D, lddy, ys, ldys, place, w, dys, lddys, dw, s);
+    return combine_grad<F16>(dy, n_tokens, top_k, D, lddy, ys, ldys, place, w, dys, lddys, dw, s);
 }
