@@ -74,6 +74,8 @@ struct Tile {
     static constexpr int BM = 16 * MT, BN = 64 * NT;
     static constexpr int XB = BM * 128, WB = BN * 32, STAGE = XB + WB;
     static constexpr int XI = BM / 32, WI = BN / 128, LOADS = XI + WI;  // copies of a wavefront
+    static constexpr int PANEL = 4 * 16 * NT * 8;                       // scales of a wavefront
+    static constexpr int BYTES = STAGES * STAGE + 4 * PANEL;
     static_assert(MT % 2 == 0 && NT % 2 == 0, "whole copies");
 
     // x: first row of the tile; n0: first column
@@ -97,103 +99,156 @@ struct Tile {
             const int r = xlr + 32 * u;
             xoff[u] = (uint32_t)((r < rows ? r : rows - 1) * ldx * 2) + xchunk;
         }
-        // W: two chunks a row, 32 rows a copy.  An operand's rows are 32 p + 8 (a / 4)
-        // + 4 o + a % 4 (a = l % 16, tile 2 p + o): row r sits at pair x = 16 o + 8
-        // (a / 8) + a % 8 of its copy, its chunks exchanged where a >= 8, so that 16
-        // rows at one chunk cover all banks.
+        // W: two chunks a row, 32 rows a copy, each wavefront its own columns (so that
+        // they wait for no other's).  An operand's rows are 32 p + 8 (a / 4) + 4 o + a %
+        // 4 (a = l % 16, tile 2 p + o): row r sits at pair x = 16 o + 8 (a / 8) + a % 8
+        // of its copy, its chunks exchanged where a >= 8, so that 16 rows at one chunk
+        // cover all banks.
         const int wx = lane >> 1, wa = wx & 15;
         const int wrow = 8 * (wa >> 2) + 4 * (wx >> 4) + (wa & 3);
         const int wchunk = 16 * ((lane & 1) ^ (wa >> 3));
         uint32_t woff[WI];
 #pragma unroll
-        for (int u = 0; u < WI; ++u) woff[u] = (uint32_t)((32 * (wave + 4 * u) + wrow) * row_bytes) + wchunk;
+        for (int u = 0; u < WI; ++u) woff[u] = (uint32_t)((32 * (WI * wave + u) + wrow) * row_bytes) + wchunk;
+        int lg = 0;
         auto load = [&](int s) {
-            uint8_t* d = smem + (s % STAGES) * STAGE;
+            uint8_t* d = smem + lg * STAGE;
+            lg = lg + 1 == STAGES ? 0 : lg + 1;
             const int64_t k = (int64_t)s * BK;
             const int left = k < K ? (int)(K - k < BK ? K - k : BK) : 0;
 #pragma unroll
+            for (int u = 0; u < WI; ++u)
+                copy16(wr, within(woff[u], wchunk, left / 2), d + XB + (WI * wave + u) * 1024, (uint32_t)(k / 2));
+#pragma unroll
             for (int u = 0; u < XI; ++u)
                 copy16(xr, within(xoff[u], xchunk, 2 * left), d + (wave + 4 * u) * 1024, (uint32_t)(2 * k));
-#pragma unroll
-            for (int u = 0; u < WI; ++u)
-                copy16(wr, within(woff[u], wchunk, left / 2), d + XB + (wave + 4 * u) * 1024, (uint32_t)(k / 2));
         };
 
-        // Scales: lane l < 16 NT has the column n0 + 16 NT wave + l of four groups; in
-        // use, a lane takes its operand's rows' from there.
+        // Scales: lane l < 16 NT loads those of the column n0 + 16 NT wave + l, four
+        // groups at a time, and puts 512 s and -z s into LDS ([group][column], each
+        // wavefront its own), where the lanes that use them read them.
         const int64_t sn = n0 + 16 * NT * wave + (lane < 16 * NT ? lane : 0);
         const int64_t srow = (sn < N ? sn : N - 1) * KG;
-        uint32_t sc[2], zp;
-        auto load_scales = [&](int g0) {
+        float* panel = reinterpret_cast<float*>(smem + STAGES * STAGE + wave * PANEL);
+        uint32_t four_a, four_b, four_z;
+        auto load_four = [&](int g0) {
+            four_a = four_b = 0;
+            four_z = 0x08080808u;
             if (g0 + 4 <= KG) {
-                __builtin_memcpy(sc, wt.scales + srow + g0, 8);
-                if (wt.zeros) __builtin_memcpy(&zp, wt.zeros + srow + g0, 4);
-            } else {
-                sc[0] = sc[1] = zp = 0;
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    if (g0 + g < KG) {
-                        sc[g >> 1] |= (uint32_t)wt.scales[srow + g0 + g] << (16 * (g & 1));
-                        if (wt.zeros) zp |= (uint32_t)wt.zeros[srow + g0 + g] << (8 * g);
-                    }
-            }
-            if (!wt.zeros) zp = 0x08080808u;
-        };
-        float s512[NT], sz[NT];
-        auto scales_of = [&](int s) {
-            // group 32: the lane's chunk fq / 2 of the stage is a group of its own
-            const int g = wt.group == 32 ? 2 * s + (fq >> 1) : wt.group == 64 ? s : s >> 1;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int from = 32 * (i >> 1) + 8 * (fr >> 2) + 4 * (i & 1) + (fr & 3);
-                const uint32_t a = (uint32_t)__shfl((int)sc[0], from, 64), b = (uint32_t)__shfl((int)sc[1], from, 64);
-                const uint32_t z = (uint32_t)__shfl((int)zp, from, 64) >> (8 * (g & 3));
-                const float f = scale_f32(((g & 2 ? b : a) >> (16 * (g & 1))) & 0xffffu, wt.s_f16);
-                s512[i] = 512.0f * f;
-                sz[i] = -(float)(z & 15u) * f;
+                u32x2 v;
+                __builtin_memcpy(&v, wt.scales + srow + g0, 8);
+                four_a = v.x;
+                four_b = v.y;
+                if (wt.zeros) __builtin_memcpy(&four_z, wt.zeros + srow + g0, 4);
+            } else if (g0 < KG) {
+                const int n = KG - g0;
+                four_a = wt.scales[srow + g0];
+                if (n > 1) four_a |= (uint32_t)wt.scales[srow + g0 + 1] << 16;
+                if (n > 2) four_b = wt.scales[srow + g0 + 2];
+                if (wt.zeros) {
+                    four_z = wt.zeros[srow + g0];
+                    if (n > 1) four_z |= (uint32_t)wt.zeros[srow + g0 + 1] << 8;
+                    if (n > 2) four_z |= (uint32_t)wt.zeros[srow + g0 + 2] << 16;
+                }
             }
         };
+        auto put_four = [&]() {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float f = scale_f32(((g & 2 ? four_b : four_a) >> (16 * (g & 1))) & 0xffffu, wt.s_f16);
+                gqf8::f32x2 v;
+                v.x = 512.0f * f;
+                v.y = -(float)((four_z >> (8 * g)) & 15u) * f;
+                if (lane < 16 * NT) reinterpret_cast<gqf8::f32x2*>(panel)[16 * NT * g + lane] = v;
+            }
+        };
+        const int gshift = wt.group == 32 ? 0 : wt.group == 64 ? 1 : 2;  // half stages of a group
+        const int per4 = 2 << gshift;                                    // stages of four groups
 
         f32x4 acc[NT][MT];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{};
-        const int p0 = gqf8::pos128(fr, 2 * fq), p1 = gqf8::pos128(fr, 2 * fq + 1);
-        // byte of this lane's eight of W: pair 8 (fr / 8) + fr % 8 (+ 16 for odd tiles), chunk fq / 2
-        const int wat = 32 * fr + 16 * ((fq >> 1) ^ (fr >> 3)) + 8 * (fq & 1);
+        // Operand c of a stage: the 32 inputs of its half c / NT, tile c % NT.  A lane
+        // has the eight of dword fq of the half's chunk; of X the chunk 4 (c / NT) + fq.
+        const int wbase = XB + 16 * NT * wave * 32 + 32 * fr + 4 * fq;
+        const int w_half[2] = {wbase + 16 * (fr >> 3), wbase + 16 * (1 - (fr >> 3))};
+        const int x_half[2] = {gqf8::pos128(fr, fq), gqf8::pos128(fr, 4 + fq)};
+        const gqf8::f32x2* pbase = reinterpret_cast<const gqf8::f32x2*>(panel) + 8 * (fr >> 2) + (fr & 3);
+        struct Raw {
+            uint32_t w;
+            gqf8::f32x2 s;
+        };
+        auto read_raw = [&](int buf, int s, int c, Raw& r) {
+            const int i = c % NT, h = c / NT;
+            r.w = *reinterpret_cast<const uint32_t*>(smem + buf * STAGE + w_half[h] + 1024 * (i >> 1) + 512 * (i & 1));
+            r.s = pbase[16 * NT * (((2 * s + h) >> gshift) & 3) + 32 * (i >> 1) + 4 * (i & 1)];
+        };
+        auto read_x = [&](int buf, int h, typename T::x8 (&b)[MT]) {
+            const u32x4* d = reinterpret_cast<const u32x4*>(smem + buf * STAGE);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) b[j] = __builtin_bit_cast(typename T::x8, d[128 * j + x_half[h]]);
+        };
+        // A stage, whose rows b0 of the first half, first operand a and second one's
+        // bytes are in registers: each operand is formed while the one before it is
+        // multiplied, its bytes read while the one before that is.  The barrier before
+        // the last products says two things: the next stage's rows have landed for
+        // everyone, and nobody needs this stage's buffer, into which the one STAGES
+        // ahead is sent.
         if (S > 0) {
+            load_four(0);
 #pragma unroll
             for (int s = 0; s < STAGES; ++s) load(s);
-        }
-        const int gps = wt.group == 32 ? 2 : 1, spg = wt.group == 128 ? 2 : 1;  // groups a stage, stages a group
-        const int per4 = 4 * spg / gps;                                         // stages of four groups
-        for (int s = 0; s < S; ++s) {
-            if (s % per4 == 0) load_scales(s / spg * gps);
+            put_four();
+            load_four(4);
             wait_copies<(STAGES - 1) * LOADS>();
             gqd::lds_barrier();
-            const uint8_t* d = smem + (s % STAGES) * STAGE;
-            scales_of(s);
-            const u32x4* xd = reinterpret_cast<const u32x4*>(d);
-            const uint8_t* wd = d + XB + (16 * NT * wave) * 32 + wat;
-            u32x2 w[NT];
+            typename T::x8 b0[MT], b1[MT], a;
+            Raw r[2];
+            read_raw(0, 0, 0, r[0]);
+            read_raw(0, 0, 1, r[1]);
+            read_x(0, 0, b0);
+            a = weights8<T>(r[0].w, r[0].s.x, r[0].s.y);
+            int buf = 0;
+            for (int s = 0; s < S; ++s) {
+                const int nbuf = buf + 1 == STAGES ? 0 : buf + 1;
+                read_x(buf, 1, b1);
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-                w[i] = *reinterpret_cast<const u32x2*>(wd + 1024 * (i >> 1) + 512 * (i & 1));
+                for (int c = 0; c < 2 * NT; ++c) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (c == 2 * NT - 2) {
+                        wait_copies<(STAGES - 2) * LOADS>();
+                        if ((s + 1) % per4 == 0) {
+                            put_four();
+                            load_four(((s + 1) / per4 + 1) * 4);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    if (c == 2 * NT - 1) {
+                        gqd::lds_barrier();
+                        load(s + STAGES);
+                        read_x(nbuf, 0, b0);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    // (r[(c + 1) % 2] is operand c + 1's)
+                    const Raw& n = r[(c + 1) & 1];
+                    const typename T::x8 next = weights8<T>(n.w, n.s.x, n.s.y);
+                    if (c + 2 < 2 * NT) read_raw(buf, s, c + 2, r[c & 1]);
+                    else read_raw(nbuf, s + 1, c + 2 - 2 * NT, r[c & 1]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                typename T::x8 b[MT];
+                    for (int j = 0; j < MT; ++j)
+                        acc[c % NT][j] = T::mfma(a, c < NT ? b0[j] : b1[j], acc[c % NT][j]);
+                    a = next;
 #pragma unroll
-                for (int j = 0; j < MT; ++j) b[j] = __builtin_bit_cast(typename T::x8, xd[128 * j + (h ? p1 : p0)]);
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const typename T::x8 a = weights8<T>(w[i][h], s512[i], sz[i]);
-#pragma unroll
-                    for (int j = 0; j < MT; ++j) acc[i][j] = T::mfma(a, b[j], acc[i][j]);
+                    for (int j = 0; j < MT; ++j) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                      // MFMA
+                        if (j < 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);           // LDS reads
+                        __builtin_amdgcn_sched_group_barrier(0x002, 24 / MT, 0);                // VALU
+                    }
                 }
+                buf = nbuf;
             }
-            gqd::lds_barrier();
-            load(s + STAGES);
         }
         wait_copies<0>();
         // lane: columns 32 p + 8 fq .. + 7 (tiles 2 p, 2 p + 1) of row 16 j + fr
@@ -254,7 +309,7 @@ hipError_t tile(const G4Weights& w, const Rows& a, hipStream_t s) {
     const int64_t gm = a.offsets ? most_tiles(a.M, a.n_experts, U::BM) : (a.M + U::BM - 1) / U::BM;
     const int64_t gn = (w.N + U::BN - 1) / U::BN;
     if (!grid_ok(gm * gn, 256)) return hipErrorInvalidValue;
-    const int lds = STAGES * U::STAGE;
+    const int lds = U::BYTES;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_tile<T, MT, NT>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
