@@ -227,9 +227,9 @@ struct Tile {
                     }
                     if (c == 2 * NT - 1) {
                         gqd::lds_barrier();
-                        load(s + STAGES);
-                        read_x(nbuf, 0, b0);
                         __builtin_amdgcn_sched_barrier(0);
+                        read_x(nbuf, 0, b0);
+                        load(s + STAGES);
                     }
                     // (r[(c + 1) % 2] is operand c + 1's)
                     const Raw& n = r[(c + 1) & 1];
@@ -240,11 +240,14 @@ struct Tile {
                     for (int j = 0; j < MT; ++j)
                         acc[c % NT][j] = T::mfma(a, c < NT ? b0[j] : b1[j], acc[c % NT][j]);
                     a = next;
+                    if (c == 2 * NT - 3) __asm__ volatile("" : "+v"(a));  // (formed here, not behind the next branch)
 #pragma unroll
                     for (int j = 0; j < MT; ++j) {
+                        if (c == 2 * NT - 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                      // MFMA
                         if (j < 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);           // LDS reads
                         __builtin_amdgcn_sched_group_barrier(0x002, 24 / MT, 0);                // VALU
+                        if (c == 2 * NT - 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0); // copies
                     }
                 }
                 buf = nbuf;
