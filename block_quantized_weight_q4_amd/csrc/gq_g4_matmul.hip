@@ -7,6 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gq_g4_device.h"
 #include "gq_g4_internal.h"
 #include "gq_g4_stream.h"
@@ -49,7 +51,6 @@ __global__ __launch_bounds__(64 * W) void k_g4_few(G4Weights wt, Rows a) {
 // ------------------------------------------------------- many rows (tiles) ----
 
 constexpr int BK = 64;     // inputs of a stage
-constexpr int STAGES = 3;  // in LDS
 
 // Eight weights s (q - z) of a dword, rounded to 16 bits; s512 = 512 s, sz = -z s.
 // A nibble as an e4m3 byte is q 2^-9 (subnormal below 8, the first normal binade
@@ -67,16 +68,17 @@ __device__ __forceinline__ typename T::x8 weights8(uint32_t w, float s512, float
 
 // BM = 16 MT rows of X by BN = 64 NT columns; four wavefronts, each all the rows
 // by a quarter of the columns, so that a weight is expanded by one wavefront only,
-// in registers, right before the matrix instructions that use it.  Both operands
-// of a stage of 64 inputs go to LDS as they are in memory, STAGES ahead.
-template <typename T, int MT, int NT>
+// in registers, right before the matrix instructions that use it.  Both operands go
+// to LDS as they are in memory: X in stages of 64 inputs, W in blocks of two stages
+// (64 bytes a row).
+template <typename T, int MT, int NT, int NW, int XS>
 struct Tile {
-    static constexpr int BM = 16 * MT, BN = 64 * NT;
-    static constexpr int XB = BM * 128, WB = BN * 32, STAGE = XB + WB;
-    static constexpr int XI = BM / 32, WI = BN / 128, LOADS = XI + WI;  // copies of a wavefront
-    static constexpr int PANEL = 4 * 16 * NT * 8;                       // scales of a wavefront
-    static constexpr int BYTES = STAGES * STAGE + 4 * PANEL;
-    static_assert(MT % 2 == 0 && NT % 2 == 0, "whole copies");
+    static constexpr int BM = 32 * MT, BN = 32 * NT * NW;
+    static constexpr int XB = BM * 128, WB = BN * 64;
+    static constexpr int XI = BM / 8 / NW, WI = 2 * NT;  // copies of a wavefront
+    static constexpr int PANEL = 32 * NT * 8;         // scales of a wavefront
+    static constexpr int W_AT = XS * XB, P_AT = W_AT + 2 * WB, BYTES = P_AT + NW * PANEL;
+    static_assert(BM % (8 * NW) == 0 && NT <= 2, "whole copies, a lane a column");
 
     // x: first row of the tile; n0: first column
     static __device__ __forceinline__ void run(const G4Weights& wt, const uint16_t* __restrict__ x, int64_t ldx,
@@ -84,54 +86,53 @@ struct Tile {
                                                uint8_t* smem) {
         const int lane = threadIdx.x & 63;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int fr = lane & 15, fq = lane >> 4;
+        const int fr = lane & 31, fq = lane >> 5;
         const int64_t N = wt.N, K = wt.K, row_bytes = K / 2;
         const int S = (int)((K + BK - 1) / BK), KG = (int)((K + wt.group - 1) / wt.group);
         const int64_t w_rows = N - n0 < BN ? N - n0 : BN;
         const Rsrc wr = make_rsrc(wt.W + n0 * row_bytes, w_rows * row_bytes);
         const Rsrc xr = make_rsrc(x, ((rows - 1) * ldx + K) * 2);
 
-        // X: rows of 128 bytes, chunks swizzled by row pairs; wavefront w brings rows 8 (w + 4 u) .. + 7
+        // X: rows of 128 bytes, chunks swizzled by row pairs; wavefront w brings rows 8 (w + NW u) .. + 7
         uint32_t xoff[XI];
         const int xlr = 8 * wave + (lane >> 3), xchunk = 16 * ((lane & 7) ^ ((xlr >> 1) & 7));
 #pragma unroll
         for (int u = 0; u < XI; ++u) {
-            const int r = xlr + 32 * u;
+            const int r = xlr + 8 * NW * u;
             xoff[u] = (uint32_t)((r < rows ? r : rows - 1) * ldx * 2) + xchunk;
         }
-        // W: two chunks a row, 32 rows a copy, each wavefront its own columns (so that
-        // they wait for no other's).  An operand's rows are 32 p + 8 (a / 4) + 4 o + a %
-        // 4 (a = l % 16, tile 2 p + o): row r sits at pair x = 16 o + 8 (a / 8) + a % 8
-        // of its copy, its chunks exchanged where a >= 8, so that 16 rows at one chunk
-        // cover all banks.
-        const int wx = lane >> 1, wa = wx & 15;
-        const int wrow = 8 * (wa >> 2) + 4 * (wx >> 4) + (wa & 3);
-        const int wchunk = 16 * ((lane & 1) ^ (wa >> 3));
+        // W: each wavefront its own columns (so that they wait for no other's), 16 rows of
+        // four chunks a copy, chunk c of row r at c ^ (r / 4), so that 16 rows at one chunk
+        // cover all banks
+        const int cr = lane >> 2, wchunk = 16 * ((lane & 3) ^ (cr >> 2));
         uint32_t woff[WI];
 #pragma unroll
-        for (int u = 0; u < WI; ++u) woff[u] = (uint32_t)((32 * (WI * wave + u) + wrow) * row_bytes) + wchunk;
-        int lg = 0;
-        auto load = [&](int s) {
-            uint8_t* d = smem + lg * STAGE;
-            lg = lg + 1 == STAGES ? 0 : lg + 1;
+        for (int u = 0; u < WI; ++u) woff[u] = (uint32_t)((32 * NT * wave + 16 * u + cr) * row_bytes) + wchunk;
+        auto load_x = [&](int s, int buf) __attribute__((always_inline)) {
             const int64_t k = (int64_t)s * BK;
             const int left = k < K ? (int)(K - k < BK ? K - k : BK) : 0;
-#pragma unroll
-            for (int u = 0; u < WI; ++u)
-                copy16(wr, within(woff[u], wchunk, left / 2), d + XB + (WI * wave + u) * 1024, (uint32_t)(k / 2));
+            uint8_t* d = smem + buf * XB;
 #pragma unroll
             for (int u = 0; u < XI; ++u)
-                copy16(xr, within(xoff[u], xchunk, 2 * left), d + (wave + 4 * u) * 1024, (uint32_t)(2 * k));
+                copy16(xr, within(xoff[u], xchunk, 2 * left), d + (wave + NW * u) * 1024, (uint32_t)(2 * k));
+        };
+        auto load_w = [&](int b, int buf) __attribute__((always_inline)) {
+            const int64_t k = (int64_t)b * (2 * BK);
+            const int left = k < K ? (int)(K - k < 2 * BK ? K - k : 2 * BK) : 0;
+            uint8_t* d = smem + W_AT + buf * WB;
+#pragma unroll
+            for (int u = 0; u < WI; ++u)
+                copy16(wr, within(woff[u], wchunk, left / 2), d + (WI * wave + u) * 1024, (uint32_t)(k / 2));
         };
 
-        // Scales: lane l < 16 NT loads those of the column n0 + 16 NT wave + l, four
-        // groups at a time, and puts 512 s and -z s into LDS ([group][column], each
-        // wavefront its own), where the lanes that use them read them.
-        const int64_t sn = n0 + 16 * NT * wave + (lane < 16 * NT ? lane : 0);
+        // Scales: lane l < 32 NT has those of the column n0 + 32 NT wave + l, four groups
+        // at a time, and puts 512 s and -z s of the group in use into LDS (each wavefront
+        // its own), where the lanes of the operand's rows read them.
+        const int64_t sn = n0 + 32 * NT * wave + (lane < 32 * NT ? lane : 0);
         const int64_t srow = (sn < N ? sn : N - 1) * KG;
-        float* panel = reinterpret_cast<float*>(smem + STAGES * STAGE + wave * PANEL);
-        uint32_t four_a, four_b, four_z;
-        auto load_four = [&](int g0) {
+        gqf8::f32x2* panel = reinterpret_cast<gqf8::f32x2*>(smem + P_AT + wave * PANEL);
+        uint32_t four_a, four_b, four_z;  // groups 4 i .. 4 i + 3, the next of them lowest
+        auto load_four = [&](int g0) __attribute__((always_inline)) {
             four_a = four_b = 0;
             four_z = 0x08080808u;
             if (g0 + 4 <= KG) {
@@ -152,131 +153,172 @@ struct Tile {
                 }
             }
         };
-        auto put_four = [&]() {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float f = scale_f32(((g & 2 ? four_b : four_a) >> (16 * (g & 1))) & 0xffffu, wt.s_f16);
-                gqf8::f32x2 v;
-                v.x = 512.0f * f;
-                v.y = -(float)((four_z >> (8 * g)) & 15u) * f;
-                if (lane < 16 * NT) reinterpret_cast<gqf8::f32x2*>(panel)[16 * NT * g + lane] = v;
-            }
+        // group g into LDS: behind the reads of the one before it (a wavefront's LDS operations keep their order)
+        auto put_scales = [&](int g) __attribute__((always_inline)) {
+            const float f = scale_f32(four_a & 0xffffu, wt.s_f16);
+            gqf8::f32x2 v;
+            v.x = 512.0f * f;
+            v.y = -(float)(four_z & 15u) * f;
+            if (lane < 32 * NT) panel[lane] = v;
+            four_a = (four_a >> 16) | (four_b << 16);
+            four_b >>= 16;
+            four_z >>= 8;
+            if ((g & 3) == 3) load_four(g + 1);
         };
         const int gshift = wt.group == 32 ? 0 : wt.group == 64 ? 1 : 2;  // half stages of a group
-        const int per4 = 2 << gshift;                                    // stages of four groups
 
-        f32x4 acc[NT][MT];
+        f32x16 acc[NT][MT];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{};
-        // Operand c of a stage: the 32 inputs of its half c / NT, tile c % NT.  A lane
-        // has the eight of dword fq of the half's chunk; of X the chunk 4 (c / NT) + fq.
-        const int wbase = XB + 16 * NT * wave * 32 + 32 * fr + 4 * fq;
-        const int w_half[2] = {wbase + 16 * (fr >> 3), wbase + 16 * (1 - (fr >> 3))};
-        const int x_half[2] = {gqf8::pos128(fr, fq), gqf8::pos128(fr, 4 + fq)};
-        const gqf8::f32x2* pbase = reinterpret_cast<const gqf8::f32x2*>(panel) + 8 * (fr >> 2) + (fr & 3);
+            for (int j = 0; j < MT; ++j) acc[i][j] = f32x16{};
+        // Operand c of a stage: the 16 inputs of its step c / NT (eight of them a lane:
+        // chunk 2 (c / NT) + fq of X, dword 2 (c / NT % 2) + fq of W's chunk), tile c % NT.
+        // Row a = l % 32 of a tile of W is its column 16 (a / 4 % 2) + 4 (a / 8) + a % 4, so
+        // that a lane ends up with 16 neighbouring columns of one row of Y.
+        const int wcol = 16 * ((fr >> 2) & 1) + 4 * (fr >> 3) + (fr & 3), wr16 = wcol & 15;
+        const int wbase = W_AT + 1024 * (WI * wave + (wcol >> 4)) + 64 * wr16 + 4 * fq;
+        int w_half[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) w_half[h] = wbase + 16 * (h ^ (wr16 >> 2));
+        int x_step[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) x_step[t] = gqf8::pos128(fr, 2 * t + fq);
+        const gqf8::f32x2* pbase = panel + wcol;
         struct Raw {
             uint32_t w;
             gqf8::f32x2 s;
         };
-        auto read_raw = [&](int buf, int s, int c, Raw& r) {
-            const int i = c % NT, h = c / NT;
-            r.w = *reinterpret_cast<const uint32_t*>(smem + buf * STAGE + w_half[h] + 1024 * (i >> 1) + 512 * (i & 1));
-            r.s = pbase[16 * NT * (((2 * s + h) >> gshift) & 3) + 32 * (i >> 1) + 4 * (i & 1)];
+        // (t: step of W's block)
+        auto read_raw = [&](int buf, int t, int i, Raw& r) __attribute__((always_inline)) {
+            r.w = *reinterpret_cast<const uint32_t*>(smem + buf * WB + w_half[t >> 1] + 8 * (t & 1) + 2048 * i);
+            r.s = pbase[32 * i];
         };
-        auto read_x = [&](int buf, int h, typename T::x8 (&b)[MT]) {
-            const u32x4* d = reinterpret_cast<const u32x4*>(smem + buf * STAGE);
-#pragma unroll
-            for (int j = 0; j < MT; ++j) b[j] = __builtin_bit_cast(typename T::x8, d[128 * j + x_half[h]]);
+        auto read_x = [&](int buf, int t, int j) __attribute__((always_inline)) {
+            const u32x4* d = reinterpret_cast<const u32x4*>(smem + buf * XB);
+            return __builtin_bit_cast(typename T::x8, d[256 * j + x_step[t]]);
         };
-        // A stage, whose rows b0 of the first half, first operand a and second one's
-        // bytes are in registers: each operand is formed while the one before it is
-        // multiplied, its bytes read while the one before that is.  The barrier before
-        // the last products says two things: the next stage's rows have landed for
-        // everyone, and nobody needs this stage's buffer, into which the one STAGES
-        // ahead is sent.
+        // A stage, whose first step's rows b, first operand a and second one's bytes
+        // are in registers: each operand is formed while the one before it is
+        // multiplied, its bytes read while the one before that is; a step's rows are
+        // read into the registers of the last step's as its last products need them no
+        // more.  The barrier before a stage's last products says two things: the next
+        // stage's rows have landed for everyone, and nobody needs this stage's buffer,
+        // into which the one XS ahead is sent.
         if (S > 0) {
             load_four(0);
+            load_w(0, 0);
 #pragma unroll
-            for (int s = 0; s < STAGES; ++s) load(s);
-            put_four();
-            load_four(4);
-            wait_copies<(STAGES - 1) * LOADS>();
+            for (int s = 0; s < XS; ++s) load_x(s, s);
+            load_w(1, 1);
+            put_scales(0);
+            wait_copies<(XS - 1) * XI + WI>();
             gqd::lds_barrier();
-            typename T::x8 b0[MT], b1[MT], a;
+            typename T::x8 b[MT], a;
             Raw r[2];
             read_raw(0, 0, 0, r[0]);
             read_raw(0, 0, 1, r[1]);
-            read_x(0, 0, b0);
-            a = weights8<T>(r[0].w, r[0].s.x, r[0].s.y);
-            int buf = 0;
-            for (int s = 0; s < S; ++s) {
-                const int nbuf = buf + 1 == STAGES ? 0 : buf + 1;
-                read_x(buf, 1, b1);
 #pragma unroll
-                for (int c = 0; c < 2 * NT; ++c) {
+            for (int j = 0; j < MT; ++j) b[j] = read_x(0, 0, j);
+            a = weights8<T>(r[0].w, r[0].s.x, r[0].s.y);
+            int buf = 0, wb = 0;  // of this stage
+            auto stage = [&](int s, auto odd) __attribute__((always_inline)) {
+                constexpr int T0 = odd ? 4 : 0, C = 4 * NT;
+                const int nbuf = buf + 1 == XS ? 0 : buf + 1;
+                const int nwb = odd ? wb ^ 1 : wb;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
                     __builtin_amdgcn_sched_barrier(0);
-                    if (c == 2 * NT - 2) {
-                        wait_copies<(STAGES - 2) * LOADS>();
-                        if ((s + 1) % per4 == 0) {
-                            put_four();
-                            load_four(((s + 1) / per4 + 1) * 4);
-                        }
-                        __builtin_amdgcn_sched_barrier(0);
+                    // the group of the half that is read next
+                    if (c == C / 2 - 2 && wt.group == 32) put_scales(2 * s + 1);
+                    if (c == C - 2) {
+                        // until stage s + 1 has landed
+                        wait_copies<(XS - 2) * XI + (odd ? 0 : WI)>();
+                        if ((2 * s + 2) % (1 << gshift) == 0) put_scales((2 * s + 2) >> gshift);
                     }
-                    if (c == 2 * NT - 1) {
+                    if (c == C - 1) {
                         gqd::lds_barrier();
                         __builtin_amdgcn_sched_barrier(0);
-                        read_x(nbuf, 0, b0);
-                        load(s + STAGES);
+                        load_x(s + XS, buf);
+                        if constexpr (odd) load_w((s + 3) / 2, wb);
                     }
                     // (r[(c + 1) % 2] is operand c + 1's)
                     const Raw& n = r[(c + 1) & 1];
                     const typename T::x8 next = weights8<T>(n.w, n.s.x, n.s.y);
-                    if (c + 2 < 2 * NT) read_raw(buf, s, c + 2, r[c & 1]);
-                    else read_raw(nbuf, s + 1, c + 2 - 2 * NT, r[c & 1]);
-#pragma unroll
-                    for (int j = 0; j < MT; ++j)
-                        acc[c % NT][j] = T::mfma(a, c < NT ? b0[j] : b1[j], acc[c % NT][j]);
-                    a = next;
-                    if (c == 2 * NT - 3) __asm__ volatile("" : "+v"(a));  // (formed here, not behind the next branch)
+                    if (c + 2 < C) read_raw(wb, T0 + (c + 2) / NT, (c + 2) % NT, r[c & 1]);
+                    else read_raw(nwb, (odd ? 0 : 4) + (c + 2 - C) / NT, (c + 2) % NT, r[c & 1]);
+                    const bool last = c % NT == NT - 1;  // of its step
 #pragma unroll
                     for (int j = 0; j < MT; ++j) {
-                        if (c == 2 * NT - 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                      // MFMA
-                        if (j < 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);           // LDS reads
-                        __builtin_amdgcn_sched_group_barrier(0x002, 24 / MT, 0);                // VALU
-                        if (c == 2 * NT - 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0); // copies
+                        acc[c % NT][j] = T::mfma32(a, b[j], acc[c % NT][j]);
+                        if (last) b[j] = c + 1 < C ? read_x(buf, (c + 1) / NT, j) : read_x(nbuf, 0, j);
+                    }
+                    a = next;
+                    // (formed here, not behind the next branch)
+                    if (c == C - 3 || c == C / 2 - 3) __asm__ volatile("" : "+v"(a));
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                // MFMA
+                        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                // LDS reads
+                        if (last) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, 24 / MT, 0);          // VALU
+                        if (c == C - 1) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);  // copies
                     }
                 }
                 buf = nbuf;
+                wb = nwb;
+            };
+            for (int s = 0; s < S; s += 2) {  // (a stage past K adds zeros)
+                stage(s, std::false_type{});
+                stage(s + 1, std::true_type{});
             }
         }
         wait_copies<0>();
-        // lane: columns 32 p + 8 fq .. + 7 (tiles 2 p, 2 p + 1) of row 16 j + fr
+        // lane: columns 16 fq .. + 15 of the tiles of row 32 j + fr
+        const bool vec = (ldy & (y_f32 ? 3 : 7)) == 0;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-            const int row = 16 * j + fr;
+            const int row = 32 * j + fr;
             if (row >= rows) continue;
 #pragma unroll
-            for (int i = 0; i < NT; i += 2) {
-                const int64_t n = n0 + 16 * NT * wave + 16 * i + 8 * fq;
+            for (int i = 0; i < NT; ++i) {
+                const int64_t n = n0 + 32 * NT * wave + 32 * i + 16 * fq;
+                const f32x16 v = acc[i][j];
+                if (y_f32) {
+                    float* p = static_cast<float*>(y) + row * ldy + n;
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (n + r < N) {
-                        const float v = r < 4 ? acc[i][j][r & 3] : acc[i + 1][j][r & 3];
-                        if (y_f32) static_cast<float*>(y)[row * ldy + n + r] = v;
-                        else static_cast<uint16_t*>(y)[row * ldy + n + r] = T::narrow(v);
+                    for (int r = 0; r < 16; r += 4) {
+                        if (vec && n + r + 4 <= N) {
+                            *reinterpret_cast<f32x4*>(p + r) = f32x4{v[r], v[r + 1], v[r + 2], v[r + 3]};
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (n + r + e < N) p[r + e] = v[r + e];
+                        }
                     }
+                } else {
+                    uint16_t* p = static_cast<uint16_t*>(y) + row * ldy + n;
+#pragma unroll
+                    for (int r = 0; r < 16; r += 8) {
+                        if (vec && n + r + 8 <= N) {
+                            *reinterpret_cast<u32x4*>(p + r) =
+                                u32x4{T::pack(v[r], v[r + 1]), T::pack(v[r + 2], v[r + 3]),
+                                      T::pack(v[r + 4], v[r + 5]), T::pack(v[r + 6], v[r + 7])};
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (n + r + e < N) p[r + e] = T::narrow(v[r + e]);
+                        }
+                    }
+                }
             }
         }
     }
 };
 
-template <typename T, int MT, int NT>
-__global__ __launch_bounds__(256, 2) void k_g4_tile(G4Weights wt, Rows a, int gm, int gn) {
-    using U = Tile<T, MT, NT>;
+template <typename T, int MT, int NT, int NW, int XS>
+__global__ __launch_bounds__(64 * NW, 2) void k_g4_tile(G4Weights wt, Rows a, int gm, int gn) {
+    using U = Tile<T, MT, NT, NW, XS>;
     extern __shared__ __align__(16) uint8_t smem[];
     RowTile t{0, 0, 0};
     int tn = 0;
@@ -306,17 +348,17 @@ __global__ __launch_bounds__(256, 2) void k_g4_tile(G4Weights wt, Rows a, int gm
            a.ldy, a.y_f32, (int64_t)tn * U::BN, smem);
 }
 
-template <typename T, int MT, int NT>
+template <typename T, int MT, int NT, int NW, int XS>
 hipError_t tile(const G4Weights& w, const Rows& a, hipStream_t s) {
-    using U = Tile<T, MT, NT>;
+    using U = Tile<T, MT, NT, NW, XS>;
     const int64_t gm = a.offsets ? most_tiles(a.M, a.n_experts, U::BM) : (a.M + U::BM - 1) / U::BM;
     const int64_t gn = (w.N + U::BN - 1) / U::BN;
-    if (!grid_ok(gm * gn, 256)) return hipErrorInvalidValue;
+    if (!grid_ok(gm * gn, 64 * NW)) return hipErrorInvalidValue;
     const int lds = U::BYTES;
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_tile<T, MT, NT>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_tile<T, MT, NT, NW, XS>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_g4_tile<T, MT, NT>), dim3((unsigned)(gm * gn)), dim3(256), lds, s, w, a, (int)gm, (int)gn);
+    hipLaunchKernelGGL((k_g4_tile<T, MT, NT, NW, XS>), dim3((unsigned)(gm * gn)), dim3(64 * NW), lds, s, w, a, (int)gm, (int)gn);
     return hipGetLastError();
 }
 
@@ -345,8 +387,8 @@ template <typename X, typename T>
 hipError_t matmul(const G4Weights& w, const Rows& a, hipStream_t s) {
     const int64_t per = a.M / a.n_experts;  // rows an expert has
     if (per <= 16 || a.y_f32) return w.zeros ? few<X, true>(w, a, s) : few<X, false>(w, a, s);
-    if (per <= 64) return tile<T, 4, 4>(w, a, s);
-    return tile<T, 8, 4>(w, a, s);
+    if (per <= 64) return tile<T, 2, 2, 4, 2>(w, a, s);
+    return tile<T, 4, 2, 4, 2>(w, a, s);
 }
 
 }  // namespace
