@@ -50,7 +50,8 @@ __global__ __launch_bounds__(64 * W) void k_g4_few(G4Weights wt, Rows a) {
 
 // ------------------------------------------------------- many rows (tiles) ----
 
-constexpr int BK = 64;     // inputs of a stage
+constexpr int BK = 64;   // inputs of a stage
+constexpr int BAND = 4;  // row tiles of a band
 
 // Eight weights s (q - z) of a dword, rounded to 16 bits; s512 = 512 s, sz = -z s.
 // A nibble as an e4m3 byte is q 2^-9 (subnormal below 8, the first normal binade
@@ -71,8 +72,9 @@ __device__ __forceinline__ typename T::x8 weights8(uint32_t w, float s512, float
 // in registers, right before the matrix instructions that use it.  Both operands go
 // to LDS as they are in memory: X in stages of 64 inputs, W in blocks of two stages
 // (64 bytes a row).
-template <typename T, int MT, int NT, int NW, int XS>
+template <typename T, int MT, int NT>
 struct Tile {
+    static constexpr int NW = 4, XS = 2;  // wavefronts, stages of X
     static constexpr int BM = 32 * MT, BN = 32 * NT * NW;
     static constexpr int XB = BM * 128, WB = BN * 64;
     static constexpr int XI = BM / 8 / NW, WI = 2 * NT;  // copies of a wavefront
@@ -261,7 +263,7 @@ struct Tile {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                // MFMA
                         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                // LDS reads
                         if (last) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, 24 / MT, 0);          // VALU
+                        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);                // VALU
                         if (c == C - 1) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);  // copies
                     }
                 }
@@ -316,49 +318,74 @@ struct Tile {
     }
 };
 
-template <typename T, int MT, int NT, int NW, int XS>
-__global__ __launch_bounds__(64 * NW, 2) void k_g4_tile(G4Weights wt, Rows a, int gm, int gn) {
-    using U = Tile<T, MT, NT, NW, XS>;
+// Workgroups from n_full on take parts of the tiles from n_full on, PARTS a tile,
+// by rows, then by columns (dense): the last, partial round of tiles would take as
+// long as a whole one on a part of the CUs.
+template <typename T, int MT, int NT, int PARTS>
+__global__ __launch_bounds__(256, 2) void k_g4_tile(G4Weights wt, Rows a, int gm, int gn, int n_full) {
+    using U = Tile<T, MT, NT>;
+    constexpr int PM = PARTS > 1 ? 2 : 1, PN = PARTS > 2 ? 2 : 1;
+    using P = Tile<T, MT / PM, NT / PN>;
     extern __shared__ __align__(16) uint8_t smem[];
     RowTile t{0, 0, 0};
-    int tn = 0;
+    int64_t n0 = 0;
+    bool part = false;
     if (a.offsets) {
         auto pick = [&](int total) {
             // (the grid is sized for the most tiles there can be: only the real ones are dealt out to the XCDs)
             const int64_t real = (int64_t)(total < gm ? total : gm) * gn;
             if (blockIdx.x >= real) return -1;
             const int id = xcd_order(blockIdx.x, (int)real);
-            tn = id % gn;
+            n0 = (int64_t)(id % gn) * U::BN;
             return id / gn;
         };
         if (!tile_of(a.offsets, a.n_experts, a.M, U::BM, pick, t)) return;
     } else {
-        const int id = xcd_order(blockIdx.x, gm * gn);
-        constexpr int BAND = 8;
+        int id, q = 0;
+        part = PARTS > 1 && (int)blockIdx.x >= n_full;
+        if (part) {
+            q = ((int)blockIdx.x - n_full) % PARTS;
+            id = n_full + ((int)blockIdx.x - n_full) / PARTS;
+        } else {
+            id = xcd_order(blockIdx.x, n_full);
+        }
+        // bands of at most BAND row tiles, each walked column of tiles by column
         const int bands = (gm + BAND - 1) / BAND, h = (gm + bands - 1) / bands;
         const int band = id / (h * gn), hb = gm - band * h < h ? gm - band * h : h;
         const int c = id - band * h * gn;
-        tn = c / hb;
-        t.row0 = (int64_t)(band * h + c % hb) * U::BM;
-        t.rows = a.M - t.row0 < U::BM ? (int)(a.M - t.row0) : U::BM;
+        n0 = (int64_t)(c / hb) * U::BN + (q >> 1) * P::BN;
+        t.row0 = (int64_t)(band * h + c % hb) * U::BM + (q & 1) * P::BM;
+        const int64_t left = a.M - t.row0, most = part ? P::BM : U::BM;
+        if (left <= 0 || n0 >= wt.N) return;
+        t.rows = (int)(left < most ? left : most);
     }
-    U::run(of_expert(wt, t.e), static_cast<const uint16_t*>(a.X) + t.row0 * a.ldx, a.ldx, t.rows,
-           a.y_f32 ? static_cast<void*>(static_cast<float*>(a.Y) + t.row0 * a.ldy)
-                   : static_cast<void*>(static_cast<uint16_t*>(a.Y) + t.row0 * a.ldy),
-           a.ldy, a.y_f32, (int64_t)tn * U::BN, smem);
+    const G4Weights w = of_expert(wt, t.e);
+    const uint16_t* x = static_cast<const uint16_t*>(a.X) + t.row0 * a.ldx;
+    void* y = a.y_f32 ? static_cast<void*>(static_cast<float*>(a.Y) + t.row0 * a.ldy)
+                      : static_cast<void*>(static_cast<uint16_t*>(a.Y) + t.row0 * a.ldy);
+    if constexpr (PARTS > 1) {
+        if (part || (PARTS == 2 && a.offsets && t.rows <= P::BM)) {  // (an expert's last rows)
+            P::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
+            return;
+        }
+    }
+    U::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
 }
 
-template <typename T, int MT, int NT, int NW, int XS>
+template <typename T, int MT, int NT, int PARTS>
 hipError_t tile(const G4Weights& w, const Rows& a, hipStream_t s) {
-    using U = Tile<T, MT, NT, NW, XS>;
+    using U = Tile<T, MT, NT>;
     const int64_t gm = a.offsets ? most_tiles(a.M, a.n_experts, U::BM) : (a.M + U::BM - 1) / U::BM;
-    const int64_t gn = (w.N + U::BN - 1) / U::BN;
-    if (!grid_ok(gm * gn, 64 * NW)) return hipErrorInvalidValue;
-    const int lds = U::BYTES;
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_tile<T, MT, NT, NW, XS>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const int64_t gn = (w.N + U::BN - 1) / U::BN, tiles = gm * gn;
+    const int64_t slots = 2 * gqk_cu_count(), tail = tiles % slots;
+    const int64_t n_full = PARTS > 1 && !a.offsets && PARTS * tail <= slots ? tiles - tail : tiles;
+    const int64_t grid = n_full + PARTS * (tiles - n_full);
+    if (!grid_ok(grid, 256)) return hipErrorInvalidValue;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_tile<T, MT, NT, PARTS>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_g4_tile<T, MT, NT, NW, XS>), dim3((unsigned)(gm * gn)), dim3(64 * NW), lds, s, w, a, (int)gm, (int)gn);
+    hipLaunchKernelGGL((k_g4_tile<T, MT, NT, PARTS>), dim3((unsigned)grid), dim3(256), U::BYTES, s, w, a, (int)gm,
+                       (int)gn, (int)n_full);
     return hipGetLastError();
 }
 
@@ -387,8 +414,8 @@ template <typename X, typename T>
 hipError_t matmul(const G4Weights& w, const Rows& a, hipStream_t s) {
     const int64_t per = a.M / a.n_experts;  // rows an expert has
     if (per <= 16 || a.y_f32) return w.zeros ? few<X, true>(w, a, s) : few<X, false>(w, a, s);
-    if (per <= 64) return tile<T, 2, 2, 4, 2>(w, a, s);
-    return tile<T, 4, 2, 4, 2>(w, a, s);
+    if (per <= 64) return tile<T, 2, 2, 1>(w, a, s);
+    return tile<T, 4, 2, 2>(w, a, s);
 }
 
 }  // namespace
