@@ -18,7 +18,6 @@ using namespace gqg4;
 namespace {
 
 constexpr int BK = 64;     // rows of W (columns of dY) of a stage
-constexpr int BN = 256;    // columns of a tile: 64 of each of the four wavefronts
 constexpr int STAGES = 3;  // in LDS
 
 struct Rows {
@@ -30,55 +29,57 @@ struct Rows {
     const int32_t* offsets;
 };
 
-// BM = 16 MT rows by BN columns.  DMA: rows of dY are whole 16-byte pieces, copied
-// straight to LDS; otherwise they go through registers, element by element at
+// BM = 16 MT rows by BN columns, 64 a wavefront; KS = 2: two wavefronts have the
+// same columns and half of the sum each.  DMA: rows of dY are whole 16-byte pieces,
+// copied straight to LDS; otherwise they go through registers, element by element at
 // their end.
-template <typename T, int MT, bool DMA>
+template <typename T, int MT, int KS, bool DMA>
 struct Tile {
-    static constexpr int BM = 16 * MT;
+    static constexpr int BM = 16 * MT, BN = 256 / KS;
     static constexpr int XB = BM * 128, WB = BK * (BN / 2), STAGE = XB + WB;
-    static constexpr int XI = BM / 32, WI = 2;
+    static constexpr int XI = BM / 32, WI = 2 / KS;
     // scales of a wavefront's 64 columns (two groups at most) and a stage's 64 rows, two stages
     static constexpr int SCALES = 2 * 2 * BK * 8;
     static constexpr int BYTES = STAGES * STAGE + 4 * SCALES;
+    static_assert(KS == 1 || 2 * 4096 * MT <= BYTES, "the join");
 
     static __device__ __forceinline__ void run(const G4Weights& wt, const uint16_t* __restrict__ dy, int64_t lddy,
                                                int rows, uint16_t* __restrict__ dx, int64_t lddx, int64_t k0,
                                                uint8_t* smem) {
         const int lane = threadIdx.x & 63;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int wn = wave % (4 / KS), ks = wave / (4 / KS);
         const int fr = lane & 15, fq = lane >> 4;
         const int64_t N = wt.N, K = wt.K, row_bytes = K / 2, KG = (K + wt.group - 1) / wt.group;
         const int S = (int)((N + BK - 1) / BK);
 
-        // dY: rows of 128 bytes, chunks swizzled by row pairs; wavefront w has rows 8 (w + 4 u) .. + 7
-        const int xlr = 8 * wave + (lane >> 3), xchunk = 8 * ((lane & 7) ^ ((xlr >> 1) & 7));  // (elements)
-        const uint16_t* xp[XI];
-#pragma unroll
-        for (int u = 0; u < XI; ++u) {
-            const int r = xlr + 32 * u;
-            xp[u] = dy + (int64_t)(r < rows ? r : rows - 1) * lddy;
-        }
-        // W: rows of 128 bytes; the 32-byte pieces of rows 8 apart are exchanged, so
-        // that the four rows that the lanes read at once are in different banks
-        auto load = [&](int s) {
+        // dY: rows of 128 bytes, chunks swizzled by row pairs; wavefront w has rows 8 (w + 4
+        // u) .. + 7, from a resource of their own (zeros past the last row and past N)
+        const int xr8 = lane >> 3, xlr = 8 * wave + xr8, xchunk = 8 * ((lane & 7) ^ ((xlr >> 1) & 7));  // (elements)
+        // W.  The four rows, 8 apart, that the lanes read at once have to be in different
+        // banks.  KS = 1: rows of 128 bytes, whose 32-byte pieces are exchanged by r / 8;
+        // KS = 2: rows of 64 bytes, row 32 h + 8 a + b of the stage at 32 h + 4 b + a.
+        auto load = [&](int s) __attribute__((always_inline)) {
             uint8_t* d = smem + (s % STAGES) * STAGE;
             const int64_t n = (int64_t)s * BK;
             const int left = n < N ? (int)(N - n < BK ? N - n : BK) : 0;
 #pragma unroll
             for (int u = 0; u < XI; ++u) {
                 uint8_t* l = d + (wave + 4 * u) * 1024;
+                const int first = 8 * wave + 32 * u, have = rows - first < 8 ? rows - first : 8;
                 if constexpr (DMA) {
-                    // (past the row's end its first piece, which meets weights of zero)
-                    copy16(reinterpret_cast<const uint8_t*>(xp[u] + (xchunk < left ? n + xchunk : 0)), l);
+                    const Rsrc xr = make_rsrc(dy + (have > 0 ? first * lddy : 0),
+                                              have > 0 ? ((have - 1) * lddy + N) * 2 : 0);
+                    copy16(xr, within((uint32_t)(xr8 * lddy + xchunk) * 2, xchunk, left), l, (uint32_t)(2 * n));
                 } else {
+                    const uint16_t* p = dy + (first + xr8 < rows ? first + xr8 : rows - 1) * lddy + n + xchunk;
                     u32x4 v{};
                     if (xchunk + 8 <= left) {
-                        __builtin_memcpy(&v, xp[u] + n + xchunk, 16);
+                        __builtin_memcpy(&v, p, 16);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if (xchunk + i < left) v[i / 2] |= (uint32_t)xp[u][n + xchunk + i] << (16 * (i & 1));
+                            if (xchunk + i < left) v[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
                     }
                     reinterpret_cast<u32x4*>(l)[lane] = v;
                 }
@@ -86,35 +87,46 @@ struct Tile {
             const Rsrc wr = make_rsrc(wt.W + n * row_bytes + k0 / 2, left ? left * row_bytes - k0 / 2 : 0);
 #pragma unroll
             for (int u = 0; u < WI; ++u) {
-                const int r = 8 * (wave + 4 * u) + (lane >> 3);
-                const int chunk = 16 * ((lane & 7) ^ (2 * ((r >> 3) & 3)));
+                int r, chunk;
+                if constexpr (KS == 1) {
+                    r = 8 * (wave + 4 * u) + (lane >> 3);
+                    chunk = 16 * ((lane & 7) ^ (2 * ((r >> 3) & 3)));
+                } else {
+                    const int at = 16 * wave + (lane >> 2);
+                    r = (at & 32) + 8 * (at & 3) + ((at >> 2) & 7);
+                    chunk = 16 * (lane & 3);
+                }
                 copy16(wr, within((uint32_t)(r * row_bytes) + chunk, chunk, (int)(K - k0 < BN ? K - k0 : BN) / 2),
                        d + XB + (wave + 4 * u) * 1024);
             }
         };
         // Scales: lane l has row n + l of the stage; as 512 s and -z s in LDS, [group][row].
         float* panel = reinterpret_cast<float*>(smem + STAGES * STAGE + wave * SCALES);
-        const int64_t kw = k0 + 64 * wave < K ? k0 + 64 * wave : K - 1;  // (columns past K are not stored)
+        const int64_t kw = k0 + 64 * wn < K ? k0 + 64 * wn : K - 1;  // (columns past K are not stored)
         const int64_t g0 = kw / wt.group, g1 = wt.group == 32 && g0 + 1 < KG ? g0 + 1 : g0;
+        const uint8_t* zeros = wt.zeros ? wt.zeros : reinterpret_cast<const uint8_t*>(wt.scales);
         struct Scale {
             uint32_t s[2], z[2];
         };
-        auto load_scales = [&](int s, Scale& c) {
+        bool in = false;  // row n + lane is one of W's
+        auto load_scales = [&](int s, Scale& c) __attribute__((always_inline)) {
+            // (no branch: four loads each time.  Without zero points their place is read in
+            // the scales, which are twice as many bytes)
             const int64_t n = (int64_t)s * BK + lane;
-            const bool in = n < N;
+            in = n < N;
             const int64_t at = (in ? n : 0) * KG;
-            c.s[0] = in ? wt.scales[at + g0] : 0u;
-            c.s[1] = in ? wt.scales[at + g1] : 0u;
-            c.z[0] = wt.zeros ? wt.zeros[at + g0] & 15u : 8u;
-            c.z[1] = wt.zeros ? wt.zeros[at + g1] & 15u : 8u;
+            c.s[0] = wt.scales[at + g0];
+            c.s[1] = wt.scales[at + g1];
+            c.z[0] = zeros[at + g0];
+            c.z[1] = zeros[at + g1];
         };
-        auto put_scales = [&](int s, const Scale& c) {
+        auto put_scales = [&](int s, const Scale& c) __attribute__((always_inline)) {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const float f = scale_f32(c.s[g], wt.s_f16);
+                const float f = in ? scale_f32(c.s[g], wt.s_f16) : 0.0f;
                 float* p = panel + ((s & 1) * 2 + g) * (2 * BK) + 2 * lane;
                 p[0] = 512.0f * f;
-                p[1] = -(float)c.z[g] * f;
+                p[1] = -(float)(wt.zeros ? c.z[g] & 15u : 8u) * f;
             }
         };
         f32x4 acc[4][MT];
@@ -122,64 +134,142 @@ struct Tile {
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[t][j] = f32x4{};
-        const int p0 = gqf8::pos128(fr, fq), p1 = gqf8::pos128(fr, 4 + fq);
-        // lane: columns 64 wave + 4 fr .. + 3 (two bytes), rows 32 h + 8 fq .. + 7
-        const int wat = (8 * fq) * 128 + ((wave ^ fq) * 32) + 2 * fr;
+        const int x_half[2] = {gqf8::pos128(fr, fq), gqf8::pos128(fr, 4 + fq)};
+        // lane: columns 64 wn + 4 fr .. + 3 (two bytes), rows 32 h + 8 fq .. + 7, ROW bytes apart
+        constexpr int ROW = KS == 1 ? 128 : 256, HALF = 32 * (BN / 2);
+        const int wat = KS == 1 ? 8 * fq * 128 + (wn ^ fq) * 32 + 2 * fr : fq * 64 + wn * 32 + 2 * fr;
         const int gsel = wt.group == 32 ? fr >> 3 : 0;
+        uint32_t w[4][2];  // the bytes of rows 2 i and 2 i + 1
+        f32x4 f[4];        // (512 s, -z s) of them
+        auto read_raw = [&](int s, int buf, int h, int i) __attribute__((always_inline)) {
+            const uint8_t* wd = smem + buf * STAGE + XB + HALF * h + wat;
+            const f32x4* sp = reinterpret_cast<const f32x4*>(panel + ((s & 1) * 2 + gsel) * (2 * BK) +
+                                                             2 * (32 * h + 8 * fq));
+            w[i][0] = *reinterpret_cast<const uint16_t*>(wd + 2 * ROW * i);
+            w[i][1] = *reinterpret_cast<const uint16_t*>(wd + 2 * ROW * i + ROW);
+            f[i] = sp[i];
+        };
+        auto read_x = [&](int buf, int h, int j) __attribute__((always_inline)) {
+            const u32x4* d = reinterpret_cast<const u32x4*>(smem + buf * STAGE);
+            return __builtin_bit_cast(typename T::x8, d[128 * j + x_half[h]]);
+        };
+        // rows 2 i and 2 i + 1 of the operands of the four columns
+        auto expand = [&](u32x4 (&a)[4], int i) __attribute__((always_inline)) {
+            // (joined by a byte permute: a read into the upper half of a register waits for the lower one's)
+            const uint32_t v = __builtin_amdgcn_perm(w[i][1], w[i][0], 0x05040100u);
+            const int lo = (int)(v & 0x0f0f0f0fu), hi = (int)((v >> 4) & 0x0f0f0f0fu);
+            const gqf8::f32x2 e0 = __builtin_amdgcn_cvt_pk_f32_fp8(lo, false);
+            const gqf8::f32x2 e1 = __builtin_amdgcn_cvt_pk_f32_fp8(lo, true);
+            const gqf8::f32x2 o0 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, false);
+            const gqf8::f32x2 o1 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, true);
+            auto f0 = [&](float q) { return __builtin_fmaf(q, f[i][0], f[i][1]); };
+            auto f1 = [&](float q) { return __builtin_fmaf(q, f[i][2], f[i][3]); };
+            a[0][i] = T::pack(f0(e0.x), f1(e1.x));
+            a[1][i] = T::pack(f0(o0.x), f1(o1.x));
+            a[2][i] = T::pack(f0(e0.y), f1(e1.y));
+            a[3][i] = T::pack(f0(o0.y), f1(o1.y));
+        };
+        // A half of a stage (KS = 2: this wavefront's), whose operands a and rows b are in
+        // registers: the next half's operands are formed while these are multiplied, its
+        // rows read as the last products need b no more.  The barrier before a stage's last
+        // products says two things: the next stage has landed for everyone, and nobody
+        // needs this one's buffer, into which the one STAGES ahead is sent.
         Scale sc;
         if (S > 0) {
             load_scales(0, sc);
 #pragma unroll
-            for (int s = 0; s < STAGES; ++s) load(s);
+            for (int s = 0; s < STAGES - 1; ++s) load(s);
             put_scales(0, sc);
             load_scales(1, sc);
-        }
-        for (int s = 0; s < S; ++s) {
-            if constexpr (DMA) wait_copies<(STAGES - 1) * (XI + WI)>();
+            load(STAGES - 1);  // (the same order as in the loop, for the waits that the compiler counts)
+            if constexpr (DMA) wait_copies<(STAGES - 1) * (XI + WI) + 4>();
             else wait_copies<0>();
             gqd::lds_barrier();
-            const uint8_t* d = smem + (s % STAGES) * STAGE;
-            const u32x4* xd = reinterpret_cast<const u32x4*>(d);
+            u32x4 a[4];
+            typename T::x8 b[MT];
+            const int h0 = KS == 1 ? 0 : ks;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                typename T::x8 b[MT];
+            for (int i = 0; i < 4; ++i) {
+                read_raw(0, 0, h0, i);
+                expand(a, i);
+            }
 #pragma unroll
-                for (int j = 0; j < MT; ++j) b[j] = __builtin_bit_cast(typename T::x8, xd[128 * j + (h ? p1 : p0)]);
-                const uint8_t* wd = d + XB + 32 * h * 128 + wat;
-                const f32x4* sp = reinterpret_cast<const f32x4*>(panel + ((s & 1) * 2 + gsel) * (2 * BK) +
-                                                                 2 * (32 * h + 8 * fq));
-                u32x4 a[4];
+            for (int j = 0; j < MT; ++j) b[j] = read_x(0, h0, j);
+            int buf = 0;
+            for (int s = 0; s < S; ++s) {
+                const int nbuf = buf + 1 == STAGES ? 0 : buf + 1;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t w = (uint32_t)*reinterpret_cast<const uint16_t*>(wd + 256 * i) |
-                                       (uint32_t)*reinterpret_cast<const uint16_t*>(wd + 256 * i + 128) << 16;
-                    const int lo = (int)(w & 0x0f0f0f0fu), hi = (int)((w >> 4) & 0x0f0f0f0fu);
-                    const f32x4 f = sp[i];  // (512 s, -z s) of rows 2 i, 2 i + 1
-                    const gqf8::f32x2 e0 = __builtin_amdgcn_cvt_pk_f32_fp8(lo, false);
-                    const gqf8::f32x2 e1 = __builtin_amdgcn_cvt_pk_f32_fp8(lo, true);
-                    const gqf8::f32x2 o0 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, false);
-                    const gqf8::f32x2 o1 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, true);
-                    auto f0 = [&](float q) { return __builtin_fmaf(q, f[0], f[1]); };
-                    auto f1 = [&](float q) { return __builtin_fmaf(q, f[2], f[3]); };
-                    a[0][i] = T::pack(f0(e0.x), f1(e1.x));
-                    a[1][i] = T::pack(f0(o0.x), f1(o1.x));
-                    a[2][i] = T::pack(f0(e0.y), f1(e1.y));
-                    a[3][i] = T::pack(f0(o0.y), f1(o1.y));
+                for (int hh = 0; hh < 2 / KS; ++hh) {
+                    const bool last = hh == 2 / KS - 1;  // of the stage
+                    if (last) {
+                        // until stage s + 1 has landed: the copies of s + 2 and four loads of
+                        // scales are younger
+                        if constexpr (DMA) wait_copies<(STAGES - 2) * (XI + WI) + 4>();
+                        else wait_copies<0>();
+                        put_scales(s + 1, sc);
+                        load_scales(s + 2, sc);
+                        gqd::lds_barrier();
+                        load(s + STAGES);
+                    }
+                    const int nh = last ? h0 : 1, from = last ? nbuf : buf;
+                    u32x4 next[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        // (one read ahead; the first products have no operand formed beside them)
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (t == 0) read_raw(last ? s + 1 : s, from, nh, 0);
+                        if (t < 3) read_raw(last ? s + 1 : s, from, nh, t + 1);
+                        if (t > 0) expand(next, t - 1);
+                        if (t == 3) expand(next, 3);
+#pragma unroll
+                        for (int j = 0; j < MT; ++j) {
+                            acc[t][j] = T::mfma(__builtin_bit_cast(typename T::x8, a[t]), b[j], acc[t][j]);
+                            if (t == 3) b[j] = read_x(from, nh, j);
+                        }
+                        if (t == 3) {
+                            // (formed here, not behind the next barrier)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) __asm__ volatile("" : "+v"(next[i]));
+                        }
+#pragma unroll
+                        for (int j = 0; j < MT; ++j) {
+                            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // MFMA
+                            if (t < 3) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);       // LDS reads
+                            if (t == 3) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                            if (t > 0 && t < 3) __builtin_amdgcn_sched_group_barrier(0x002, 24 / MT, 0);  // VALU
+                            if (t == 3) __builtin_amdgcn_sched_group_barrier(0x002, 48 / MT, 0);
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) a[t] = next[t];
                 }
+                buf = nbuf;
+            }
+        }
+        wait_copies<0>();
+        if constexpr (KS == 2) {
+            // the second half's sums to the wavefronts of the first
+            __syncthreads();
+            f32x4* part = reinterpret_cast<f32x4*>(smem) + wn * (4 * MT * 64) + lane;
+            if (ks == 1) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int j = 0; j < MT; ++j)
-                        acc[t][j] = T::mfma(__builtin_bit_cast(typename T::x8, a[t]), b[j], acc[t][j]);
+                    for (int j = 0; j < MT; ++j) part[64 * (t * MT + j)] = acc[t][j];
             }
-            put_scales(s + 1, sc);
-            load_scales(s + 2, sc);
-            gqd::lds_barrier();
-            load(s + STAGES);
+            __syncthreads();
+            if (ks == 1) return;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    const f32x4 o = part[64 * (t * MT + j)];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[t][j][r] += o[r];
+                }
         }
-        wait_copies<0>();
-        // lane: columns 64 wave + 16 fq .. + 15 of row 16 j + fr: 4 r + t
-        const int64_t k = k0 + 64 * wave + 16 * fq;
+        // lane: columns 64 wn + 16 fq .. + 15 of row 16 j + fr: 4 r + t
+        const int64_t k = k0 + 64 * wn + 16 * fq;
         if (k >= K) return;  // (K is a multiple of 32)
         const bool vec = (lddx & 7) == 0;
 #pragma unroll
@@ -204,14 +294,15 @@ struct Tile {
     }
 };
 
-template <typename T, int MT, bool DMA>
+template <typename T, int MT, int KS, bool DMA>
 __global__ __launch_bounds__(256, 2) void k_g4_dx(G4Weights wt, Rows a, int gm, int gn) {
-    using U = Tile<T, MT, DMA>;
+    using U = Tile<T, MT, KS, DMA>;
     extern __shared__ __align__(16) uint8_t smem[];
     RowTile t{0, 0, 0};
     int tn = 0;
     if (a.offsets) {
         auto pick = [&](int total) {
+            // (the grid is sized for the most tiles there can be: only the real ones are dealt out to the XCDs)
             const int64_t real = (int64_t)(total < gm ? total : gm) * gn;
             if (blockIdx.x >= real) return -1;
             const int id = xcd_order(blockIdx.x, (int)real);
@@ -225,35 +316,51 @@ __global__ __launch_bounds__(256, 2) void k_g4_dx(G4Weights wt, Rows a, int gm, 
         t.row0 = (int64_t)(id / gn) * U::BM;
         t.rows = a.M - t.row0 < U::BM ? (int)(a.M - t.row0) : U::BM;
     }
-    U::run(of_expert(wt, t.e), a.dY + t.row0 * a.lddy, a.lddy, t.rows, a.dX + t.row0 * a.lddx, a.lddx,
-           (int64_t)tn * BN, smem);
+    const G4Weights w = of_expert(wt, t.e);
+    const uint16_t* dy = a.dY + t.row0 * a.lddy;
+    uint16_t* dx = a.dX + t.row0 * a.lddx;
+    if constexpr (MT == 8) {
+        if (a.offsets && t.rows <= 64) {  // an expert's last rows
+            Tile<T, 4, KS, DMA>::run(w, dy, a.lddy, t.rows, dx, a.lddx, (int64_t)tn * U::BN, smem);
+            return;
+        }
+    }
+    U::run(w, dy, a.lddy, t.rows, dx, a.lddx, (int64_t)tn * U::BN, smem);
 }
 
-template <typename T, int MT, bool DMA>
+template <typename T, int MT, int KS, bool DMA>
 hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
-    using U = Tile<T, MT, DMA>;
+    using U = Tile<T, MT, KS, DMA>;
     const int64_t gm = a.offsets ? most_tiles(a.M, a.n_experts, U::BM) : (a.M + U::BM - 1) / U::BM;
-    const int64_t gn = (w.K + BN - 1) / BN;
+    const int64_t gn = (w.K + U::BN - 1) / U::BN;
     if (!grid_ok(gm * gn, 256)) return hipErrorInvalidValue;
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_dx<T, MT, DMA>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_dx<T, MT, KS, DMA>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_g4_dx<T, MT, DMA>), dim3((unsigned)(gm * gn)), dim3(256), U::BYTES, s, w, a, (int)gm,
+    hipLaunchKernelGGL((k_g4_dx<T, MT, KS, DMA>), dim3((unsigned)(gm * gn)), dim3(256), U::BYTES, s, w, a, (int)gm,
                        (int)gn);
     return hipGetLastError();
 }
 
+// Shape of the tiles (us; rows x sum x columns).  128 x 256 where they fill half of the
+// CUs (24,120 rows of 128 experts x 704 x 2816: 149, 64 rows 187; 1024 x 17408 x 5120:
+// 317, 64 rows 354); otherwise more and smaller ones with the sum in two halves: 64 x
+// 128 (256 x 17408 x 5120: 168, 128 x 256 314), for up to 32 rows 32 x 128 (16 x 9728 x
+// 2560: 78, 32 x 256 115, 64 x 128 87), unless there are enough of 32 x 256 (2048 rows
+// of 128 experts x 704 x 2816: 49, 32 x 128 59, 64 x 256 56).
 template <typename T, bool DMA>
 hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
     const int64_t per = a.M / a.n_experts;  // rows an expert has
-    if (per <= 32) return launch<T, 2, DMA>(w, a, s);
-    if (per <= 64) return launch<T, 4, DMA>(w, a, s);
-    return launch<T, 8, DMA>(w, a, s);
+    auto tiles = [&](int64_t rows) { return (per / rows + 1) * (a.n_experts < a.M ? a.n_experts : a.M) * ((w.K + 255) / 256); };
+    if (per <= 32) return tiles(32) >= 256 ? launch<T, 2, 1, DMA>(w, a, s) : launch<T, 2, 2, DMA>(w, a, s);
+    if (tiles(128) < 128) return launch<T, 4, 2, DMA>(w, a, s);
+    return per <= 64 ? launch<T, 4, 1, DMA>(w, a, s) : launch<T, 8, 1, DMA>(w, a, s);
 }
 
 template <typename T>
 hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
-    return w.N % 8 == 0 && a.lddy % 8 == 0 ? launch<T, true>(w, a, s) : launch<T, false>(w, a, s);
+    // (copies address eight rows in 31 bits)
+    return w.N % 8 == 0 && a.lddy % 8 == 0 && a.lddy < (1 << 26) ? launch<T, true>(w, a, s) : launch<T, false>(w, a, s);
 }
 
 }  // namespace

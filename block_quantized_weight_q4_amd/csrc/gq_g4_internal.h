@@ -18,6 +18,11 @@ struct G4Weights {
 
 hipError_t gqk_g4_matvec(const G4Weights& w, const void* x, int x_dtype, int batch, void* y, int y_dtype,
                          hipStream_t s);
+// The same on the matrix cores, by the type of x.
+hipError_t gqk_g4_vectors_bf16(const G4Weights& w, const void* x, int batch, void* y, int y_dtype, hipStream_t s);
+hipError_t gqk_g4_vectors_f16(const G4Weights& w, const void* x, int batch, void* y, int y_dtype, hipStream_t s);
+hipError_t gqk_g4_vectors_f32(const G4Weights& w, const void* x, int batch, void* y, int y_dtype, hipStream_t s);
+
 // offsets NULL: one matrix
 hipError_t gqk_g4_matmul(const G4Weights& w, const void* X, int x_dtype, int64_t M, int64_t ldx, void* Y, int y_dtype,
                          int64_t ldy, int n_experts, const int32_t* offsets, hipStream_t s);

@@ -29,19 +29,21 @@ struct Rows {
 
 // ------------------------------------------------------------- few rows ----
 
+// Workgroup first + blockIdx.x: columns % gn, row tile / gn.
 template <typename X, bool ZP, int G, int NT, int W, int XR>
-__global__ __launch_bounds__(64 * W) void k_g4_few(G4Weights wt, Rows a) {
+__global__ __launch_bounds__(64 * W) void k_g4_few(G4Weights wt, Rows a, int gn, int64_t first) {
     using S = StreamSize<X, NT, XR>;
     __shared__ __align__(16) uint8_t smem[W * (S::BYTES > S::JOIN ? S::BYTES : S::JOIN)];
+    const int64_t id = first + blockIdx.x, tm = id / gn;
     RowTile t{0, 0, 0};
     if (a.offsets) {
-        if (!tile_of(a.offsets, a.n_experts, a.M, XR, [&](int) { return (int)blockIdx.y; }, t)) return;
+        if (!tile_of(a.offsets, a.n_experts, a.M, XR, [&](int) { return (int)tm; }, t)) return;
     } else {
-        t.row0 = (int64_t)blockIdx.y * XR;
+        t.row0 = tm * XR;
         t.rows = a.M - t.row0 < XR ? (int)(a.M - t.row0) : XR;
     }
     const int y_dtype = a.y_f32 ? gqd::DT_F32 : X::dtype;
-    stream_tile<X, ZP, G, NT, W, XR>(of_expert(wt, t.e), (int64_t)blockIdx.x * (16 * NT),
+    stream_tile<X, ZP, G, NT, W, XR>(of_expert(wt, t.e), (id - tm * gn) * (16 * NT),
                                      static_cast<const uint16_t*>(a.X) + t.row0 * a.ldx, a.ldx, t.rows, smem,
                                      [&](int i, int64_t n, float v) {
                                          store_as(a.Y, (t.row0 + i) * a.ldy + n, y_dtype, v);
@@ -393,13 +395,30 @@ template <typename X, bool ZP, int G, int NT, int W, int XR>
 hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
     const int64_t gm = a.offsets ? most_tiles(a.M, a.n_experts, XR) : (a.M + XR - 1) / XR;
     const int64_t gn = (w.N + 16 * NT - 1) / (16 * NT);
-    if (!grid_ok(gn, 64 * W) || gm > 65535) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_g4_few<X, ZP, G, NT, W, XR>), dim3((unsigned)gn, (unsigned)gm), dim3(64 * W), 0, s, w, a);
-    return hipGetLastError();
+    for (int64_t first = 0; first < gm * gn; first += MOST_GROUPS) {
+        const int64_t left = gm * gn - first;
+        hipLaunchKernelGGL((k_g4_few<X, ZP, G, NT, W, XR>), dim3((unsigned)(left < MOST_GROUPS ? left : MOST_GROUPS)),
+                           dim3(64 * W), 0, s, w, a, (int)gn, first);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
+// Shape of the streamed tiles (us; N x K; n rows of W by m of X by w wavefronts).
+// Experts with up to two rows: 32 by 4 by 2 (64 rows of 128 experts, 704 x 2816: 15.1,
+// 32 by 4 by 4 15.8, 16 by 4 by 4 16.3, 32 by 16 by 2 16.4), with more 32 by 16 by 2
+// (1024 rows, 704 x 2816: 41.7, with 4 wavefronts 45.9, 32 by 32 by 4 60.6).  One
+// matrix: up to 16 rows 32 by 16 by 4 (17408 x 5120: 20.7, 32 by 32 by 4 25.9), of up
+// to 4096 columns 16 by 16 by 4 (2560 x 9728: 9.3 and 12.5); more rows 32 by 32 by 4,
+// which reads W half as often (1024 rows of 17408 x 5120: 425, 32 by 16 by 4 540).
 template <typename X, bool ZP, int G>
 hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
+    const int64_t per = a.M / a.n_experts;  // rows an expert has
+    if (a.n_experts > 1 && per <= 2) return few<X, ZP, G, 2, 2, 4>(w, a, s);
+    if (a.n_experts > 1 && per <= 64) return few<X, ZP, G, 2, 2, 16>(w, a, s);
+    if (per > 16) return few<X, ZP, G, 2, 4, 32>(w, a, s);
+    if (w.N <= 4096) return few<X, ZP, G, 1, 4, 16>(w, a, s);
     return few<X, ZP, G, 2, 4, 16>(w, a, s);
 }
 
@@ -410,11 +429,17 @@ hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
     return few<X, ZP, 128>(w, a, s);
 }
 
+// Tiles (of 16-bit results) or stream.  A workgroup of a tile goes through all of K
+// by itself, about 0.7 us for 64 inputs, so few tiles leave CUs idle: 2560 x 9728 takes
+// 106 us in tiles with 64 to 512 rows, streamed 16 to 55, with 1024 rows 108 either way;
+// 17408 x 5120 with 64 rows 59 and 39, with 256 87 and 114 (about 450 and 950 TFLOP/s
+// where there is enough work); 704 x 2816 of 128 experts with 1024 rows 46 and 42; 2816 x
+// 2816 of 8 with 256 35 and 24, with 1000 41 and 58.  Narrow matrices leave most of a
+// tile's 256 columns empty.
 template <typename X, typename T>
 hipError_t matmul(const G4Weights& w, const Rows& a, hipStream_t s) {
-    const int64_t per = a.M / a.n_experts;  // rows an expert has
-    if (per <= 16 || a.y_f32) return w.zeros ? few<X, true>(w, a, s) : few<X, false>(w, a, s);
-    if (per <= 64) return tile<T, 2, 2, 1>(w, a, s);
+    if (a.y_f32 || w.N < 128 || a.M * w.N < 2500000) return w.zeros ? few<X, true>(w, a, s) : few<X, false>(w, a, s);
+    if (a.M / a.n_experts <= 64) return tile<T, 2, 2, 1>(w, a, s);
     return tile<T, 4, 2, 2>(w, a, s);
 }
 

@@ -43,7 +43,11 @@ struct StreamSize {
     static constexpr int WI = 2 * NT;                  // copies (1 KB) of weights
     static constexpr int ROW = BLK * X::SIZE;          // bytes of a row of X
     static constexpr int XI = XR * ROW / 1024;         // copies of X
-    static constexpr int BYTES = 1024 * (WI + XI);
+    // fp32 rows, eight at most: each value is split once, by one lane, and passed on
+    // through LDS (sixteen fill all the operand's columns anyway)
+    static constexpr bool SHARE = X::SIZE == 4 && XR <= 8;
+    static constexpr int PARTS_AT = 1024 * (WI + XI);
+    static constexpr int BYTES = PARTS_AT + (SHARE ? 3 * XR * 512 : 0);
     static constexpr int MT = XR > 16 ? XR / 16 : 1;   // operands of rows of X
     static constexpr int JOIN = 1024 * NT * MT;
     static_assert(XR * ROW % 1024 == 0, "whole copies");
@@ -152,18 +156,33 @@ __device__ __forceinline__ void stream_tile(const G4Weights& wt, int64_t n0, con
                 __builtin_memcpy(a[i][g], __builtin_assume_aligned(p, 4 * MPG), 4 * MPG);
             }
         const u32x4* xd = reinterpret_cast<const u32x4*>(mine + 1024 * S::WI);
-        u32x4 raw[MT][GPB][MPG][X::SIZE / 2];
+        // (eight inputs g, m: which of the block's)
+        auto eight = [&](int g, int m) { return g * (G / 8) + MPG * fq + m; };
+        constexpr int PIECES = X::SIZE / 2;  // 16-byte pieces of eight inputs
+        u32x4 raw[MT][GPB][MPG][S::SHARE ? 1 : PIECES];
+        bf16x8* parts = reinterpret_cast<bf16x8*>(mine + S::PARTS_AT);  // [part][row][eight]
+        if constexpr (S::SHARE) {
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
+            for (int u = 0; u < (XR * 32 + 63) / 64; ++u) {
+                const int at = 64 * u + lane, row = at >> 5, o = at & 31;
+                if (XR * 32 >= 64 || lane < XR * 32) {
+                    bf16x8 y[3];
+                    gqf8::split8(xd[gqf8::pos_wide(row, 2 * o, CH)], xd[gqf8::pos_wide(row, 2 * o + 1, CH)], y);
 #pragma unroll
-            for (int g = 0; g < GPB; ++g)
+                    for (int e = 0; e < 3; ++e) parts[gqf8::pos_wide(e * XR + row, o, 32)] = y[e];
+                }
+            }
+        } else {
 #pragma unroll
-                for (int m = 0; m < MPG; ++m)
+            for (int j = 0; j < MT; ++j)
 #pragma unroll
-                    for (int c = 0; c < X::SIZE / 2; ++c) {
-                        const int eight = g * (G / 8) + MPG * fq + m;  // which eight inputs of the block
-                        raw[j][g][m][c] = xd[gqf8::pos_wide(16 * j + xrow, (X::SIZE / 2) * eight + c, CH)];
-                    }
+                for (int g = 0; g < GPB; ++g)
+#pragma unroll
+                    for (int m = 0; m < MPG; ++m)
+#pragma unroll
+                        for (int c = 0; c < PIECES; ++c)
+                            raw[j][g][m][c] = xd[gqf8::pos_wide(16 * j + xrow, PIECES * eight(g, m) + c, CH)];
+        }
         float s[NT][GPB];
         uint32_t z4[NT][GPB];
 #pragma unroll
@@ -182,7 +201,11 @@ __device__ __forceinline__ void stream_tile(const G4Weights& wt, int64_t n0, con
             for (int j = 0; j < MT; ++j)
 #pragma unroll
                 for (int m = 0; m < MPG; ++m) {
-                    if constexpr (PARTS == 3) gqf8::split8(raw[j][g][m][0], raw[j][g][m][1], v[j][m]);
+                    if constexpr (S::SHARE) {
+#pragma unroll
+                        for (int e = 0; e < 3; ++e)
+                            v[j][m][e] = parts[gqf8::pos_wide(e * XR + xrow, eight(g, m), 32)];
+                    } else if constexpr (PARTS == 3) gqf8::split8(raw[j][g][m][0], raw[j][g][m][1], v[j][m]);
                     else v[j][m][0] = __builtin_bit_cast(typename X::x8, raw[j][g][m][0]);
                 }
 #pragma unroll

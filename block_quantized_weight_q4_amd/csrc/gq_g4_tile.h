@@ -79,6 +79,9 @@ __device__ __forceinline__ G4Weights of_expert(G4Weights w, int e) {
     return w;
 }
 
+// Workgroups of one launch (of at most 256 threads; a launch has fewer than 2^32).
+constexpr int64_t MOST_GROUPS = (int64_t)1 << 23;
+
 // Most tiles there can be: every expert ends with a partial one.
 inline int64_t most_tiles(int64_t M, int E, int TM) { return M / TM + (M < E ? M : E); }
 
