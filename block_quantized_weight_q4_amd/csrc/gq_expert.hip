@@ -108,45 +108,74 @@ __global__ __launch_bounds__(THREADS) void k_sort(const int32_t* __restrict__ id
 
 // ------------------------------------------------------------------ rows ----
 
-// Element types of rows, and 16 bytes of them.
+// Element types of rows; V of them are 16 bytes.
 struct F32 {
     static constexpr int V = 4;
-    typedef float elem;
-    static __device__ __forceinline__ float wide(float v) { return v; }
-    static __device__ __forceinline__ float narrow(float v) { return v; }
+    typedef uint32_t elem;
+    static __device__ __forceinline__ float get(const u32x4& v, int i) {
+        const uint32_t u = v[i];  // (a copy first: a bit_cast of a vector's element takes element 0)
+        return __builtin_bit_cast(float, u);
+    }
+    static __device__ __forceinline__ uint32_t narrow(float f) { return __builtin_bit_cast(uint32_t, f); }
 };
-struct Bf16 {
+struct Half16 {
     static constexpr int V = 8;
     typedef uint16_t elem;
-    static __device__ __forceinline__ float wide(uint16_t v) { return gqd::bf2f(v); }
-    static __device__ __forceinline__ uint16_t narrow(float v) { return gqd::f2bf(v); }
+    static __device__ __forceinline__ uint16_t bits(const u32x4& v, int i) {
+        return (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+    }
 };
-struct F16 {
-    static constexpr int V = 8;
-    typedef uint16_t elem;
-    static __device__ __forceinline__ float wide(uint16_t v) { return gqd::h2f(v); }
-    static __device__ __forceinline__ uint16_t narrow(float v) { return gqd::f2h(v); }
+struct Bf16 : Half16 {
+    static __device__ __forceinline__ float get(const u32x4& v, int i) {
+        const uint32_t u = i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16;
+        return __builtin_bit_cast(float, u);
+    }
+    static __device__ __forceinline__ uint16_t narrow(float f) { return gqd::f2bf(f); }
+};
+struct F16 : Half16 {
+    static __device__ __forceinline__ float get(const u32x4& v, int i) { return gqd::h2f(bits(v, i)); }
+    static __device__ __forceinline__ uint16_t narrow(float f) { return gqd::f2h(f); }
 };
 
-// N elements from p, of which the first `left` are a row's (the others zeros, not
-// read); rows start at any element, which vector memory instructions allow.
-template <int N, typename E>
-__device__ __forceinline__ void read(const E* p, int64_t left, E (&v)[N]) {
+// 16 bytes of a row from p, of whose elements `left` are the row's (the others zeros,
+// not read, not written); rows start at any element, which vector memory instructions
+// allow.  (The asm keeps the two ways apart, which would else share narrow loads.)
+template <typename E>
+__device__ __forceinline__ u32x4 read16(const E* p, int64_t left) {
+    constexpr int N = 16 / sizeof(E);
+    u32x4 v{};
     if (left >= N) {
-        __builtin_memcpy(v, p, sizeof(v));
+        __builtin_memcpy(&v, p, 16);
     } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = i < left ? p[i] : E(0);
-    }
-}
-template <int N, typename E>
-__device__ __forceinline__ void write(E* p, int64_t left, const E (&v)[N]) {
-    if (left >= N) {
-        __builtin_memcpy(p, v, sizeof(v));
-    } else {
+        __asm__ volatile("" : "+v"(p));
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i < left) p[i] = v[i];
+            if (i < left) v[i * sizeof(E) / 4] |= (uint32_t)p[i] << (i * sizeof(E) % 4 * 8);
+    }
+    return v;
+}
+template <typename E>
+__device__ __forceinline__ void write16(E* p, int64_t left, const u32x4& v) {
+    constexpr int N = 16 / sizeof(E);
+    if (left >= N) {
+        __builtin_memcpy(p, &v, 16);
+    } else {
+        __asm__ volatile("" : "+v"(p));
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < left) p[i] = (E)(v[i * sizeof(E) / 4] >> (i * sizeof(E) % 4 * 8));
+    }
+}
+// N values as type T from p on.
+template <typename T, int N>
+__device__ __forceinline__ void write_as(typename T::elem* p, int64_t left, const float (&f)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; k += T::V) {
+        u32x4 v{};
+#pragma unroll
+        for (int i = 0; i < T::V; ++i)
+            v[i * 4 / T::V] |= (uint32_t)T::narrow(f[k + i]) << (T::V == 8 ? 16 * (i & 1) : 0);
+        if (k < left) write16(p + k, left - k, v);
     }
 }
 
@@ -156,62 +185,66 @@ __device__ __forceinline__ int64_t row_of(const int32_t* __restrict__ place, int
     return p >= 0 && p < S ? p : -1;
 }
 
-// A wavefront copies 1 KB of one token's row to its slots' places.  pieces: of a
-// row.
+// A wavefront's pieces of 1 KB of the tokens' rows, `pieces` a row: f(t, d) with the
+// token and this lane's first element.
+template <int V, typename F>
+__device__ __forceinline__ void each_piece(int n_tokens, int64_t D, int64_t pieces, F f) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int64_t i = (int64_t)blockIdx.x * 4 + wave; i < pieces * n_tokens; i += (int64_t)gridDim.x * 4) {
+        const int64_t t = i / pieces, d = ((i - t * pieces) * 64 + (threadIdx.x & 63)) * V;
+        if (d < D) f(t, d);
+    }
+}
+
+// Copies each piece to the places of the token's slots.
 template <typename T>
 __global__ __launch_bounds__(256) void k_gather(const typename T::elem* __restrict__ x, int n_tokens, int top_k,
                                                 int64_t D, int64_t ldx, const int32_t* __restrict__ place,
                                                 typename T::elem* __restrict__ xs, int64_t ldxs, int64_t pieces) {
-    const int64_t i = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t = i / pieces, d = ((i - t * pieces) * 64 + (threadIdx.x & 63)) * T::V;
-    if (t >= n_tokens || d >= D) return;
     const int64_t S = (int64_t)n_tokens * top_k;
-    typename T::elem v[T::V];
-    read(x + t * ldx + d, D - d, v);
+    each_piece<T::V>(n_tokens, D, pieces, [&](int64_t t, int64_t d) {
+        const u32x4 v = read16(x + t * ldx + d, D - d);
 #pragma unroll 8
-    for (int j = 0; j < top_k; ++j) {
-        const int64_t p = row_of(place, t * top_k + j, S);
-        if (p >= 0) write(xs + p * ldxs + d, D - d, v);
-    }
+        for (int j = 0; j < top_k; ++j) {
+            const int64_t p = row_of(place, t * top_k + j, S);
+            if (p >= 0) write16(xs + p * ldxs + d, D - d, v);
+        }
+    });
 }
 
-// A wavefront adds up 1 KB of one token's slots' rows, in their order.
+// Adds up a piece of the token's slots' rows, in their order.
 template <typename T, typename Y>
 __global__ __launch_bounds__(256) void k_combine(const typename T::elem* __restrict__ ys, int n_tokens, int top_k,
                                                  int64_t D, int64_t ldys, const int32_t* __restrict__ place,
                                                  const float* __restrict__ w, typename Y::elem* __restrict__ y,
                                                  int64_t ldy, int64_t pieces) {
-    const int64_t i = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t = i / pieces, d = ((i - t * pieces) * 64 + (threadIdx.x & 63)) * T::V;
-    if (t >= n_tokens || d >= D) return;
     const int64_t S = (int64_t)n_tokens * top_k;
-    float sum[T::V];
+    each_piece<T::V>(n_tokens, D, pieces, [&](int64_t t, int64_t d) {
+        float sum[T::V];
 #pragma unroll
-    for (int e = 0; e < T::V; ++e) sum[e] = 0.0f;
-    constexpr int U = 8;  // rows on their way at once
-    for (int j0 = 0; j0 < top_k; j0 += U) {
-        typename T::elem v[U][T::V];
-        float f[U];
-        bool ok[U];
+        for (int e = 0; e < T::V; ++e) sum[e] = 0.0f;
+        constexpr int U = 8;  // rows on their way at once
+        for (int j0 = 0; j0 < top_k; j0 += U) {
+            u32x4 v[U];
+            float f[U];
+            bool ok[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = j0 + u < top_k ? j0 + u : top_k - 1;
-            const int64_t p = row_of(place, t * top_k + j, S);
-            ok[u] = p >= 0 && j0 + u < top_k;
-            f[u] = w ? w[t * top_k + j] : 1.0f;
-            if (ok[u]) read(ys + p * ldys + d, D - d, v[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (ok[u]) {
-#pragma unroll
-                for (int e = 0; e < T::V; ++e) sum[e] = __builtin_fmaf(f[u], T::wide(v[u][e]), sum[e]);
+            for (int u = 0; u < U; ++u) {
+                const int j = j0 + u < top_k ? j0 + u : top_k - 1;
+                const int64_t p = row_of(place, t * top_k + j, S);
+                ok[u] = p >= 0 && j0 + u < top_k;
+                f[u] = w ? w[t * top_k + j] : 1.0f;
+                if (ok[u]) v[u] = read16(ys + p * ldys + d, D - d);
             }
-    }
-    typename Y::elem out[T::V];
 #pragma unroll
-    for (int e = 0; e < T::V; ++e) out[e] = Y::narrow(sum[e]);
-    write(y + t * ldy + d, D - d, out);
+            for (int u = 0; u < U; ++u)
+                if (ok[u]) {
+#pragma unroll
+                    for (int e = 0; e < T::V; ++e) sum[e] = __builtin_fmaf(f[u], T::get(v[u], e), sum[e]);
+                }
+        }
+        write_as<Y>(y + t * ldy + d, D - d, sum);
+    });
 }
 
 // A workgroup has one token, its four wavefronts 1 KB pieces of the row in turn.
@@ -238,25 +271,30 @@ __global__ __launch_bounds__(256) void k_combine_grad(const typename T::elem* __
             sum[u] = 0.0f;
         }
         for (int64_t d = ((int64_t)wave * 64 + lane) * T::V; d < D; d += 256 * T::V) {
-            typename T::elem g[T::V], v[U][T::V];
-            read(dy + t * lddy + d, D - d, g);
+            const u32x4 g = read16(dy + t * lddy + d, D - d);
+            u32x4 v[U];
             if (dw) {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (p[u] >= 0) read(ys + p[u] * ldys + d, D - d, v[u]);
+                    if (p[u] >= 0) v[u] = read16(ys + p[u] * ldys + d, D - d);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (p[u] < 0) continue;
                 if (dw) {
 #pragma unroll
-                    for (int e = 0; e < T::V; ++e) sum[u] = __builtin_fmaf(T::wide(g[e]), T::wide(v[u][e]), sum[u]);
+                    for (int e = 0; e < T::V; ++e) sum[u] = __builtin_fmaf(T::get(g, e), T::get(v[u], e), sum[u]);
                 }
                 if (dys) {
-                    typename T::elem out[T::V];
+                    typename T::elem* q = dys + p[u] * lddys + d;
+                    if (w) {
+                        float out[T::V];
 #pragma unroll
-                    for (int e = 0; e < T::V; ++e) out[e] = w ? T::narrow(f[u] * T::wide(g[e])) : g[e];
-                    write(dys + p[u] * lddys + d, D - d, out);
+                        for (int e = 0; e < T::V; ++e) out[e] = f[u] * T::get(g, e);
+                        write_as<T>(q, D - d, out);
+                    } else {
+                        write16(q, D - d, g);
+                    }
                 }
             }
         }
@@ -280,8 +318,11 @@ int64_t pieces_of(int64_t D) {
     return (D + 64 * T::V - 1) / (64 * T::V);
 }
 
-// (a launch has at most 2^32 threads: 2^40 elements are at most 2^31 pieces of 512)
-dim3 grid_of(int64_t pieces) { return dim3((unsigned)((pieces + 3) / 4)); }
+// (a launch has at most 2^32 threads: beyond, the workgroups go round again)
+dim3 grid_of(int64_t pieces) {
+    constexpr int64_t MOST = (int64_t)1 << 23;
+    return dim3((unsigned)((pieces + 3) / 4 < MOST ? (pieces + 3) / 4 : MOST));
+}
 
 template <typename T>
 hipError_t gather(const void* x, int n_tokens, int top_k, int64_t D, int64_t ldx, const int32_t* place, void* xs,
