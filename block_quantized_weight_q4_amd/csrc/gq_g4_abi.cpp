@@ -76,7 +76,8 @@ gq_status gq_g4_matmul(const void* W, const void* scales, gq_dtype s_dtype, cons
     gq_status st = check_weights(s_dtype, group, N, K);
     if (st == GQ_OK) st = check_rows(N, K, M, n_experts, offsets);
     if (st != GQ_OK) return st;
-    if (ldx < K || ldy < N || !fits(M, ldx) || !fits(M, ldy)) return GQ_ERR_SHAPE;
+    // (128 rows of X are addressed in 31 bits)
+    if (ldx < K || ldx > MAX_K || ldy < N || !fits(M, ldx) || !fits(M, ldy)) return GQ_ERR_SHAPE;
     if (M == 0 || N == 0) return GQ_OK;
     if (!Y || (K > 0 && (!W || !scales || !X))) return GQ_ERR_NULL;
     if (!aligned16(Y) || !aligned16(offsets) ||

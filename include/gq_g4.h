@@ -54,9 +54,9 @@ gq_status gq_g4_matvec(const void* W, const void* scales, gq_dtype s_dtype, cons
 
 /* Product of many rows: Y[m][n] = sum_k w(n, k) X[m][k], with offsets by the
  * weights of row m's expert.  X: [M][ldx] of x_dtype (GQ_BF16 or GQ_F16; rows
- * start 16-byte aligned: ldx a multiple of 8), Y: [M][ldy] of y_dtype (GQ_F32
- * or x_dtype), any ldy >= N.  M == 0 or N == 0 is a no-op; K == 0 writes zeros.
- * Columns past N are not touched.
+ * start 16-byte aligned: ldx a multiple of 8, at most 4,194,304), Y: [M][ldy] of
+ * y_dtype (GQ_F32 or x_dtype), any ldy >= N.  M == 0 or N == 0 is a no-op; K == 0
+ * writes zeros.  Columns past N are not touched.
  * Accuracy.  GQ_F32: as gq_g4_matvec.  Y of X's type: that, or each weight
  * rounded to that type first (by the number of rows), i.e. within half its eps
  * (bf16 2^-8, fp16 2^-11, and 2^-25 |x| where a weight is below fp16's normal

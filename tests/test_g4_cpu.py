@@ -84,6 +84,7 @@ def test_matmul_validation(lib):
     for p in "XY":
         assert c(**{p: None}) == NULL and c(**{p: MIS}) == ALIGN
     assert c(off=MIS) == ALIGN and c(ldx=260) == ALIGN
+    assert c(ldx=(1 << 22) + 8) == SHAPE and c(ldx=1 << 22, M=0) == OK  # (rows of a tile are addressed in 31 bits)
     assert c(M=0) == OK and c(N=0) == OK and c(M=0, E=4, off=A) == OK
 
 
