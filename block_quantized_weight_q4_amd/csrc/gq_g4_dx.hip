@@ -10,6 +10,7 @@
 
 #include "gq_f8_stream.h"
 #include "gq_g4_device.h"
+#include "gq_g4_dx_stream.h"
 #include "gq_g4_internal.h"
 #include "gq_g4_tile.h"
 
@@ -59,6 +60,7 @@ struct Tile {
         // W.  The four rows, 8 apart, that the lanes read at once have to be in different
         // banks.  KS = 1: rows of 128 bytes, whose 32-byte pieces are exchanged by r / 8;
         // KS = 2: rows of 64 bytes, row 32 h + 8 a + b of the stage at 32 h + 4 b + a.
+        u32x4 held[DMA ? 1 : XI];  // rows on their way through registers
         auto load = [&](int s) __attribute__((always_inline)) {
             uint8_t* d = smem + (s % STAGES) * STAGE;
             const int64_t n = (int64_t)s * BK;
@@ -81,7 +83,7 @@ struct Tile {
                         for (int i = 0; i < 8; ++i)
                             if (xchunk + i < left) v[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
                     }
-                    reinterpret_cast<u32x4*>(l)[lane] = v;
+                    held[u] = v;
                 }
             }
             const Rsrc wr = make_rsrc(wt.W + n * row_bytes + k0 / 2, left ? left * row_bytes - k0 / 2 : 0);
@@ -98,6 +100,14 @@ struct Tile {
                 }
                 copy16(wr, within((uint32_t)(r * row_bytes) + chunk, chunk, (int)(K - k0 < BN ? K - k0 : BN) / 2),
                        d + XB + (wave + 4 * u) * 1024);
+            }
+        };
+        // what the last load brought (its stage's copies, WI, are younger)
+        auto put_rows = [&](int s) __attribute__((always_inline)) {
+            if constexpr (!DMA) {
+                uint8_t* d = smem + (s % STAGES) * STAGE;
+#pragma unroll
+                for (int u = 0; u < XI; ++u) reinterpret_cast<u32x4*>(d + (wave + 4 * u) * 1024)[lane] = held[u];
             }
         };
         // Scales: lane l has row n + l of the stage; as 512 s and -z s in LDS, [group][row].
@@ -155,19 +165,7 @@ struct Tile {
         };
         // rows 2 i and 2 i + 1 of the operands of the four columns
         auto expand = [&](u32x4 (&a)[4], int i) __attribute__((always_inline)) {
-            // (joined by a byte permute: a read into the upper half of a register waits for the lower one's)
-            const uint32_t v = __builtin_amdgcn_perm(w[i][1], w[i][0], 0x05040100u);
-            const int lo = (int)(v & 0x0f0f0f0fu), hi = (int)((v >> 4) & 0x0f0f0f0fu);
-            const gqf8::f32x2 e0 = __builtin_amdgcn_cvt_pk_f32_fp8(lo, false);
-            const gqf8::f32x2 e1 = __builtin_amdgcn_cvt_pk_f32_fp8(lo, true);
-            const gqf8::f32x2 o0 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, false);
-            const gqf8::f32x2 o1 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, true);
-            auto f0 = [&](float q) { return __builtin_fmaf(q, f[i][0], f[i][1]); };
-            auto f1 = [&](float q) { return __builtin_fmaf(q, f[i][2], f[i][3]); };
-            a[0][i] = T::pack(f0(e0.x), f1(e1.x));
-            a[1][i] = T::pack(f0(o0.x), f1(o1.x));
-            a[2][i] = T::pack(f0(e0.y), f1(e1.y));
-            a[3][i] = T::pack(f0(o0.y), f1(o1.y));
+            weights_2x4<T>(w[i][0], w[i][1], f[i], a, i);
         };
         // A half of a stage (KS = 2: this wavefront's), whose operands a and rows b are in
         // registers: the next half's operands are formed while these are multiplied, its
@@ -178,12 +176,15 @@ struct Tile {
         if (S > 0) {
             load_scales(0, sc);
 #pragma unroll
-            for (int s = 0; s < STAGES - 1; ++s) load(s);
+            for (int s = 0; s < STAGES - 1; ++s) {
+                load(s);
+                put_rows(s);
+            }
             put_scales(0, sc);
             load_scales(1, sc);
             load(STAGES - 1);  // (the same order as in the loop, for the waits that the compiler counts)
             if constexpr (DMA) wait_copies<(STAGES - 1) * (XI + WI) + 4>();
-            else wait_copies<0>();
+            else wait_copies<0>();  // (the rows' loads are not counted: at an end there are others)
             gqd::lds_barrier();
             u32x4 a[4];
             typename T::x8 b[MT];
@@ -204,8 +205,10 @@ struct Tile {
                     if (last) {
                         // until stage s + 1 has landed: the copies of s + 2 and four loads of
                         // scales are younger
+                        // (the register form: all but the copies of s + 2, so that its rows are there too)
                         if constexpr (DMA) wait_copies<(STAGES - 2) * (XI + WI) + 4>();
-                        else wait_copies<0>();
+                        else wait_copies<WI>();
+                        put_rows(s + 2);
                         put_scales(s + 1, sc);
                         load_scales(s + 2, sc);
                         gqd::lds_barrier();
@@ -328,6 +331,46 @@ __global__ __launch_bounds__(256, 2) void k_g4_dx(G4Weights wt, Rows a, int gm, 
     U::run(w, dy, a.lddy, t.rows, dx, a.lddx, (int64_t)tn * U::BN, smem);
 }
 
+// Workgroup: columns blockIdx.x % gn, row tile / gn.
+template <typename T, int MT, int W, int H>
+__global__ __launch_bounds__(64 * W) void k_g4_dx_few(G4Weights wt, Rows a, int gm, int gn) {
+    using U = DxStream<MT, W, H>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    RowTile t{0, 0, 0};
+    int tn = 0;
+    if (a.offsets) {
+        auto pick = [&](int total) {
+            const int64_t real = (int64_t)(total < gm ? total : gm) * gn;
+            if (blockIdx.x >= real) return -1;
+            const int id = xcd_order(blockIdx.x, (int)real);
+            tn = id % gn;
+            return id / gn;
+        };
+        if (!tile_of(a.offsets, a.n_experts, a.M, U::BM, pick, t)) return;
+    } else {
+        const int id = xcd_order(blockIdx.x, gm * gn);
+        tn = id % gn;
+        t.row0 = (int64_t)(id / gn) * U::BM;
+        t.rows = a.M - t.row0 < U::BM ? (int)(a.M - t.row0) : U::BM;
+    }
+    dx_stream<T, MT, W, H>(of_expert(wt, t.e), a.dY + t.row0 * a.lddy, a.lddy, t.rows, a.dX + t.row0 * a.lddx, a.lddx,
+                           (int64_t)tn * U::BN, smem);
+}
+
+template <typename T, int MT, int W, int H>
+hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
+    using U = DxStream<MT, W, H>;
+    const int64_t gm = a.offsets ? most_tiles(a.M, a.n_experts, U::BM) : (a.M + U::BM - 1) / U::BM;
+    const int64_t gn = (w.K + U::BN - 1) / U::BN;
+    if (!grid_ok(gm * gn, 64 * W)) return hipErrorInvalidValue;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_dx_few<T, MT, W, H>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_g4_dx_few<T, MT, W, H>), dim3((unsigned)(gm * gn)), dim3(64 * W), U::BYTES, s, w, a, (int)gm,
+                       (int)gn);
+    return hipGetLastError();
+}
+
 template <typename T, int MT, int KS, bool DMA>
 hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
     using U = Tile<T, MT, KS, DMA>;
@@ -345,20 +388,31 @@ hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
 // Shape of the tiles (us; rows x sum x columns).  128 x 256 where they fill half of the
 // CUs (24,120 rows of 128 experts x 704 x 2816: 149, 64 rows 187; 1024 x 17408 x 5120:
 // 317, 64 rows 354); otherwise more and smaller ones with the sum in two halves: 64 x
-// 128 (256 x 17408 x 5120: 168, 128 x 256 314), for up to 32 rows 32 x 128 (16 x 9728 x
-// 2560: 78, 32 x 256 115, 64 x 128 87), unless there are enough of 32 x 256 (2048 rows
-// of 128 experts x 704 x 2816: 49, 32 x 128 59, 64 x 256 56).
+// 128 (256 x 17408 x 5120: 168, 128 x 256 314); up to 32 rows of many experts 32 x 256
+// (2048 rows of 128 experts x 704 x 2816: 49, 64 x 256 56).  Rows that go through
+// registers leave none for 128.
 template <typename T, bool DMA>
 hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
     const int64_t per = a.M / a.n_experts;  // rows an expert has
     auto tiles = [&](int64_t rows) { return (per / rows + 1) * (a.n_experts < a.M ? a.n_experts : a.M) * ((w.K + 255) / 256); };
-    if (per <= 32) return tiles(32) >= 256 ? launch<T, 2, 1, DMA>(w, a, s) : launch<T, 2, 2, DMA>(w, a, s);
+    if (per <= 32) return launch<T, 2, 1, DMA>(w, a, s);
     if (tiles(128) < 128) return launch<T, 4, 2, DMA>(w, a, s);
-    return per <= 64 ? launch<T, 4, 1, DMA>(w, a, s) : launch<T, 8, 1, DMA>(w, a, s);
+    if constexpr (DMA) {
+        if (per > 64) return launch<T, 8, 1, DMA>(w, a, s);
+    }
+    return launch<T, 4, 1, DMA>(w, a, s);
 }
 
 template <typename T>
 hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
+    // Few rows (us; sum x columns): streamed by 16 wavefronts with 16 rows where there are few
+    // workgroups (16 rows x 17408 x 5120: 53, four wavefronts with 32 rows 61, tiles 139; x
+    // 9728 x 2560: 28, 36, 78), by four with 32 rows up to two a CU (32 x 2560 x 9728: 14, 16 of
+    // 16 23, tiles 24; 128 x 17408 x 5120: 111, 142, 158; 256 x 17408 x 5120: 182, 259, 158).
+    const int64_t per = (a.M + a.n_experts - 1) / a.n_experts, experts = a.n_experts < a.M ? a.n_experts : a.M;
+    auto groups = [&](int64_t rows) { return (per + rows - 1) / rows * experts * ((w.K + 63) / 64); };
+    if (groups(16) <= 256) return few<T, 1, 16, 2>(w, a, s);
+    if (groups(32) <= 512) return few<T, 2, 4, 2>(w, a, s);
     // (copies address eight rows in 31 bits)
     return w.N % 8 == 0 && a.lddy % 8 == 0 && a.lddy < (1 << 26) ? launch<T, true>(w, a, s) : launch<T, false>(w, a, s);
 }
