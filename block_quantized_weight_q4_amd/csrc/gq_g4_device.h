@@ -106,5 +106,19 @@ __device__ __forceinline__ void store_as(void* p, int64_t i, int dtype, float v)
     if (dtype == gqd::DT_F32) static_cast<float*>(p)[i] = v;
     else static_cast<uint16_t*>(p)[i] = dtype == gqd::DT_BF16 ? gqd::f2bf(v) : gqd::f2h(v);
 }
+// The first c of four neighbours (of any alignment).
+__device__ __forceinline__ void store_as(void* p, int64_t i, int dtype, f32x4 v, int c) {
+    if (c < 4) {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < c) store_as(p, i + e, dtype, v[e]);
+    } else if (dtype == gqd::DT_F32) {
+        __builtin_memcpy(static_cast<float*>(p) + i, &v, 16);
+    } else {
+        const u32x2 o = dtype == gqd::DT_BF16 ? u32x2{Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3])}
+                                              : u32x2{F16::pack(v[0], v[1]), F16::pack(v[2], v[3])};
+        __builtin_memcpy(static_cast<uint16_t*>(p) + i, &o, 8);
+    }
+}
 
 }  // namespace gqg4

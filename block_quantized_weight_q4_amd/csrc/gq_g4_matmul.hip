@@ -45,8 +45,8 @@ __global__ __launch_bounds__(64 * W) void k_g4_few(G4Weights wt, Rows a, int gn,
     const int y_dtype = a.y_f32 ? gqd::DT_F32 : X::dtype;
     stream_tile<X, ZP, G, NT, W, XR>(of_expert(wt, t.e), (id - tm * gn) * (16 * NT),
                                      static_cast<const uint16_t*>(a.X) + t.row0 * a.ldx, a.ldx, t.rows, smem,
-                                     [&](int i, int64_t n, float v) {
-                                         store_as(a.Y, (t.row0 + i) * a.ldy + n, y_dtype, v);
+                                     [&](int i, int64_t n, f32x4 v, int c) {
+                                         store_as(a.Y, (t.row0 + i) * a.ldy + n, y_dtype, v, c);
                                      });
 }
 
@@ -279,7 +279,6 @@ struct Tile {
         }
         wait_copies<0>();
         // lane: columns 16 fq .. + 15 of the tiles of row 32 j + fr
-        const bool vec = (ldy & (y_f32 ? 3 : 7)) == 0;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             const int row = 32 * j + fr;
@@ -292,8 +291,9 @@ struct Tile {
                     float* p = static_cast<float*>(y) + row * ldy + n;
 #pragma unroll
                     for (int r = 0; r < 16; r += 4) {
-                        if (vec && n + r + 4 <= N) {
-                            *reinterpret_cast<f32x4*>(p + r) = f32x4{v[r], v[r + 1], v[r + 2], v[r + 3]};
+                        if (n + r + 4 <= N) {
+                            const f32x4 o{v[r], v[r + 1], v[r + 2], v[r + 3]};
+                            __builtin_memcpy(p + r, &o, 16);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
@@ -304,10 +304,10 @@ struct Tile {
                     uint16_t* p = static_cast<uint16_t*>(y) + row * ldy + n;
 #pragma unroll
                     for (int r = 0; r < 16; r += 8) {
-                        if (vec && n + r + 8 <= N) {
-                            *reinterpret_cast<u32x4*>(p + r) =
-                                u32x4{T::pack(v[r], v[r + 1]), T::pack(v[r + 2], v[r + 3]),
-                                      T::pack(v[r + 4], v[r + 5]), T::pack(v[r + 6], v[r + 7])};
+                        if (n + r + 8 <= N) {
+                            const u32x4 o{T::pack(v[r], v[r + 1]), T::pack(v[r + 2], v[r + 3]),
+                                          T::pack(v[r + 4], v[r + 5]), T::pack(v[r + 6], v[r + 7])};
+                            __builtin_memcpy(p + r, &o, 16);  // (of any alignment)
                         } else {
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
@@ -412,12 +412,21 @@ hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
 // matrix: up to 16 rows 32 by 16 by 4 (17408 x 5120: 20.7, 32 by 32 by 4 25.9), of up
 // to 4096 columns 16 by 16 by 4 (2560 x 9728: 9.3 and 12.5); more rows 32 by 32 by 4,
 // which reads W half as often (1024 rows of 17408 x 5120: 425, 32 by 16 by 4 540).
+// Where there are thousands of workgroups, nothing is left to split: one wavefront a
+// workgroup, 32 by 32 (3015 rows of 2816 x 2816: 110, by 4 132; of 2816 x 256 27 and 58;
+// 1024 of 2560 x 9728, 2560 workgroups, 127 and 115), then 64 by 32 (3015 of 17408 x
+// 5120: 1100, 32 by 32 1155; 100,000 of 128 x 4096, bound by X, 281 and 505).
 template <typename X, bool ZP, int G>
 hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
     const int64_t per = a.M / a.n_experts;  // rows an expert has
     if (a.n_experts > 1 && per <= 2) return few<X, ZP, G, 2, 2, 4>(w, a, s);
     if (a.n_experts > 1 && per <= 64) return few<X, ZP, G, 2, 2, 16>(w, a, s);
-    if (per > 16) return few<X, ZP, G, 2, 4, 32>(w, a, s);
+    if (per > 16) {
+        const int64_t gm = a.offsets ? most_tiles(a.M, a.n_experts, 32) : (a.M + 31) / 32;
+        if (gm * ((w.N + 63) / 64) >= 5120) return few<X, ZP, G, 4, 1, 32>(w, a, s);
+        if (gm * ((w.N + 31) / 32) >= 4096) return few<X, ZP, G, 2, 1, 32>(w, a, s);
+        return few<X, ZP, G, 2, 4, 32>(w, a, s);
+    }
     if (w.N <= 4096) return few<X, ZP, G, 1, 4, 16>(w, a, s);
     return few<X, ZP, G, 2, 4, 16>(w, a, s);
 }

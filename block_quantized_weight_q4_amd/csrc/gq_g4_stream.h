@@ -49,13 +49,14 @@ struct StreamSize {
     static constexpr int PARTS_AT = 1024 * (WI + XI);
     static constexpr int BYTES = PARTS_AT + (SHARE ? 3 * XR * 512 : 0);
     static constexpr int MT = XR > 16 ? XR / 16 : 1;   // operands of rows of X
-    static constexpr int JOIN = 1024 * NT * MT;
+    static constexpr int JOIN_ROW = 20;  // floats: a tile's 16 and a gap, so that rows 4 apart lie in other banks
+    static constexpr int JOIN = 64 * JOIN_ROW * NT * MT;
     static_assert(XR * ROW % 1024 == 0, "whole copies");
 };
 
 // Rows [row0, row0 + rows) of X (1 <= rows <= XR; rows past them repeat the
 // last), the 16 NT rows of W from n0.  smem: W * max(BYTES, JOIN) bytes.
-// store(i, n, v): element (row i < rows, n < N).
+// store(i, n, v, c): elements n .. n + c - 1 of row i < rows (1 <= c <= 4).
 template <typename X, bool ZP, int G, int NT, int W, int XR, typename Store>
 __device__ __forceinline__ void stream_tile(const G4Weights& wt, int64_t n0, const void* __restrict__ Xp,
                                             int64_t ldx, int rows, uint8_t* smem, Store store) {
@@ -237,27 +238,32 @@ __device__ __forceinline__ void stream_tile(const G4Weights& wt, int64_t n0, con
     }
     wait_copies<0>();
     __syncthreads();
-    // the join: partial sums of every wavefront, added in their order
-    constexpr int TILES = NT * MT;
-    f32x4* part = reinterpret_cast<f32x4*>(smem);
+    // the join: partial sums of every wavefront, added in their order, by rows, four
+    // columns a thread
+    constexpr int TILES = NT * MT, JR = S::JOIN_ROW;
+    float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int j = 0; j < MT; ++j) part[(wave * TILES + i * MT + j) * 64 + lane] = acc[i][j];
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                part[((wave * TILES + i * MT + j) * 16 + 4 * fq + r) * JR + fr] = acc[i][j][r];
     __syncthreads();
-    for (int c = wave; c < TILES; c += W) {
-        f32x4 v = part[c * 64 + lane];
+#pragma unroll
+    for (int u = 0; u < (TILES + W - 1) / W; ++u) {
+        const int at = u * (64 * W) + (int)threadIdx.x, row = at / (4 * NT), four = at % (4 * NT);
+        const int64_t n = n0 + 4 * four;
+        if (row >= rows || n >= N) continue;
+        const float* p = part + (((four >> 2) * MT + (row >> 4)) * 16 + (row & 15)) * JR + 4 * (four & 3);
+        f32x4 v = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll
         for (int w = 1; w < W; ++w) {
-            const f32x4 o = part[(w * TILES + c) * 64 + lane];
+            const f32x4 o = *reinterpret_cast<const f32x4*>(p + w * (TILES * 16 * JR));
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] += o[r];
         }
-        const int64_t n = n0 + 16 * (c / MT) + fr;
-        const int row = 16 * (c % MT) + 4 * fq;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (row + r < rows && n < N) store(row + r, n, v[r]);
+        store(row, n, v, N - n < 4 ? (int)(N - n) : 4);
     }
 }
 

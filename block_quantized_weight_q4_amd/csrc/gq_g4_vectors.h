@@ -17,7 +17,7 @@ __global__ __launch_bounds__(64 * W) void k_g4_vectors(G4Weights wt, const void*
     using S = StreamSize<X, NT, XR>;
     __shared__ __align__(16) uint8_t smem[W * (S::BYTES > S::JOIN ? S::BYTES : S::JOIN)];
     stream_tile<X, ZP, G, NT, W, XR>(wt, (int64_t)blockIdx.x * (16 * NT), x, wt.K, batch, smem,
-                                     [&](int i, int64_t n, float v) { store_as(y, i * wt.N + n, y_dtype, v); });
+                                     [&](int i, int64_t n, f32x4 v, int c) { store_as(y, i * wt.N + n, y_dtype, v, c); });
 }
 
 // (at most MOST wavefronts: as many as 160 KB of LDS hold)
