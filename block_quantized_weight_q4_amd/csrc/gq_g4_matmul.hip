@@ -82,7 +82,7 @@ struct Tile {
     static constexpr int XI = BM / 8 / NW, WI = 2 * NT;  // copies of a wavefront
     static constexpr int PANEL = 32 * NT * 8;         // scales of a wavefront
     static constexpr int W_AT = XS * XB, P_AT = W_AT + 2 * WB, BYTES = P_AT + NW * PANEL;
-    static_assert(BM % (8 * NW) == 0 && NT <= 2, "whole copies, a lane a column");
+    static_assert(BM % (8 * NW) == 0 && NT == 2, "whole copies, a lane a column");
 
     // x: first row of the tile; n0: first column
     static __device__ __forceinline__ void run(const G4Weights& wt, const uint16_t* __restrict__ x, int64_t ldx,
@@ -176,26 +176,27 @@ struct Tile {
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[i][j] = f32x16{};
-        // Operand c of a stage: the 16 inputs of its step c / NT (eight of them a lane:
-        // chunk 2 (c / NT) + fq of X, dword 2 (c / NT % 2) + fq of W's chunk), tile c % NT.
+        // Operand c of a stage: the 16 inputs of its step t = c / 2 (eight of them a lane: dword
+        // 2 fq + t % 2 of W's chunk t / 2, so that one read brings those of two steps, and
+        // chunk 4 (t / 2) + 2 fq + t % 2 of X), tile c % 2.
         // Row a = l % 32 of a tile of W is its column 16 (a / 4 % 2) + 4 (a / 8) + a % 4, so
         // that a lane ends up with 16 neighbouring columns of one row of Y.
         const int wcol = 16 * ((fr >> 2) & 1) + 4 * (fr >> 3) + (fr & 3), wr16 = wcol & 15;
-        const int wbase = W_AT + 1024 * (WI * wave + (wcol >> 4)) + 64 * wr16 + 4 * fq;
+        const int wbase = W_AT + 1024 * (WI * wave + (wcol >> 4)) + 64 * wr16 + 8 * fq;
         int w_half[4];
 #pragma unroll
         for (int h = 0; h < 4; ++h) w_half[h] = wbase + 16 * (h ^ (wr16 >> 2));
         int x_step[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) x_step[t] = gqf8::pos128(fr, 2 * t + fq);
+        for (int t = 0; t < 4; ++t) x_step[t] = gqf8::pos128(fr, 4 * (t >> 1) + 2 * fq + (t & 1));
         const gqf8::f32x2* pbase = panel + wcol;
         struct Raw {
-            uint32_t w;
+            u32x2 w;  // of two steps
             gqf8::f32x2 s;
         };
-        // (t: step of W's block)
-        auto read_raw = [&](int buf, int t, int i, Raw& r) __attribute__((always_inline)) {
-            r.w = *reinterpret_cast<const uint32_t*>(smem + buf * WB + w_half[t >> 1] + 8 * (t & 1) + 2048 * i);
+        // (h: chunk of W's block, 32 inputs: of one group)
+        auto read_raw = [&](int buf, int h, int i, Raw& r) __attribute__((always_inline)) {
+            r.w = *reinterpret_cast<const u32x2*>(smem + buf * WB + w_half[h] + 2048 * i);
             r.s = pbase[32 * i];
         };
         auto read_x = [&](int buf, int t, int j) __attribute__((always_inline)) {
@@ -224,10 +225,10 @@ struct Tile {
             read_raw(0, 0, 1, r[1]);
 #pragma unroll
             for (int j = 0; j < MT; ++j) b[j] = read_x(0, 0, j);
-            a = weights8<T>(r[0].w, r[0].s.x, r[0].s.y);
+            a = weights8<T>(r[0].w.x, r[0].s.x, r[0].s.y);
             int buf = 0, wb = 0;  // of this stage
             auto stage = [&](int s, auto odd) __attribute__((always_inline)) {
-                constexpr int T0 = odd ? 4 : 0, C = 4 * NT;
+                constexpr int C = 4 * NT;
                 const int nbuf = buf + 1 == XS ? 0 : buf + 1;
                 const int nwb = odd ? wb ^ 1 : wb;
 #pragma unroll
@@ -246,11 +247,11 @@ struct Tile {
                         load_x(s + XS, buf);
                         if constexpr (odd) load_w((s + 3) / 2, wb);
                     }
-                    // (r[(c + 1) % 2] is operand c + 1's)
+                    // (r[(c + 1) % 2] is operand c + 1's, r[c % 2] free from the end of its second step on)
                     const Raw& n = r[(c + 1) & 1];
-                    const typename T::x8 next = weights8<T>(n.w, n.s.x, n.s.y);
-                    if (c + 2 < C) read_raw(wb, T0 + (c + 2) / NT, (c + 2) % NT, r[c & 1]);
-                    else read_raw(nwb, (odd ? 0 : 4) + (c + 2 - C) / NT, (c + 2) % NT, r[c & 1]);
+                    const typename T::x8 next = weights8<T>((c + 1) & 2 ? n.w.y : n.w.x, n.s.x, n.s.y);
+                    const bool fresh = c & 2;
+                    if (fresh) read_raw(c < 4 ? wb : nwb, c < 4 ? (odd ? 3 : 1) : (odd ? 0 : 2), c & 1, r[c & 1]);
                     const bool last = c % NT == NT - 1;  // of its step
 #pragma unroll
                     for (int j = 0; j < MT; ++j) {
@@ -263,7 +264,7 @@ struct Tile {
 #pragma unroll
                     for (int j = 0; j < MT; ++j) {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                // MFMA
-                        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                // LDS reads
+                        if (fresh) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS reads
                         if (last) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                         __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);                // VALU
                         if (c == C - 1) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);  // copies
