@@ -273,10 +273,12 @@ struct Tile {
                 buf = nbuf;
                 wb = nwb;
             };
-            for (int s = 0; s < S; s += 2) {  // (a stage past K adds zeros)
+            int s = 0;
+            for (; s + 1 < S; s += 2) {
                 stage(s, std::false_type{});
                 stage(s + 1, std::true_type{});
             }
+            if (s < S) stage(s, std::false_type{});
         }
         wait_copies<0>();
         // lane: columns 16 fq .. + 15 of the tiles of row 32 j + fr
@@ -367,7 +369,12 @@ __global__ __launch_bounds__(256, 2) void k_g4_tile(G4Weights wt, Rows a, int gm
     void* y = a.y_f32 ? static_cast<void*>(static_cast<float*>(a.Y) + t.row0 * a.ldy)
                       : static_cast<void*>(static_cast<uint16_t*>(a.Y) + t.row0 * a.ldy);
     if constexpr (PARTS > 1) {
-        if (part || (PARTS == 2 && a.offsets && t.rows <= P::BM)) {  // (an expert's last rows)
+        // an expert's last rows
+        if (a.offsets && t.rows > P::BM && t.rows <= 96) {
+            Tile<T, 3, NT>::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
+            return;
+        }
+        if (part || (a.offsets && t.rows <= P::BM)) {
             P::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
             return;
         }
