@@ -94,11 +94,22 @@ __global__ __launch_bounds__(64 * W) void k_g4_dot(G4Weights wt, const float* __
 }
 
 template <bool ZP, int R, int W>
-hipError_t dot(const G4Weights& w, const void* x, void* y, int y_dtype, hipStream_t s) {
-    if (!grid_ok((w.N + R - 1) / R, 64 * W)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_g4_dot<ZP, R, W>), dim3((unsigned)((w.N + R - 1) / R)), dim3(64 * W), 0, s, w,
-                       static_cast<const float*>(x), y, y_dtype);
-    return hipGetLastError();
+hipError_t dot(G4Weights w, const void* x, void* y, int y_dtype, hipStream_t s) {
+    // (a launch has fewer than 2^32 threads)
+    constexpr int64_t MOST = (int64_t)R << 24;
+    const int64_t N = w.N, KG = (w.K + w.group - 1) / w.group;
+    for (int64_t n = 0; n < N; n += MOST) {
+        w.N = N - n < MOST ? N - n : MOST;
+        hipLaunchKernelGGL((k_g4_dot<ZP, R, W>), dim3((unsigned)((w.N + R - 1) / R)), dim3(64 * W), 0, s, w,
+                           static_cast<const float*>(x), y, y_dtype);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        w.W += MOST * (w.K / 2);
+        w.scales += MOST * KG;
+        if (ZP) w.zeros += MOST * KG;
+        y = static_cast<uint8_t*>(y) + MOST * (y_dtype == gqd::DT_F32 ? 4 : 2);
+    }
+    return hipSuccess;
 }
 
 template <bool ZP>

@@ -354,3 +354,20 @@ def test_sort_of_the_most_slots(gq, T, k):
     gq.gq_expert_sort(ids, 4096, off, place)
     want_off, want = P.sort(ids.cpu().numpy(), 4096)
     assert np.array_equal(off.cpu().numpy(), want_off) and np.array_equal(place.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("batch,xdt,ydt", [(1, F32, F32), (1, F32, H), (1, BF, BF), (2, F32, BF), (16, H, H)])
+def test_matvec_of_the_most_rows(gq, batch, xdt, ydt, zeros):
+    """The largest N, more rows than one launch of one fp32 vector has room for."""
+    N, K = 268435200, 32
+    W = torch.randint(0, 256, (N, K // 2), device="cuda", dtype=U8)
+    s = torch.full((N, 1), 0.25, dtype=BF, device="cuda")
+    z = torch.randint(0, 16, (N, 1), device="cuda", dtype=U8) if zeros else None
+    x = torch.randint(-2, 3, (batch, K), generator=gen(batch), device="cuda").to(xdt)
+    y = gq.gq_g4_matvec(W, s, x, poisoned(batch, N, dt=ydt), zeros=z, group=32)
+    assert not y.isnan().any()
+    r = torch.cat([torch.arange(70), torch.arange(2 ** 26 - 40, 2 ** 26 + 40), torch.arange(2 ** 27 - 40, 2 ** 27 + 40),
+                   torch.arange(N - 70, N)]).cuda()
+    ref, _ = P.product(x, P.wide(W[r], s[r], None if z is None else z[r], 32))
+    assert torch.equal(y[:, r], ref.to(ydt))
