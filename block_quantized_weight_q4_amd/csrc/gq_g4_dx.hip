@@ -408,11 +408,13 @@ hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
     // Few rows (us; sum x columns): streamed by 16 wavefronts with 16 rows where there are few
     // workgroups (16 rows x 17408 x 5120: 53, four wavefronts with 32 rows 61, tiles 139; x
     // 9728 x 2560: 28, 36, 78), by four with 32 rows up to two a CU (32 x 2560 x 9728: 14, 16 of
-    // 16 23, tiles 24; 128 x 17408 x 5120: 111, 142, 158; 256 x 17408 x 5120: 182, 259, 158).
+    // 16 23, tiles 24; 128 x 17408 x 5120: 111, 142, 158; 256 x 17408 x 5120: 182, 259, 158);
+    // experts with a row or two, up to eight a CU (96 rows of 128, 2816 x 704: 26, tiles 38;
+    // 96 of 128, 704 x 2816, 4224 workgroups: 35, 22).
     const int64_t per = (a.M + a.n_experts - 1) / a.n_experts, experts = a.n_experts < a.M ? a.n_experts : a.M;
     auto groups = [&](int64_t rows) { return (per + rows - 1) / rows * experts * ((w.K + 63) / 64); };
     if (groups(16) <= 256) return few<T, 1, 16, 2>(w, a, s);
-    if (groups(32) <= 512) return few<T, 2, 4, 2>(w, a, s);
+    if (groups(32) <= (a.n_experts > 1 && per <= 2 ? 2048 : 512)) return few<T, 2, 4, 2>(w, a, s);
     // (copies address eight rows in 31 bits)
     return w.N % 8 == 0 && a.lddy % 8 == 0 && a.lddy < (1 << 26) ? launch<T, true>(w, a, s) : launch<T, false>(w, a, s);
 }
