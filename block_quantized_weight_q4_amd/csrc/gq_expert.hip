@@ -21,7 +21,9 @@ constexpr int MAX_E = 4096;
 // others, so that no workgroup waits for another and one launch does it: the ids
 // are few bytes and come from the caches.  Then it scans the experts, and its
 // wavefronts place their slots one after another: equal ids of a wavefront find
-// each other by a ballot for each bit of the id.
+// each other by a ballot for each bit of the id.  3015 x 8 slots: 7.5 us; 1,048,576 slots
+// 80 to 106 us, bound by every workgroup's reading all 4 MB of ids from its L2 and counting
+// them in LDS (counts of a launch before would halve that, and make every routing two).
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void k_sort(const int32_t* __restrict__ ids, int S, int E, int chunk,
                                                   int32_t* __restrict__ offsets, int32_t* __restrict__ place) {
@@ -196,7 +198,8 @@ __device__ __forceinline__ void each_piece(int n_tokens, int64_t D, int64_t piec
     }
 }
 
-// Copies each piece to the places of the token's slots.
+// Copies each piece to the places of the token's slots.  3015 x 8 slots of 2816 bf16 (153
+// MB): 31 us, the rate of a large copy.
 template <typename T>
 __global__ __launch_bounds__(256) void k_gather(const typename T::elem* __restrict__ x, int n_tokens, int top_k,
                                                 int64_t D, int64_t ldx, const int32_t* __restrict__ place,
@@ -212,7 +215,8 @@ __global__ __launch_bounds__(256) void k_gather(const typename T::elem* __restri
     });
 }
 
-// Adds up a piece of the token's slots' rows, in their order.
+// Adds up a piece of the token's slots' rows, in their order.  3015 x 8 slots of 2816 bf16
+// (153 MB): 31 us, 4.9 TB/s.
 template <typename T, typename Y>
 __global__ __launch_bounds__(256) void k_combine(const typename T::elem* __restrict__ ys, int n_tokens, int top_k,
                                                  int64_t D, int64_t ldys, const int32_t* __restrict__ place,
@@ -249,6 +253,7 @@ __global__ __launch_bounds__(256) void k_combine(const typename T::elem* __restr
 
 // A workgroup has one token, its four wavefronts 1 KB pieces of the row in turn.
 // (dys may be ys: no __restrict__, and a piece is read before it is written)
+// 3015 x 8 slots of 2816 bf16 (289 MB): 64 us, 4.5 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine_grad(const typename T::elem* __restrict__ dy, int n_tokens,
                                                       int top_k, int64_t D, int64_t lddy, const typename T::elem* ys,

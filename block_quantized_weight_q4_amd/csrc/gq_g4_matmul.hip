@@ -69,11 +69,20 @@ __device__ __forceinline__ typename T::x8 weights8(uint32_t w, float s512, float
                                                    T::pack(f(b.x), f(d.x)), T::pack(f(b.y), f(d.y))});
 }
 
-// BM = 16 MT rows of X by BN = 64 NT columns; four wavefronts, each all the rows
+// BM = 32 MT rows of X by BN = 128 NT columns; four wavefronts, each all the rows
 // by a quarter of the columns, so that a weight is expanded by one wavefront only,
 // in registers, right before the matrix instructions that use it.  Both operands go
 // to LDS as they are in memory: X in stages of 64 inputs, W in blocks of two stages
 // (64 bytes a row).
+//
+// Bound by the matrix cores and what they are fed with: 3015 x 17408 x 5120 takes 465 to
+// 482 us (1.12 to 1.15 PFLOP/s; a library's product of the same rows with expanded
+// weights 505, of 8192^3 1.13 to 1.33 PFLOP/s, depending on the card and its heat), with
+// the matrix cores busy 70% of the time and 60% of the issue cycles spent on expanding
+// (20 instructions for eight weights).  Two workgroups a CU hide each other's starts and
+// ends; eight wavefronts in one, 16 x 16 instructions (576 us) and two barriers a stage
+// (703 us) were slower.  Short sums are bound by those starts and by the stores: 24,120
+// rows of 128 experts, 2816 x 704 (11 stages a tile), 141 us, 680 TFLOP/s.
 template <typename T, int MT, int NT>
 struct Tile {
     static constexpr int NW = 4, XS = 2;  // wavefronts, stages of X
@@ -452,7 +461,8 @@ hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
 // 17408 x 5120 with 64 rows 59 and 39, with 256 87 and 114 (about 450 and 950 TFLOP/s
 // where there is enough work); 704 x 2816 of 128 experts with 1024 rows 46 and 42; 2816 x
 // 2816 of 8 with 256 35 and 24, with 1000 41 and 58.  Narrow matrices leave most of a
-// tile's 256 columns empty.
+// tile's 256 columns empty.  (fp32 results carry no rounded weights, and exact ones take
+// the streamed form at any size: 3015 x 17408 x 5120 in 1.13 ms.)
 template <typename X, typename T>
 hipError_t matmul(const G4Weights& w, const Rows& a, hipStream_t s) {
     if (a.y_f32 || w.N < 128 || a.M * w.N < 2500000) return w.zeros ? few<X, true>(w, a, s) : few<X, false>(w, a, s);

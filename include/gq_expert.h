@@ -15,7 +15,10 @@
  * stride >= D and any D (rows whose stride is a multiple of 16 bytes are the
  * fastest).  n_tokens * top_k <= 1,048,576 slots, D <= 268,435,200, an operand
  * at most 2^40 elements (GQ_ERR_SHAPE beyond).  A place outside
- * [0, n_tokens * top_k) stands for a slot without a row.  Every result is the
+ * [0, n_tokens * top_k) stands for a slot without a row; no two slots may have
+ * the same one (gq_expert_sort gives none twice; a result row of two slots is
+ * one of theirs, piece by piece).  Results lie apart from the inputs and from
+ * each other, but for dys, which may be ys.  Every result is the
  * same each time: sums have one order, nothing is added atomically to an output.
  */
 #ifndef GQ_EXPERT_H
