@@ -371,3 +371,60 @@ def test_matvec_of_the_most_rows(gq, batch, xdt, ydt, zeros):
                    torch.arange(N - 70, N)]).cuda()
     ref, _ = P.product(x, P.wide(W[r], s[r], None if z is None else z[r], 32))
     assert torch.equal(y[:, r], ref.to(ydt))
+
+
+def ends(n, k=60):
+    """Positions at both ends of n and around its powers of two."""
+    at = [torch.arange(k), torch.arange(n - k, n)]
+    at += [torch.arange(2 ** b - k, 2 ** b + k) for b in range(10, n.bit_length()) if 2 ** b + k < n]
+    return torch.unique(torch.cat(at)).cuda()
+
+
+@pytest.mark.parametrize("M,N,ydt", [(1, 3, F32), (40, 70, F32), (16, 33, BF), (320, 8000, BF), (100, 300, F32)])
+def test_longest_rows(gq, M, N, ydt):
+    """The largest K and row stride: integers at a few of the inputs, so that results are exact."""
+    K = 4194304
+    g = gen(M, N)
+    W = torch.randint(0, 256, (N, K // 2), device="cuda", dtype=U8)
+    s = torch.full((N, K // 64), 0.5, dtype=BF, device="cuda")
+    z = torch.randint(0, 16, (N, K // 64), generator=g, device="cuda", dtype=U8)
+    x = torch.zeros(M, K, dtype=BF, device="cuda")
+    at = ends(K)
+    x[:, at] = torch.randint(-2, 3, (M, at.numel()), generator=g, device="cuda").to(BF)
+    y = gq.gq_g4_matmul(W, s, x, poisoned(M, N, dt=ydt), zeros=z, group=64)
+    r = slice(max(0, N - 200), N)
+    q = torch.where(at % 2 == 0, W[r][:, at // 2] & 15, W[r][:, at // 2] >> 4).double()
+    w = 0.5 * (q - z[r][:, at // 64].double())
+    assert torch.equal(y[:, r], (x[:, at].double() @ w.t()).to(ydt))
+    if M <= 16:
+        v = gq.gq_g4_matvec(W, s, x, poisoned(M, N, dt=F32), zeros=z, group=64)
+        assert torch.equal(v[:, r].double(), x[:, at].double() @ w.t())
+
+
+@pytest.mark.parametrize("M,odd", [(1, 0), (1, 3), (40, 0), (40, 5)])
+def test_longest_sums_of_dx(gq, M, odd):
+    N, K = (1 << 26) + 72, 64
+    g = gen(M, odd)
+    W = torch.randint(0, 256, (N, K // 2), device="cuda", dtype=U8)
+    s = torch.full((N, 2), 0.5, dtype=BF, device="cuda")
+    dy = torch.zeros(M, N + odd, dtype=BF, device="cuda")[:, :N]
+    at = ends(N)
+    dy[:, at] = torch.randint(-2, 3, (M, at.numel()), generator=g, device="cuda").to(BF)
+    dx = gq.gq_g4_matmul_dx(W, s, dy, poisoned(M, K, dt=BF), group=32)
+    assert torch.equal(dx, (dy[:, at].double() @ P.wide(W[at], s[at], None, 32)).to(BF))
+
+
+def test_offsets_that_are_none(gq):
+    """Decreasing, negative and too large offsets: nothing outside X and Y is touched, nor rows of no expert."""
+    g = gen(91)
+    E, N, K, M = 4, 96, 128, 300
+    W, s, z = weights(g, (E,), N, K, 64)
+    for off in ([0, 400, 300, 2 ** 31 - 1, 2 ** 31 - 1], [-2 ** 31, -5, 10, 3, 20], [300, 200, 100, 50, 0]):
+        o = torch.tensor(off, dtype=torch.int64).to(I32).cuda()
+        for f, a, b in ((gq.gq_g4_matmul, K, N), (gq.gq_g4_matmul_dx, N, K)):
+            x = normal(g, M, a, dt=BF)
+            big = torch.full((M + 600, b), 7.0, dtype=BF, device="cuda")
+            f(W, s, x, big[:M], zeros=z, group=64, offsets=o)
+            assert (big[M:] == 7.0).all()
+            if off[0] == 300:
+                assert (big == 7.0).all()
