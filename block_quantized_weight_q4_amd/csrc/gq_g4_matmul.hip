@@ -91,7 +91,7 @@ struct Tile {
     static constexpr int XI = BM / 8 / NW, WI = 2 * NT;  // copies of a wavefront
     static constexpr int PANEL = 32 * NT * 8;         // scales of a wavefront
     static constexpr int W_AT = XS * XB, P_AT = W_AT + 2 * WB, BYTES = P_AT + NW * PANEL;
-    static_assert(BM % (8 * NW) == 0 && NT == 2, "whole copies, a lane a column");
+    static_assert(BM % (8 * NW) == 0 && NT <= 2, "whole copies, a lane a column");
 
     // x: first row of the tile; n0: first column
     static __device__ __forceinline__ void run(const G4Weights& wt, const uint16_t* __restrict__ x, int64_t ldx,
@@ -185,9 +185,9 @@ struct Tile {
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[i][j] = f32x16{};
-        // Operand c of a stage: the 16 inputs of its step t = c / 2 (eight of them a lane: dword
+        // Operand c of a stage: the 16 inputs of its step t = c / NT (eight of them a lane: dword
         // 2 fq + t % 2 of W's chunk t / 2, so that one read brings those of two steps, and
-        // chunk 4 (t / 2) + 2 fq + t % 2 of X), tile c % 2.
+        // chunk 4 (t / 2) + 2 fq + t % 2 of X), tile c % NT.
         // Row a = l % 32 of a tile of W is its column 16 (a / 4 % 2) + 4 (a / 8) + a % 4, so
         // that a lane ends up with 16 neighbouring columns of one row of Y.
         const int wcol = 16 * ((fr >> 2) & 1) + 4 * (fr >> 3) + (fr & 3), wr16 = wcol & 15;
@@ -231,7 +231,7 @@ struct Tile {
             typename T::x8 b[MT], a;
             Raw r[2];
             read_raw(0, 0, 0, r[0]);
-            read_raw(0, 0, 1, r[1]);
+            if constexpr (NT == 2) read_raw(0, 0, 1, r[1]);
 #pragma unroll
             for (int j = 0; j < MT; ++j) b[j] = read_x(0, 0, j);
             a = weights8<T>(r[0].w.x, r[0].s.x, r[0].s.y);
@@ -256,11 +256,14 @@ struct Tile {
                         load_x(s + XS, buf);
                         if constexpr (odd) load_w((s + 3) / 2, wb);
                     }
-                    // (r[(c + 1) % 2] is operand c + 1's, r[c % 2] free from the end of its second step on)
-                    const Raw& n = r[(c + 1) & 1];
-                    const typename T::x8 next = weights8<T>((c + 1) & 2 ? n.w.y : n.w.x, n.s.x, n.s.y);
-                    const bool fresh = c & 2;
-                    if (fresh) read_raw(c < 4 ? wb : nwb, c < 4 ? (odd ? 3 : 1) : (odd ? 0 : 2), c & 1, r[c & 1]);
+                    // r[which(c)] has the bytes of operand c: of the two tiles in turn, with one tile of
+                    // the chunks in turn.  Two operands ahead the next chunk's are read, when the others
+                    // that lay there are formed.
+                    auto which = [](int c) { return NT == 2 ? c & 1 : (c >> 1) & 1; };
+                    const Raw& n = r[which(c + 1)];
+                    const typename T::x8 next = weights8<T>((c + 1) / NT & 1 ? n.w.y : n.w.x, n.s.x, n.s.y);
+                    const bool fresh = NT == 2 ? c & 2 : !(c & 1), more = c + 2 < C;  // (of this stage)
+                    if (fresh) read_raw(more ? wb : nwb, more ? (odd ? 3 : 1) : (odd ? 0 : 2), c & (NT - 1), r[which(c + 2)]);
                     const bool last = c % NT == NT - 1;  // of its step
 #pragma unroll
                     for (int j = 0; j < MT; ++j) {
@@ -332,14 +335,13 @@ struct Tile {
     }
 };
 
-// Workgroups from n_full on take parts of the tiles from n_full on, PARTS a tile,
-// by rows, then by columns (dense): the last, partial round of tiles would take as
-// long as a whole one on a part of the CUs.
+// Workgroups from n_full on take halves of the tiles from n_full on, PARTS = 2 a tile,
+// by columns (dense; by rows weights would be expanded twice): the last, partial round
+// of tiles would take as long as a whole one on a part of the CUs.
 template <typename T, int MT, int NT, int PARTS>
 __global__ __launch_bounds__(256, 2) void k_g4_tile(G4Weights wt, Rows a, int gm, int gn, int n_full) {
     using U = Tile<T, MT, NT>;
-    constexpr int PM = PARTS > 1 ? 2 : 1, PN = PARTS > 2 ? 2 : 1;
-    using P = Tile<T, MT / PM, NT / PN>;
+    using P = Tile<T, MT, NT / PARTS>;
     extern __shared__ __align__(16) uint8_t smem[];
     RowTile t{0, 0, 0};
     int64_t n0 = 0;
@@ -367,24 +369,27 @@ __global__ __launch_bounds__(256, 2) void k_g4_tile(G4Weights wt, Rows a, int gm
         const int bands = (gm + BAND - 1) / BAND, h = (gm + bands - 1) / bands;
         const int band = id / (h * gn), hb = gm - band * h < h ? gm - band * h : h;
         const int c = id - band * h * gn;
-        n0 = (int64_t)(c / hb) * U::BN + (q >> 1) * P::BN;
-        t.row0 = (int64_t)(band * h + c % hb) * U::BM + (q & 1) * P::BM;
-        const int64_t left = a.M - t.row0, most = part ? P::BM : U::BM;
-        if (left <= 0 || n0 >= wt.N) return;
-        t.rows = (int)(left < most ? left : most);
+        n0 = (int64_t)(c / hb) * U::BN + q * P::BN;
+        if (n0 >= wt.N) return;
+        t.row0 = (int64_t)(band * h + c % hb) * U::BM;
+        t.rows = a.M - t.row0 < U::BM ? (int)(a.M - t.row0) : U::BM;
     }
     const G4Weights w = of_expert(wt, t.e);
     const uint16_t* x = static_cast<const uint16_t*>(a.X) + t.row0 * a.ldx;
     void* y = a.y_f32 ? static_cast<void*>(static_cast<float*>(a.Y) + t.row0 * a.ldy)
                       : static_cast<void*>(static_cast<uint16_t*>(a.Y) + t.row0 * a.ldy);
     if constexpr (PARTS > 1) {
-        // an expert's last rows
-        if (a.offsets && t.rows > P::BM && t.rows <= 96) {
-            Tile<T, 3, NT>::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
+        if (part) {
+            P::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
             return;
         }
-        if (part || (a.offsets && t.rows <= P::BM)) {
-            P::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
+        // an expert's last rows
+        if (a.offsets && t.rows <= 64) {
+            Tile<T, 2, NT>::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
+            return;
+        }
+        if (a.offsets && t.rows <= 96) {
+            Tile<T, 3, NT>::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
             return;
         }
     }
@@ -456,16 +461,17 @@ hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
 }
 
 // Tiles (of 16-bit results) or stream.  A workgroup of a tile goes through all of K
-// by itself, about 0.7 us for 64 inputs, so few tiles leave CUs idle: 2560 x 9728 takes
-// 106 us in tiles with 64 to 512 rows, streamed 16 to 55, with 1024 rows 108 either way;
-// 17408 x 5120 with 64 rows 59 and 39, with 256 87 and 114 (about 450 and 950 TFLOP/s
-// where there is enough work); 704 x 2816 of 128 experts with 1024 rows 46 and 42; 2816 x
-// 2816 of 8 with 256 35 and 24, with 1000 41 and 58.  Narrow matrices leave most of a
-// tile's 256 columns empty.  (fp32 results carry no rounded weights, and exact ones take
-// the streamed form at any size: 3015 x 17408 x 5120 in 1.13 ms.)
+// by itself, so that few tiles leave CUs idle and take as long as many: 2560 x 9728 takes
+// 92 us in tiles with 256 to 1024 rows, streamed 39 to 115, with 768 rows 95 and 92;
+// 17408 x 5120 with 64 rows 56 and 38, with 128 51 and 65, with 256 70 and 110; 4096 x
+// 4096 with 400 rows 41 and 42, with 600 42 and 58; 2816 x 2816 of 8 experts with 600 rows
+// 41 and 40, with 1000 41 and 58; 704 x 2816 of 128 with 1024 51 and 45, with 4096 57 and
+// 87.  Narrow matrices leave most of a tile's 256 columns empty.  (fp32 results carry no
+// rounded weights, and exact ones take the streamed form at any size: 3015 x 17408 x 5120
+// in 1.13 ms.)
 template <typename X, typename T>
 hipError_t matmul(const G4Weights& w, const Rows& a, hipStream_t s) {
-    if (a.y_f32 || w.N < 128 || a.M * w.N < 2500000) return w.zeros ? few<X, true>(w, a, s) : few<X, false>(w, a, s);
+    if (a.y_f32 || w.N < 128 || a.M * w.N < 1700000) return w.zeros ? few<X, true>(w, a, s) : few<X, false>(w, a, s);
     if (a.M / a.n_experts <= 64) return tile<T, 2, 2, 1>(w, a, s);
     return tile<T, 4, 2, 2>(w, a, s);
 }

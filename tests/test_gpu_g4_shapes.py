@@ -37,7 +37,8 @@ def gq():
 
 @pytest.mark.parametrize("G", [32, 64, 128])
 @pytest.mark.parametrize("M,N,K", [(2500, 1000, 32), (2049, 1300, 64), (2600, 1003, 96), (3015, 1000, 416),
-                                   (4097, 700, 160), (20000, 130, 224), (1500, 1700, 2848), (9000, 513, 544)])
+                                   (4097, 700, 160), (20000, 130, 224), (1500, 1700, 2848), (9000, 513, 544), (1024, 2560, 544), (128, 17408, 160),
+                                   (140, 12300, 704)])
 def test_tiles(gq, M, N, K, G):
     """Many rows to 16 bits: every end of the inputs, whole and partial last rounds."""
     run_rows(gq, M, N, K, G, BF if G != 64 else H, BF if G != 64 else H, zeros=M % 2 == 0, sdt=H if G == 32 else BF,
