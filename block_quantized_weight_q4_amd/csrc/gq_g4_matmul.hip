@@ -75,14 +75,14 @@ __device__ __forceinline__ typename T::x8 weights8(uint32_t w, float s512, float
 // to LDS as they are in memory: X in stages of 64 inputs, W in blocks of two stages
 // (64 bytes a row).
 //
-// Bound by the matrix cores and what they are fed with: 3015 x 17408 x 5120 takes 465 to
-// 482 us (1.12 to 1.15 PFLOP/s; a library's product of the same rows with expanded
+// Bound by the matrix cores and what they are fed with: 3015 x 17408 x 5120 takes 466 to
+// 484 us (1.11 to 1.15 PFLOP/s; a library's product of the same rows with expanded
 // weights 505, of 8192^3 1.13 to 1.33 PFLOP/s, depending on the card and its heat), with
-// the matrix cores busy 70% of the time and 60% of the issue cycles spent on expanding
+// the matrix cores busy 72% of the time and 60% of the issue cycles spent on expanding
 // (20 instructions for eight weights).  Two workgroups a CU hide each other's starts and
 // ends; eight wavefronts in one, 16 x 16 instructions (576 us) and two barriers a stage
 // (703 us) were slower.  Short sums are bound by those starts and by the stores: 24,120
-// rows of 128 experts, 2816 x 704 (11 stages a tile), 141 us, 680 TFLOP/s.
+// rows of 128 experts, 2816 x 704 (11 stages a tile), 141 to 147 us, 650 to 680 TFLOP/s.
 template <typename T, int MT, int NT>
 struct Tile {
     static constexpr int NW = 4, XS = 2;  // wavefronts, stages of X
