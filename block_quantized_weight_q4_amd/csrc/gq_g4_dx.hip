@@ -338,9 +338,9 @@ __global__ __launch_bounds__(256, 2) void k_g4_dx(G4Weights wt, Rows a, int gm, 
 }
 
 // Workgroup: columns blockIdx.x % gn, row tile / gn.
-template <typename T, int MT, int W, int H>
+template <typename T, int MT, int W, int H, int C>
 __global__ __launch_bounds__(64 * W) void k_g4_dx_few(G4Weights wt, Rows a, int gm, int gn) {
-    using U = DxStream<MT, W, H>;
+    using U = DxStream<MT, W, H, C>;
     extern __shared__ __align__(16) uint8_t smem[];
     RowTile t{0, 0, 0};
     int tn = 0;
@@ -359,20 +359,20 @@ __global__ __launch_bounds__(64 * W) void k_g4_dx_few(G4Weights wt, Rows a, int 
         t.row0 = (int64_t)(id / gn) * U::BM;
         t.rows = a.M - t.row0 < U::BM ? (int)(a.M - t.row0) : U::BM;
     }
-    dx_stream<T, MT, W, H>(of_expert(wt, t.e), a.dY + t.row0 * a.lddy, a.lddy, t.rows, a.dX + t.row0 * a.lddx, a.lddx,
+    dx_stream<T, MT, W, H, C>(of_expert(wt, t.e), a.dY + t.row0 * a.lddy, a.lddy, t.rows, a.dX + t.row0 * a.lddx, a.lddx,
                            (int64_t)tn * U::BN, smem);
 }
 
-template <typename T, int MT, int W, int H>
+template <typename T, int MT, int W, int H, int C>
 hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
-    using U = DxStream<MT, W, H>;
+    using U = DxStream<MT, W, H, C>;
     const int64_t gm = a.offsets ? most_tiles(a.M, a.n_experts, U::BM) : (a.M + U::BM - 1) / U::BM;
     const int64_t gn = (w.K + U::BN - 1) / U::BN;
     if (!grid_ok(gm * gn, 64 * W)) return hipErrorInvalidValue;
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_dx_few<T, MT, W, H>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_dx_few<T, MT, W, H, C>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_g4_dx_few<T, MT, W, H>), dim3((unsigned)(gm * gn)), dim3(64 * W), U::BYTES, s, w, a, (int)gm,
+    hipLaunchKernelGGL((k_g4_dx_few<T, MT, W, H, C>), dim3((unsigned)(gm * gn)), dim3(64 * W), U::BYTES, s, w, a, (int)gm,
                        (int)gn);
     return hipGetLastError();
 }
@@ -413,14 +413,16 @@ template <typename T>
 hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
     // Few rows (us; sum x columns): streamed by 16 wavefronts with 16 rows where there are few
     // workgroups (16 rows x 17408 x 5120: 53, four wavefronts with 32 rows 61, tiles 139; x
-    // 9728 x 2560: 28, 36, 78), by four with 32 rows up to two a CU (32 x 2560 x 9728: 14, 16 of
+    // 9728 x 2560: 28, 36, 78), of 32 columns each where that leaves half of the CUs idle (44
+    // and 24; one row 37 and 20, with 64 columns 47 and 24), by four with 32 rows up to two a CU (32 x 2560 x 9728: 14, 16 of
     // 16 23, tiles 24; 128 x 17408 x 5120: 111, 142, 158; 256 x 17408 x 5120: 182, 259, 158);
     // experts with a row or two, up to eight a CU (96 rows of 128, 2816 x 704: 26, tiles 38;
     // 96 of 128, 704 x 2816, 4224 workgroups: 35, 22).
     const int64_t per = (a.M + a.n_experts - 1) / a.n_experts, experts = a.n_experts < a.M ? a.n_experts : a.M;
     auto groups = [&](int64_t rows) { return (per + rows - 1) / rows * experts * ((w.K + 63) / 64); };
-    if (groups(16) <= 256) return few<T, 1, 16, 2>(w, a, s);
-    if (groups(32) <= (a.n_experts > 1 && per <= 2 ? 2048 : 512)) return few<T, 2, 4, 2>(w, a, s);
+    if (groups(16) <= 128) return few<T, 1, 16, 2, 32>(w, a, s);
+    if (groups(16) <= 256) return few<T, 1, 16, 2, 64>(w, a, s);
+    if (groups(32) <= (a.n_experts > 1 && per <= 2 ? 2048 : 512)) return few<T, 2, 4, 2, 64>(w, a, s);
     // (copies address eight rows in 31 bits)
     return w.N % 8 == 0 && a.lddy % 8 == 0 && a.lddy < (1 << 26) ? launch<T, true>(w, a, s) : launch<T, false>(w, a, s);
 }

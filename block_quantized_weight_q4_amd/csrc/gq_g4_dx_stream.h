@@ -5,16 +5,16 @@
 // along the sum, so each weight is formed first, exactly, and rounded to 16 bits
 // for the matrix cores.
 //
-// A workgroup has 64 columns of W and splits its N rows over its W wavefronts:
+// A workgroup has 64 or 32 columns of W and splits its N rows over its W wavefronts:
 // wavefront w takes the blocks of 32 H rows w, w + W, ...  Each has a buffer of LDS
 // of its own, which global-to-LDS copies fill with its next block as soon as this
 // one's bytes are in registers; the rows of dY, which all workgroups share, come
 // from the caches straight into registers.  The partial sums are joined in LDS in
 // wavefront order.
 //
-// 16 rows of 17408 x 5120 (46 MB): 53 us, of 2560 x 9728 13 us; bound by forming the
-// weights (about 20 instructions for eight) on as many CUs as there are 64 columns: 80 and
-// 152 of 256.  (Tiles, whose wavefronts share a stage, took 139 and 24 us.)
+// 16 rows of 17408 x 5120 (46 MB): 44 us, of 2560 x 9728 12.5 us; bound by forming the
+// weights (about 20 instructions for eight) on as many CUs as there are 32 or 64 columns:
+// 160 and 152 of 256.  (Tiles, whose wavefronts share a stage, took 139 and 24 us.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -46,24 +46,42 @@ __device__ __forceinline__ void weights_2x4(uint32_t w0, uint32_t w1, f32x4 f, u
     a[3][i] = T::pack(f0(o0.y), f1(o1.y));
 }
 
-template <int MT, int W, int H>
+// Of two neighbouring columns and rows 4 k .. + 3: w0 to w3 their bytes (one a row), f
+// and g the scales of rows 4 k, 4 k + 1 and of the other two.
+template <typename T>
+__device__ __forceinline__ void weights_4x2(const uint32_t* w, f32x4 f, f32x4 g, u32x4 (&a)[2], int k) {
+    const uint32_t v = __builtin_amdgcn_perm(__builtin_amdgcn_perm(w[3], w[2], 0x0c0c0400u),
+                                             __builtin_amdgcn_perm(w[1], w[0], 0x0c0c0400u), 0x05040100u);
+    const uint32_t q[2] = {v & 0x0f0f0f0fu, (v >> 4) & 0x0f0f0f0fu};
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const gqf8::f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[t], false);
+        const gqf8::f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[t], true);
+        a[t][2 * k] = T::pack(__builtin_fmaf(b.x, f[0], f[1]), __builtin_fmaf(b.y, f[2], f[3]));
+        a[t][2 * k + 1] = T::pack(__builtin_fmaf(c.x, g[0], g[1]), __builtin_fmaf(c.y, g[2], g[3]));
+    }
+}
+
+// C columns (64 or 32), of C / 16 operands.
+template <int MT, int W, int H, int C>
 struct DxStream {
-    static constexpr int BM = 16 * MT, BN = 64, BR = 32 * H;
-    static constexpr int WB = BR * 32;                // bytes of weights of a wavefront
-    static constexpr int SB = 2 * BR * 8;             // its scales: two groups at most
-    static constexpr int JOIN = 4 * MT * 1024;
+    static constexpr int BM = 16 * MT, BN = C, BR = 32 * H, NT = C / 16;
+    static constexpr int GROUPS = C / 32;             // groups of the columns, at most
+    static constexpr int WB = BR * (C / 2);           // bytes of weights of a wavefront
+    static constexpr int SB = GROUPS * BR * 8;        // its scales
+    static constexpr int JOIN = NT * MT * 1024;
     static constexpr int ONE = WB + SB;
     static constexpr int BYTES = W * (ONE > JOIN ? ONE : JOIN);
-    static_assert(BR % 64 == 0, "whole wavefronts of scales");
+    static_assert(BR % 64 == 0 && (C == 64 || C == 32), "whole wavefronts of scales");
 };
 
 // Rows [0, rows) of dy (1 <= rows <= 16 MT; rows past them repeat the last) by columns
-// k0 .. k0 + 63 of W.
-template <typename T, int MT, int W, int H>
+// k0 .. k0 + C - 1 of W.
+template <typename T, int MT, int W, int H, int C>
 __device__ __forceinline__ void dx_stream(const G4Weights& wt, const uint16_t* __restrict__ dy, int64_t lddy, int rows,
                                           uint16_t* __restrict__ dx, int64_t lddx, int64_t k0, uint8_t* smem) {
-    using S = DxStream<MT, W, H>;
-    constexpr int BR = S::BR;
+    using S = DxStream<MT, W, H, C>;
+    constexpr int BR = S::BR, NT = S::NT, GROUPS = S::GROUPS;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, fq = lane >> 4;
@@ -72,34 +90,39 @@ __device__ __forceinline__ void dx_stream(const G4Weights& wt, const uint16_t* _
     uint8_t* mine = smem + wave * S::ONE;
     float* panel = reinterpret_cast<float*>(mine + S::WB);  // [group][row]: 512 s and -z s
 
-    // W: 32 rows of 32 bytes a copy, row 8 a + b at 4 b + a, so that the four rows, 8 apart,
-    // that the lanes read at once lie in different banks
-    const int at = lane >> 1, cr = 8 * (at & 3) + (at >> 2), chunk = 16 * (lane & 1);
-    const uint32_t woff = within((uint32_t)(cr * row_bytes) + chunk, chunk, (int)(K - k0 < 64 ? K - k0 : 64) / 2);
+    // W: C / 2 bytes of 32 rows (64 of 32 columns) a copy, row 8 a + b of 32 at 4 b + a, so that
+    // the four rows, 8 apart, that the lanes read at once lie in different banks
+    constexpr int COPY = 2048 / C, CHUNKS = C / 32;  // rows of a copy, 16-byte chunks of a row
+    const int at = lane / CHUNKS, cr = (at & 32) + 8 * (at & 3) + ((at >> 2) & 7), chunk = 16 * (lane % CHUNKS);
+    const uint32_t woff = within((uint32_t)(cr * row_bytes) + chunk, chunk, (int)(K - k0 < C ? K - k0 : C) / 2);
     const int64_t g0 = k0 / wt.group, g1 = wt.group == 32 && g0 + 1 < KG ? g0 + 1 : g0;
     const uint16_t* p[MT];  // this lane's eight columns of dY of a block
 #pragma unroll
     for (int j = 0; j < MT; ++j) p[j] = dy + (16 * j + fr < rows ? 16 * j + fr : rows - 1) * lddy + 8 * fq;
 
     u32x4 b[H][MT];
-    uint32_t sc[H / 2][2], zp[H / 2][2];
+    uint32_t sc[H / 2][GROUPS], zp[H / 2][GROUPS];
     auto load = [&](int nb) __attribute__((always_inline)) {
         const int64_t n = (int64_t)nb * BR;
         const int left = n < N ? (int)(N - n < BR ? N - n : BR) : 0;
         const Rsrc wr = make_rsrc(wt.W + (left ? n : 0) * row_bytes + k0 / 2, left ? left * row_bytes - k0 / 2 : 0);
 #pragma unroll
-        for (int h = 0; h < H; ++h) copy16(wr, woff + (uint32_t)(32 * h * row_bytes), mine + 1024 * h);
+        for (int h = 0; h < BR / COPY; ++h) copy16(wr, woff + (uint32_t)(COPY * h * row_bytes), mine + 1024 * h);
 #pragma unroll
         for (int h = 0; h < H / 2; ++h) {
             const int64_t r = 64 * h + lane < left ? n + 64 * h + lane : 0;
-            sc[h][0] = wt.scales[r * KG + g0];
-            sc[h][1] = wt.scales[r * KG + g1];
-            zp[h][0] = zp[h][1] = 8;
-            if (wt.zeros) {
-                zp[h][0] = wt.zeros[r * KG + g0];
-                zp[h][1] = wt.zeros[r * KG + g1];
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                sc[h][g] = wt.scales[r * KG + (g ? g1 : g0)];
+                zp[h][g] = 8;
             }
-            if (64 * h + lane >= left) sc[h][0] = sc[h][1] = 0;  // (rows past N are zeros)
+            if (wt.zeros) {
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) zp[h][g] = wt.zeros[r * KG + (g ? g1 : g0)];
+            }
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g)
+                if (64 * h + lane >= left) sc[h][g] = 0;  // (rows past N are zeros)
         }
         if (left == BR) {
 #pragma unroll
@@ -125,13 +148,13 @@ __device__ __forceinline__ void dx_stream(const G4Weights& wt, const uint16_t* _
                 }
         }
     };
-    f32x4 acc[4][MT];
+    f32x4 acc[NT][MT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[t][j] = f32x4{};
-    // lane: columns 4 fr .. + 3 (two bytes), rows 32 h + 8 fq .. + 7
-    const int wat = 32 * fq + 2 * fr, gsel = wt.group == 32 ? fr >> 3 : 0;
+    // lane: columns NT fr .. (two bytes, or one), rows 32 h + 8 fq .. + 7
+    const int wat = (C / 2) * fq + (C / 32) * fr, gsel = GROUPS == 2 && wt.group == 32 ? fr >> 3 : 0;
     if (wave < NB) {
         load(wave);
         for (int nb = wave; nb < NB; nb += W) {
@@ -140,11 +163,15 @@ __device__ __forceinline__ void dx_stream(const G4Weights& wt, const uint16_t* _
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[h][i] = *reinterpret_cast<const uint16_t*>(mine + 1024 * h + 128 * i + wat);
+                for (int i = 0; i < 8; ++i) {
+                    const uint8_t* q = mine + (16 * C) * h + (2 * C) * i + wat;
+                    if constexpr (C == 64) w[h][i] = *reinterpret_cast<const uint16_t*>(q);
+                    else w[h][i] = *q;
+                }
 #pragma unroll
             for (int h = 0; h < H / 2; ++h)
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
+                for (int g = 0; g < GROUPS; ++g) {
                     const float f = scale_f32(sc[h][g], wt.s_f16);
                     float* o = panel + g * (2 * BR) + 2 * (64 * h + lane);
                     o[0] = 512.0f * f;
@@ -160,11 +187,16 @@ __device__ __forceinline__ void dx_stream(const G4Weights& wt, const uint16_t* _
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const f32x4* sp = reinterpret_cast<const f32x4*>(panel + gsel * (2 * BR) + 2 * (32 * h + 8 * fq));
-                u32x4 a[4];
+                u32x4 a[NT];
+                if constexpr (C == 64) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) weights_2x4<T>(w[h][2 * i], w[h][2 * i + 1], sp[i], a, i);
+                    for (int i = 0; i < 4; ++i) weights_2x4<T>(w[h][2 * i], w[h][2 * i + 1], sp[i], a, i);
+                } else {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                    for (int k = 0; k < 2; ++k) weights_4x2<T>(&w[h][4 * k], sp[2 * k], sp[2 * k + 1], a, k);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int j = 0; j < MT; ++j)
                         acc[t][j] = T::mfma(__builtin_bit_cast(typename T::x8, a[t]),
@@ -175,24 +207,29 @@ __device__ __forceinline__ void dx_stream(const G4Weights& wt, const uint16_t* _
     wait_copies<0>();
     __syncthreads();
     // the join: partial sums of every wavefront, added in their order
+    constexpr int FOURS = NT * MT;  // of a lane: four neighbouring columns each
     f32x4* part = reinterpret_cast<f32x4*>(smem);
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            part[(wave * (4 * MT) + 4 * j + r) * 64 + lane] = f32x4{acc[0][j][r], acc[1][j][r], acc[2][j][r], acc[3][j][r]};
+        for (int r = 0; r < NT; ++r) {
+            f32x4 v;
+            if constexpr (C == 64) v = f32x4{acc[0][j][r], acc[1][j][r], acc[2][j][r], acc[3][j][r]};
+            else v = f32x4{acc[0][j][2 * r], acc[1][j][2 * r], acc[0][j][2 * r + 1], acc[1][j][2 * r + 1]};
+            part[(wave * FOURS + NT * j + r) * 64 + lane] = v;
+        }
     __syncthreads();
-    for (int c = wave; c < 4 * MT; c += W) {
+    for (int c = wave; c < FOURS; c += W) {
         f32x4 v = part[c * 64 + lane];
 #pragma unroll
         for (int w = 1; w < W; ++w) {
-            const f32x4 o = part[(w * (4 * MT) + c) * 64 + lane];
+            const f32x4 o = part[(w * FOURS + c) * 64 + lane];
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] += o[r];
         }
-        // lane: columns 16 fq + 4 (c % 4) .. + 3 of row 16 (c / 4) + fr
-        const int64_t k = k0 + 16 * fq + 4 * (c & 3);
-        const int row = 16 * (c >> 2) + fr;
+        // lane: columns 4 NT fq + 4 (c % NT) .. + 3 of row 16 (c / NT) + fr
+        const int64_t k = k0 + 4 * NT * fq + 4 * (c % NT);
+        const int row = 16 * (c / NT) + fr;
         if (row < rows && k < K) {  // (K is a multiple of 32)
             const u32x2 o{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
             __builtin_memcpy(dx + row * lddx + k, &o, 8);

@@ -92,7 +92,8 @@ def test_streamed_experts(gq, counts):
     run_rows(gq, sum(counts) + 3, 2724, 64, 64, BF, F32, counts=counts)
 
 
-DX = [(1, 12441, 896, 128), (37, 1021, 512, 32), (16, 1024, 544, 64), (300, 130, 96, 128),  # 16 wavefronts
+DX = [(1, 12441, 896, 128), (37, 1021, 512, 32), (16, 1024, 544, 64), (300, 130, 96, 128),  # 16 wavefronts, 32 columns
+      (300, 130, 544, 32), (16, 265, 9024, 64), (1, 200, 10272, 128),                     # 64 columns
       (1000, 77, 512, 64), (1003, 640, 544, 32), (128, 100, 5120, 128),                   # four
       (4000, 72, 512, 128), (4100, 71, 544, 32), (700, 264, 2816, 64),                    # tiles of 64 rows, sum in halves
       (10000, 72, 512, 64), (9999, 73, 544, 128), (9999, 200, 800, 32)]                   # of 128 (64, through registers)
