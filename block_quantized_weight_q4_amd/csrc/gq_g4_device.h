@@ -15,7 +15,6 @@ using gqf8::bld16;
 using gqf8::copy16;
 using gqf8::grid_ok;
 using gqf8::make_rsrc;
-using gqf8::NOWHERE;
 using gqf8::Rsrc;
 using gqf8::wait_copies;
 using gqf8::wait_reads;
@@ -32,7 +31,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 struct Bf16 {
     typedef bf16x8 x8;
     static constexpr int dtype = gqd::DT_BF16;
-    static __device__ __forceinline__ float wide(uint16_t u) { return gqd::bf2f(u); }
     static __device__ __forceinline__ uint16_t narrow(float v) { return gqd::f2bf(v); }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
@@ -47,7 +45,6 @@ struct Bf16 {
 struct F16 {
     typedef f16x8 x8;
     static constexpr int dtype = gqd::DT_F16;
-    static __device__ __forceinline__ float wide(uint16_t u) { return gqd::h2f(u); }
     static __device__ __forceinline__ uint16_t narrow(float v) { return gqd::f2h(v); }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});

@@ -400,7 +400,8 @@ hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
 template <typename T, bool DMA>
 hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
     const int64_t per = a.M / a.n_experts;  // rows an expert has
-    auto tiles = [&](int64_t rows) { return (per / rows + 1) * (a.n_experts < a.M ? a.n_experts : a.M) * ((w.K + 255) / 256); };
+    const int64_t experts = a.n_experts < a.M ? a.n_experts : a.M;
+    auto tiles = [&](int64_t rows) { return (per / rows + 1) * experts * ((w.K + 255) / 256); };
     if (per <= 32) return launch<T, 2, 1, DMA>(w, a, s);
     if (tiles(128) < 128) return launch<T, 4, 2, DMA>(w, a, s);
     if constexpr (DMA) {
@@ -414,10 +415,10 @@ hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
     // Few rows (us; sum x columns): streamed by 16 wavefronts with 16 rows where there are few
     // workgroups (16 rows x 17408 x 5120: 53, four wavefronts with 32 rows 61, tiles 139; x
     // 9728 x 2560: 28, 36, 78), of 32 columns each where that leaves half of the CUs idle (44
-    // and 24; one row 37 and 20, with 64 columns 47 and 24), by four with 32 rows up to two a CU (32 x 2560 x 9728: 14, 16 of
-    // 16 23, tiles 24; 128 x 17408 x 5120: 111, 142, 158; 256 x 17408 x 5120: 182, 259, 158);
-    // experts with a row or two, up to eight a CU (96 rows of 128, 2816 x 704: 26, tiles 38;
-    // 96 of 128, 704 x 2816, 4224 workgroups: 35, 22).
+    // and 24; one row 37 and 20, with 64 columns 47 and 24), by four with 32 rows up to two a
+    // CU (32 x 2560 x 9728: 14, 16 of 16 23, tiles 24; 128 x 17408 x 5120: 111, 142, 158; 256
+    // x 17408 x 5120: 182, 259, 158); experts with a row or two, up to eight a CU (96 rows of
+    // 128, 2816 x 704: 26, tiles 38; 96 of 128, 704 x 2816, 4224 workgroups: 35, 22).
     const int64_t per = (a.M + a.n_experts - 1) / a.n_experts, experts = a.n_experts < a.M ? a.n_experts : a.M;
     auto groups = [&](int64_t rows) { return (per + rows - 1) / rows * experts * ((w.K + 63) / 64); };
     if (groups(16) <= 128) return few<T, 1, 16, 2, 32>(w, a, s);
