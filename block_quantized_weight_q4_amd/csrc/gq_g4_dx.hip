@@ -303,8 +303,9 @@ struct Tile {
     }
 };
 
+// The launch has the tiles from number `first` on.
 template <typename T, int MT, int KS, bool DMA>
-__global__ __launch_bounds__(256, 2) void k_g4_dx(G4Weights wt, Rows a, int gm, int gn) {
+__global__ __launch_bounds__(256, 2) void k_g4_dx(G4Weights wt, Rows a, int gm, int gn, int64_t first) {
     using U = Tile<T, MT, KS, DMA>;
     extern __shared__ __align__(16) uint8_t smem[];
     RowTile t{0, 0, 0};
@@ -312,17 +313,17 @@ __global__ __launch_bounds__(256, 2) void k_g4_dx(G4Weights wt, Rows a, int gm, 
     if (a.offsets) {
         auto pick = [&](int total) {
             // (the grid is sized for the most tiles there can be: only the real ones are dealt out to the XCDs)
-            const int64_t real = (int64_t)(total < gm ? total : gm) * gn;
+            const int64_t real = (int64_t)(total < gm ? total : gm) * gn - first;
             if (blockIdx.x >= real) return -1;
-            const int id = xcd_order(blockIdx.x, (int)real);
-            tn = id % gn;
-            return id / gn;
+            const int64_t id = first + xcd_order(blockIdx.x, real < gridDim.x ? (int)real : (int)gridDim.x);
+            tn = (int)(id % gn);
+            return (int)(id / gn);
         };
         if (!tile_of(a.offsets, a.n_experts, a.M, U::BM, pick, t)) return;
     } else {
-        const int id = xcd_order(blockIdx.x, gm * gn);
-        tn = id % gn;
-        t.row0 = (int64_t)(id / gn) * U::BM;
+        const int64_t id = first + xcd_order(blockIdx.x, gridDim.x);
+        tn = (int)(id % gn);
+        t.row0 = id / gn * U::BM;
         t.rows = a.M - t.row0 < U::BM ? (int)(a.M - t.row0) : U::BM;
     }
     const G4Weights w = of_expert(wt, t.e);
@@ -368,7 +369,7 @@ hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
     using U = DxStream<MT, W, H, C>;
     const int64_t gm = a.offsets ? most_tiles(a.M, a.n_experts, U::BM) : (a.M + U::BM - 1) / U::BM;
     const int64_t gn = (w.K + U::BN - 1) / U::BN;
-    if (!grid_ok(gm * gn, 64 * W)) return hipErrorInvalidValue;
+    if (!grid_ok(gm * gn, 64 * W)) return hipErrorInvalidValue;  // (never: at most four times the groups counted below)
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_dx_few<T, MT, W, H, C>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
     if (e != hipSuccess) return e;
@@ -382,13 +383,15 @@ hipError_t launch(const G4Weights& w, const Rows& a, hipStream_t s) {
     using U = Tile<T, MT, KS, DMA>;
     const int64_t gm = a.offsets ? most_tiles(a.M, a.n_experts, U::BM) : (a.M + U::BM - 1) / U::BM;
     const int64_t gn = (w.K + U::BN - 1) / U::BN;
-    if (!grid_ok(gm * gn, 256)) return hipErrorInvalidValue;
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_dx<T, MT, KS, DMA>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_g4_dx<T, MT, KS, DMA>), dim3((unsigned)(gm * gn)), dim3(256), U::BYTES, s, w, a, (int)gm,
-                       (int)gn);
-    return hipGetLastError();
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_dx<T, MT, KS, DMA>),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
+    for (int64_t first = 0; first < gm * gn && e == hipSuccess; first += MOST_GROUPS) {
+        const int64_t left = gm * gn - first;
+        hipLaunchKernelGGL((k_g4_dx<T, MT, KS, DMA>), dim3((unsigned)(left < MOST_GROUPS ? left : MOST_GROUPS)),
+                           dim3(256), U::BYTES, s, w, a, (int)gm, (int)gn, first);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 // Shape of the tiles (us; rows x sum x columns).  128 x 256 where they fill half of the

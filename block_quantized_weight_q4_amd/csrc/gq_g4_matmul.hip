@@ -335,11 +335,12 @@ struct Tile {
     }
 };
 
-// Workgroups from n_full on take halves of the tiles from n_full on, PARTS = 2 a tile,
-// by columns (dense; by rows weights would be expanded twice): the last, partial round
-// of tiles would take as long as a whole one on a part of the CUs.
+// The launch has n_full tiles from number `first` on, and workgroups from n_full on take
+// halves of the tiles behind them, PARTS = 2 a tile, by columns (dense; by rows weights
+// would be expanded twice): the last, partial round of tiles would take as long as a
+// whole one on a part of the CUs.
 template <typename T, int MT, int NT, int PARTS>
-__global__ __launch_bounds__(256, 2) void k_g4_tile(G4Weights wt, Rows a, int gm, int gn, int n_full) {
+__global__ __launch_bounds__(256, 2) void k_g4_tile(G4Weights wt, Rows a, int gm, int gn, int n_full, int64_t first) {
     using U = Tile<T, MT, NT>;
     using P = Tile<T, MT, NT / PARTS>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -349,26 +350,27 @@ __global__ __launch_bounds__(256, 2) void k_g4_tile(G4Weights wt, Rows a, int gm
     if (a.offsets) {
         auto pick = [&](int total) {
             // (the grid is sized for the most tiles there can be: only the real ones are dealt out to the XCDs)
-            const int64_t real = (int64_t)(total < gm ? total : gm) * gn;
+            const int64_t real = (int64_t)(total < gm ? total : gm) * gn - first;
             if (blockIdx.x >= real) return -1;
-            const int id = xcd_order(blockIdx.x, (int)real);
-            n0 = (int64_t)(id % gn) * U::BN;
-            return id / gn;
+            const int64_t id = first + xcd_order(blockIdx.x, real < n_full ? (int)real : n_full);
+            n0 = id % gn * U::BN;
+            return (int)(id / gn);
         };
         if (!tile_of(a.offsets, a.n_experts, a.M, U::BM, pick, t)) return;
     } else {
-        int id, q = 0;
+        int here, q = 0;
         part = PARTS > 1 && (int)blockIdx.x >= n_full;
         if (part) {
             q = ((int)blockIdx.x - n_full) % PARTS;
-            id = n_full + ((int)blockIdx.x - n_full) / PARTS;
+            here = n_full + ((int)blockIdx.x - n_full) / PARTS;
         } else {
-            id = xcd_order(blockIdx.x, n_full);
+            here = xcd_order(blockIdx.x, n_full);
         }
+        const int64_t id = first + here;
         // bands of at most BAND row tiles, each walked column of tiles by column
         const int bands = (gm + BAND - 1) / BAND, h = (gm + bands - 1) / bands;
-        const int band = id / (h * gn), hb = gm - band * h < h ? gm - band * h : h;
-        const int c = id - band * h * gn;
+        const int band = (int)(id / (h * gn)), hb = gm - band * h < h ? gm - band * h : h;
+        const int c = (int)(id % (h * gn));
         n0 = (int64_t)(c / hb) * U::BN + q * P::BN;
         if (n0 >= wt.N) return;
         t.row0 = (int64_t)(band * h + c % hb) * U::BM;
@@ -403,14 +405,19 @@ hipError_t tile(const G4Weights& w, const Rows& a, hipStream_t s) {
     const int64_t gn = (w.N + U::BN - 1) / U::BN, tiles = gm * gn;
     const int64_t slots = 2 * gqk_cu_count(), tail = tiles % slots;
     const int64_t n_full = PARTS > 1 && !a.offsets && PARTS * tail <= slots ? tiles - tail : tiles;
-    const int64_t grid = n_full + PARTS * (tiles - n_full);
-    if (!grid_ok(grid, 256)) return hipErrorInvalidValue;
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_tile<T, MT, NT, PARTS>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_tile<T, MT, NT, PARTS>),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_g4_tile<T, MT, NT, PARTS>), dim3((unsigned)grid), dim3(256), U::BYTES, s, w, a, (int)gm,
-                       (int)gn, (int)n_full);
-    return hipGetLastError();
+    int64_t first = 0;
+    do {
+        const int64_t here = n_full - first < MOST_GROUPS ? n_full - first : MOST_GROUPS;
+        const int64_t grid = here + (first + here == n_full ? PARTS * (tiles - n_full) : 0);
+        hipLaunchKernelGGL((k_g4_tile<T, MT, NT, PARTS>), dim3((unsigned)grid), dim3(256), U::BYTES, s, w, a, (int)gm,
+                           (int)gn, (int)here, first);
+        e = hipGetLastError();
+        first += here;
+    } while (e == hipSuccess && first < n_full);
+    return e;
 }
 
 template <typename X, bool ZP, int G, int NT, int W, int XR>

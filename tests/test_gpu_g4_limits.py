@@ -1,0 +1,112 @@
+"""GPU: calls of the 4-bit products with more tiles than one launch has workgroups
+for (2^24 of 256 threads), on integers whose results are exact."""
+from __future__ import annotations
+
+import sys
+
+import pytest
+import torch
+
+from tests.test_gpu_g4_products import ends_of, gen, poisoned
+from tests.test_gpu_g4_shapes import ends
+
+pytestmark = pytest.mark.gpu
+
+F32, BF, U8 = torch.float32, torch.bfloat16, torch.uint8
+
+
+@pytest.fixture(autouse=True)
+def _name_the_case(request):
+    print("\n[gpu case] %s" % request.node.nodeid, flush=True)
+    sys.stdout.flush()
+    torch.cuda.empty_cache()
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
+@pytest.fixture(scope="module")
+def gq():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import block_quantized_weight_q4_amd as g
+    return g
+
+
+def ints(g, *shape, dt=BF):
+    return torch.randint(-2, 3, shape, generator=g, device="cuda", dtype=torch.int8).to(dt)
+
+
+@pytest.mark.parametrize("M", [2 ** 30 + 77, 2 ** 30 + 64 * 2 ** 21 + 1])
+def test_dx_of_the_most_rows(gq, M):
+    """One matrix of 3 rows: 2^24 tiles of 64 rows and more, dX of 69 GB and more.  Sums of 3 * 2 * 15 halves have 7 bits."""
+    N, K = 3, 32
+    g = gen(M)
+    W = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=U8)
+    s = torch.full((N, 1), 0.5, dtype=BF, device="cuda")
+    z = torch.tensor([[3], [0], [15]], device="cuda", dtype=U8)
+    dy = ints(g, M, N)
+    dx = gq.gq_g4_matmul_dx(W, s, dy, poisoned(M, K, dt=BF), zeros=z, group=32)
+    q = torch.stack([W & 15, W >> 4], 2).view(N, K).float()
+    w = 0.5 * (q - z.float())
+    step = 1 << 24
+    for r in range(0, M, step):
+        d = dy[r:r + step].float()
+        ref = d[:, :1] * w[0] + d[:, 1:2] * w[1] + d[:, 2:] * w[2]
+        assert torch.equal(dx[r:r + step], ref.to(BF)), r
+
+
+@pytest.mark.parametrize("N", [1, 8])  # through registers, copied
+def test_dx_of_experts_with_the_longest_rows(gq, N):
+    """1090 experts with a row or two of 4,194,304 columns: 17.9 million tiles."""
+    E, K, G = 1100, 4194304, 128
+    counts = [1] * E
+    counts[0], counts[700], counts[E - 1] = 3, 0, 2
+    counts[5:14] = [0] * 9
+    M = sum(counts) + 2
+    g = gen(N)
+    W = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=U8)
+    s = (2.0 ** torch.randint(-2, 2, (E, N, 1), generator=g, device="cuda")).to(BF).repeat(1, 1, K // G)
+    off = ends_of(counts, M)
+    dy = ints(g, M, N)
+    dx = poisoned(M, K, dt=BF)
+    gq.gq_g4_matmul_dx(W, s, dy, dx, group=G, offsets=off)
+    e = torch.repeat_interleave(torch.arange(E), torch.tensor(counts)).cuda()  # of each row
+    assert dx[e.numel():].isnan().all()
+    at = ends(K)
+    for r in range(0, e.numel(), 64):
+        er = e[r:r + 64]
+        b = W[er][:, :, at // 2]
+        q = torch.where(at % 2 == 0, b & 15, b >> 4).double()
+        ref = ((q - 8) * s[er, :, :1].double() * dy[r:r + er.numel(), :, None].double()).sum(1)
+        assert torch.equal(dx[r:r + er.numel(), at], ref.to(BF)), r
+        assert not dx[r:r + er.numel()].isnan().any()
+
+
+def test_product_of_experts_with_the_most_columns(gq):
+    """4096 experts of 1,048,576 columns, a row each but for two: 17.0 million tiles, weights of 69 GB."""
+    E, N, K, M = 4096, 1048576, 32, 4098
+    counts = [1] * E
+    counts[1], counts[E - 1] = 0, 2
+    g = gen(17)
+    some = torch.randint(0, 256, (64, N, K // 2), generator=g, device="cuda", dtype=U8)
+    W = torch.empty(E, N, K // 2, dtype=U8, device="cuda")
+    for e in range(0, E, 64):
+        W[e:e + 64] = some ^ (e // 64 * 37 % 256)
+    del some
+    s = (2.0 ** torch.randint(-2, 2, (E, 1, 1), generator=g, device="cuda")).to(BF).repeat(1, N, 1)
+    x = ints(g, M, K)
+    y = gq.gq_g4_matmul(W, s, x, poisoned(M, N, dt=BF), group=32, offsets=ends_of(counts, M))
+    e = torch.repeat_interleave(torch.arange(E), torch.tensor(counts)).cuda()
+    assert y[e.numel():].isnan().all()
+    at = ends(N, 8)
+
+    def check(r, n):  # rows r at columns n
+        b = W[e[r]][:, n] if isinstance(n, slice) else W[e[r][:, None], n]
+        q = torch.stack([b & 15, b >> 4], 3).view(*b.shape[:2], K).float()
+        ref = ((q - 8) * x[r, None].float()).sum(2) * s[e[r], :1, 0].float()  # (exact: integers below 2^11)
+        assert torch.equal(y[r][:, n], ref.to(BF))
+    for r in torch.arange(e.numel(), device="cuda").split(64):
+        check(r, at)
+    for r in (0, 1, 2047, 2048, 4094, 4095):
+        assert not y[r].isnan().any()
+        check(torch.tensor([r], device="cuda"), slice(0, N))
