@@ -28,9 +28,21 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 // 16-bit element types of the products' inputs.
+//
+// Weights that are rounded to them are formed as fma(q 2^-9, a, b): a nibble as an e4m3
+// byte is q 2^-9 (subnormal below 8, the first normal binade from 8 on), which one
+// instruction converts two at a time.  affine() gives a and b of a scale and its zero
+// point; the fma is exact in fp32 (16 bits), so the rounding to 16 bits is the only one.
+// UNIT: what a sum of such weights is multiplied with.
 struct Bf16 {
     typedef bf16x8 x8;
     static constexpr int dtype = gqd::DT_BF16;
+    // 2^-9 of the weights: a scale times 512 would be infinite from 2^119 on.  (Weights
+    // below 2^-117 are subnormal bf16 numbers so.)
+    static constexpr float UNIT = 512.0f;
+    static __device__ __forceinline__ gqf8::f32x2 affine(float s, uint32_t z) {
+        return gqf8::f32x2{s, (float)z * -0x1p-9f * s};
+    }
     static __device__ __forceinline__ uint16_t narrow(float v) { return gqd::f2bf(v); }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
@@ -45,6 +57,14 @@ struct Bf16 {
 struct F16 {
     typedef f16x8 x8;
     static constexpr int dtype = gqd::DT_F16;
+    // The weights themselves: fp16 has no range to spare.  A finite scale above 2^112 becomes
+    // that, so that no product overflows: its weights are zeros or infinite either way.
+    static constexpr float UNIT = 1.0f;
+    static __device__ __forceinline__ gqf8::f32x2 affine(float s, uint32_t z) {
+        const float m = __builtin_fabsf(s);
+        if (m > 0x1p112f && m < __builtin_inff()) s = __builtin_copysignf(0x1p112f, s);
+        return gqf8::f32x2{512.0f * s, -(float)z * s};
+    }
     static __device__ __forceinline__ uint16_t narrow(float v) { return gqd::f2h(v); }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
@@ -60,6 +80,16 @@ struct F16 {
 __device__ __forceinline__ float scale_f32(uint32_t bits16, int s_f16) {
     const float h = gqd::h2f(bits16), b = gqd::bf2f((uint16_t)bits16);
     return s_f16 ? h : b;
+}
+
+// Sums of weights in T's unit, as they are.
+template <typename T, typename V, int N = sizeof(V) / 4>
+__device__ __forceinline__ V in_unit(V v) {
+    if constexpr (T::UNIT != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= T::UNIT;
+    }
+    return v;
 }
 
 // Quants minus zero points of a dword's eight nibbles, as signed bytes: even

@@ -116,7 +116,7 @@ struct Tile {
                 for (int u = 0; u < XI; ++u) reinterpret_cast<u32x4*>(d + (wave + 4 * u) * 1024)[lane] = held[u];
             }
         };
-        // Scales: lane l has row n + l of the stage; as 512 s and -z s in LDS, [group][row].
+        // Scales: lane l has row n + l of the stage; as T::affine gives them in LDS, [group][row].
         float* panel = reinterpret_cast<float*>(smem + STAGES * STAGE + wave * SCALES);
         const int64_t kw = k0 + 64 * wn < K ? k0 + 64 * wn : K - 1;  // (columns past K are not stored)
         const int64_t g0 = kw / wt.group, g1 = wt.group == 32 && g0 + 1 < KG ? g0 + 1 : g0;
@@ -140,9 +140,10 @@ struct Tile {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 const float f = in ? scale_f32(c.s[g], wt.s_f16) : 0.0f;
+                const gqf8::f32x2 v = T::affine(f, wt.zeros ? c.z[g] & 15u : 8u);
                 float* p = panel + ((s & 1) * 2 + g) * (2 * BK) + 2 * lane;
-                p[0] = 512.0f * f;
-                p[1] = -(float)(wt.zeros ? c.z[g] & 15u : 8u) * f;
+                p[0] = v.x;
+                p[1] = v.y;
             }
         };
         f32x4 acc[4][MT];
@@ -156,7 +157,7 @@ struct Tile {
         const int wat = KS == 1 ? 8 * fq * 128 + (wn ^ fq) * 32 + 2 * fr : fq * 64 + wn * 32 + 2 * fr;
         const int gsel = wt.group == 32 ? fr >> 3 : 0;
         uint32_t w[4][2];  // the bytes of rows 2 i and 2 i + 1
-        f32x4 f[4];        // (512 s, -z s) of them
+        f32x4 f[4];        // (T::affine) of them
         auto read_raw = [&](int s, int buf, int h, int i) __attribute__((always_inline)) {
             const uint8_t* wd = smem + buf * STAGE + XB + HALF * h + wat;
             const f32x4* sp = reinterpret_cast<const f32x4*>(panel + ((s & 1) * 2 + gsel) * (2 * BK) +
@@ -285,6 +286,8 @@ struct Tile {
         for (int j = 0; j < MT; ++j) {
             const int row = 16 * j + fr;
             if (row >= rows) continue;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[t][j] = in_unit<T>(acc[t][j]);
             uint16_t* p = dx + (int64_t)row * lddx + k;
             if (vec) {
 #pragma unroll

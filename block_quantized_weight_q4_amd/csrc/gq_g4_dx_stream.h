@@ -27,8 +27,8 @@
 namespace gqg4 {
 
 // Weights of rows 2 i and 2 i + 1 of four neighbouring columns, as dword i of the
-// operands of those columns: w0, w1 their bytes (two a row), f (512 s, -z s) of the
-// two rows.  A nibble as an e4m3 byte is q 2^-9; s (q - z) is exact in fp32.
+// operands of those columns, in T's unit: w0, w1 their bytes (two a row), f (T::affine)
+// of the two rows.
 template <typename T>
 __device__ __forceinline__ void weights_2x4(uint32_t w0, uint32_t w1, f32x4 f, u32x4 (&a)[4], int i) {
     // (joined by a byte permute: a read into the upper half of a register waits for the lower one's)
@@ -88,7 +88,7 @@ __device__ __forceinline__ void dx_stream(const G4Weights& wt, const uint16_t* _
     const int64_t N = wt.N, K = wt.K, row_bytes = K / 2, KG = (K + wt.group - 1) / wt.group;
     const int NB = (int)((N + BR - 1) / BR);
     uint8_t* mine = smem + wave * S::ONE;
-    float* panel = reinterpret_cast<float*>(mine + S::WB);  // [group][row]: 512 s and -z s
+    float* panel = reinterpret_cast<float*>(mine + S::WB);  // [group][row]: T::affine
 
     // W: C / 2 bytes of 32 rows (64 of 32 columns) a copy, row 8 a + b of 32 at 4 b + a, so that
     // the four rows, 8 apart, that the lanes read at once lie in different banks
@@ -173,9 +173,10 @@ __device__ __forceinline__ void dx_stream(const G4Weights& wt, const uint16_t* _
 #pragma unroll
                 for (int g = 0; g < GROUPS; ++g) {
                     const float f = scale_f32(sc[h][g], wt.s_f16);
+                    const gqf8::f32x2 v = T::affine(f, zp[h][g] & 15u);
                     float* o = panel + g * (2 * BR) + 2 * (64 * h + lane);
-                    o[0] = 512.0f * f;
-                    o[1] = -(float)(zp[h][g] & 15u) * f;
+                    o[0] = v.x;
+                    o[1] = v.y;
                 }
             u32x4 x[H][MT];
 #pragma unroll
@@ -231,6 +232,7 @@ __device__ __forceinline__ void dx_stream(const G4Weights& wt, const uint16_t* _
         const int64_t k = k0 + 4 * NT * fq + 4 * (c % NT);
         const int row = 16 * (c / NT) + fr;
         if (row < rows && k < K) {  // (K is a multiple of 32)
+            v = in_unit<T>(v);
             const u32x2 o{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
             __builtin_memcpy(dx + row * lddx + k, &o, 8);
         }

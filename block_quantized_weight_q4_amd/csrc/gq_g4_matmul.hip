@@ -55,16 +55,13 @@ __global__ __launch_bounds__(64 * W) void k_g4_few(G4Weights wt, Rows a, int gn,
 constexpr int BK = 64;   // inputs of a stage
 constexpr int BAND = 4;  // row tiles of a band
 
-// Eight weights s (q - z) of a dword, rounded to 16 bits; s512 = 512 s, sz = -z s.
-// A nibble as an e4m3 byte is q 2^-9 (subnormal below 8, the first normal binade
-// from 8 on), which one instruction converts two at a time; s (q - z) is exact in
-// fp32 (16 bits), so the one rounding is the last.
+// Eight weights of a dword, rounded to 16 bits, in T's unit; s and sz as T::affine gives them.
 template <typename T>
-__device__ __forceinline__ typename T::x8 weights8(uint32_t w, float s512, float sz) {
+__device__ __forceinline__ typename T::x8 weights8(uint32_t w, float s, float sz) {
     const int lo = (int)(w & 0x0f0f0f0fu), hi = (int)((w >> 4) & 0x0f0f0f0fu);
     const gqf8::f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(lo, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(lo, true);
     const gqf8::f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8(hi, false), d = __builtin_amdgcn_cvt_pk_f32_fp8(hi, true);
-    auto f = [&](float q) { return __builtin_fmaf(q, s512, sz); };
+    auto f = [&](float q) { return __builtin_fmaf(q, s, sz); };
     return __builtin_bit_cast(typename T::x8, u32x4{T::pack(f(a.x), f(c.x)), T::pack(f(a.y), f(c.y)),
                                                    T::pack(f(b.x), f(d.x)), T::pack(f(b.y), f(d.y))});
 }
@@ -139,7 +136,7 @@ struct Tile {
         };
 
         // Scales: lane l < 32 NT has those of the column n0 + 32 NT wave + l, four groups
-        // at a time, and puts 512 s and -z s of the group in use into LDS (each wavefront
+        // at a time, and puts T::affine of the group in use into LDS (each wavefront
         // its own), where the lanes of the operand's rows read them.
         const int64_t sn = n0 + 32 * NT * wave + (lane < 32 * NT ? lane : 0);
         const int64_t srow = (sn < N ? sn : N - 1) * KG;
@@ -168,10 +165,7 @@ struct Tile {
         };
         // group g into LDS: behind the reads of the one before it (a wavefront's LDS operations keep their order)
         auto put_scales = [&](int g) __attribute__((always_inline)) {
-            const float f = scale_f32(four_a & 0xffffu, wt.s_f16);
-            gqf8::f32x2 v;
-            v.x = 512.0f * f;
-            v.y = -(float)(four_z & 15u) * f;
+            const gqf8::f32x2 v = T::affine(scale_f32(four_a & 0xffffu, wt.s_f16), four_z & 15u);
             if (lane < 32 * NT) panel[lane] = v;
             four_a = (four_a >> 16) | (four_b << 16);
             four_b >>= 16;
@@ -301,7 +295,7 @@ struct Tile {
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 const int64_t n = n0 + 32 * NT * wave + 32 * i + 16 * fq;
-                const f32x16 v = acc[i][j];
+                const f32x16 v = in_unit<T>(acc[i][j]);
                 if (y_f32) {
                     float* p = static_cast<float*>(y) + row * ldy + n;
 #pragma unroll

@@ -28,9 +28,10 @@
  *
  * Range.  A sum over a group is formed before its scale meets it; the
  * accuracies below hold for fp32 and bf16 inputs that are zero or from 2^-94 up
- * to below 2^112 and fp16 ones of any size, and where sums and results are
- * normal numbers of their type.  A NaN or infinite input or scale makes the
- * outputs that read it NaN or infinite; nothing else is affected by it.
+ * to below 2^112 and fp16 ones of any size, for finite scales of any size, and
+ * where sums and results are normal numbers of their type.  A NaN or infinite
+ * input or scale makes the outputs that read it NaN or infinite; nothing else is
+ * affected by it.
  */
 #ifndef GQ_G4_H
 #define GQ_G4_H
@@ -59,9 +60,9 @@ gq_status gq_g4_matvec(const void* W, const void* scales, gq_dtype s_dtype, cons
  * writes zeros.  Columns past N are not touched.
  * Accuracy.  GQ_F32: as gq_g4_matvec.  Y of X's type: that, or each weight
  * rounded to that type first (by the number of rows), i.e. within half its eps
- * (bf16 2^-8, fp16 2^-11, and 2^-25 |x| where a weight is below fp16's normal
- * numbers) times sum |w x| more; weights of 65520 and more are infinite then
- * in fp16. */
+ * (bf16 2^-8, fp16 2^-11) times sum |w x| more, and 2^-25 |x| where a weight is
+ * below fp16's normal numbers, 2^-125 |x| where one is below 2^-117 in bf16;
+ * weights of 65520 and more are infinite then in fp16. */
 gq_status gq_g4_matmul(const void* W, const void* scales, gq_dtype s_dtype, const void* zeros, int32_t group,
                        int64_t N, int64_t K, const void* X, gq_dtype x_dtype, int64_t M, int64_t ldx, void* Y,
                        gq_dtype y_dtype, int64_t ldy, int32_t n_experts, const int32_t* offsets,
