@@ -1,5 +1,6 @@
 """GPU: calls of the 4-bit products with more tiles than one launch has workgroups
-for (2^24 of 256 threads), on integers whose results are exact."""
+for (2^24 of 256 threads), on integers whose results are exact; offsets that are
+none, at the sizes that take tiles."""
 from __future__ import annotations
 
 import sys
@@ -7,7 +8,7 @@ import sys
 import pytest
 import torch
 
-from tests.test_gpu_g4_products import ends_of, gen, poisoned
+from tests.test_gpu_g4_products import ends_of, gen, poisoned, weights
 from tests.test_gpu_g4_shapes import ends
 
 pytestmark = pytest.mark.gpu
@@ -110,3 +111,31 @@ def test_product_of_experts_with_the_most_columns(gq):
     for r in (0, 1, 2047, 2048, 4094, 4095):
         assert not y[r].isnan().any()
         check(torch.tensor([r], device="cuda"), slice(0, N))
+
+
+def inside(t, rows):
+    """t between `rows` rows (whole 16 bytes) of 7 (results) or NaN (operands) on each side: the whole, and the part that is t."""
+    full = torch.full((t.shape[0] + 2 * rows, t.shape[1]), 7.0 if t.isnan().all() else float("nan"), dtype=t.dtype,
+                      device="cuda")
+    part = full[rows:rows + t.shape[0]]
+    return full, part.copy_(t) if not t.isnan().all() else part
+
+
+# tiles of 128 rows and of 64; gradients in tiles of 64 with the sum in halves, of 128, of 64 through registers, of 32
+@pytest.mark.parametrize("grad,M,N,K,E", [(False, 3000, 1000, 160, 4), (False, 3000, 1000, 96, 60), (True, 3000, 72, 512, 4),
+                                          (True, 9000, 72, 512, 4), (True, 9000, 73, 544, 4), (True, 3000, 72, 544, 300)])
+def test_offsets_that_are_none_of_many_rows(gq, grad, M, N, K, E):
+    """Decreasing, overlapping, negative and too large offsets: nothing beside X is read, nothing beside Y written."""
+    g = gen(M, N, E)
+    W, s, z = weights(g, (E,), N, K, 32)
+    kinds = [torch.linspace(M, 0, E + 1), torch.arange(E + 1) % 2 * M, torch.arange(E + 1) % 3 * 2.0 ** 30 - 2.0 ** 30,
+             torch.randint(-M, 2 * M, (E + 1,), generator=torch.Generator().manual_seed(M)),
+             torch.full((E + 1,), 2.0 ** 31 - 128)]
+    for i, off in enumerate(kinds):
+        off = off.to(torch.int64).to(torch.int32).cuda()
+        _, x = inside(torch.randn(M, N if grad else K, generator=g, device="cuda").to(BF), 304)
+        full, y = inside(poisoned(M, K if grad else N, dt=BF), 304)
+        (gq.gq_g4_matmul_dx if grad else gq.gq_g4_matmul)(W, s, x, y, zeros=z, group=32, offsets=off)
+        assert (full[:304] == 7.0).all() and (full[-304:] == 7.0).all() and full.isfinite().all(), i
+        if i in (0, 4):  # no expert has rows
+            assert (full == 7.0).all()
