@@ -92,7 +92,7 @@ struct Tile {
 
     // x: first row of the tile; n0: first column
     static __device__ __forceinline__ void run(const G4Weights& wt, const uint16_t* __restrict__ x, int64_t ldx,
-                                               int rows, void* __restrict__ y, int64_t ldy, int y_f32, int64_t n0,
+                                               int rows, uint16_t* __restrict__ y, int64_t ldy, int64_t n0,
                                                uint8_t* smem) {
         const int lane = threadIdx.x & 63;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -296,32 +296,17 @@ struct Tile {
             for (int i = 0; i < NT; ++i) {
                 const int64_t n = n0 + 32 * NT * wave + 32 * i + 16 * fq;
                 const f32x16 v = in_unit<T>(acc[i][j]);
-                if (y_f32) {
-                    float* p = static_cast<float*>(y) + row * ldy + n;
+                uint16_t* p = y + row * ldy + n;
 #pragma unroll
-                    for (int r = 0; r < 16; r += 4) {
-                        if (n + r + 4 <= N) {
-                            const f32x4 o{v[r], v[r + 1], v[r + 2], v[r + 3]};
-                            __builtin_memcpy(p + r, &o, 16);
-                        } else {
+                for (int r = 0; r < 16; r += 8) {
+                    if (n + r + 8 <= N) {
+                        const u32x4 o{T::pack(v[r], v[r + 1]), T::pack(v[r + 2], v[r + 3]),
+                                      T::pack(v[r + 4], v[r + 5]), T::pack(v[r + 6], v[r + 7])};
+                        __builtin_memcpy(p + r, &o, 16);  // (of any alignment)
+                    } else {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (n + r + e < N) p[r + e] = v[r + e];
-                        }
-                    }
-                } else {
-                    uint16_t* p = static_cast<uint16_t*>(y) + row * ldy + n;
-#pragma unroll
-                    for (int r = 0; r < 16; r += 8) {
-                        if (n + r + 8 <= N) {
-                            const u32x4 o{T::pack(v[r], v[r + 1]), T::pack(v[r + 2], v[r + 3]),
-                                          T::pack(v[r + 4], v[r + 5]), T::pack(v[r + 6], v[r + 7])};
-                            __builtin_memcpy(p + r, &o, 16);  // (of any alignment)
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (n + r + e < N) p[r + e] = T::narrow(v[r + e]);
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            if (n + r + e < N) p[r + e] = T::narrow(v[r + e]);
                     }
                 }
             }
@@ -372,24 +357,23 @@ __global__ __launch_bounds__(256, 2) void k_g4_tile(G4Weights wt, Rows a, int gm
     }
     const G4Weights w = of_expert(wt, t.e);
     const uint16_t* x = static_cast<const uint16_t*>(a.X) + t.row0 * a.ldx;
-    void* y = a.y_f32 ? static_cast<void*>(static_cast<float*>(a.Y) + t.row0 * a.ldy)
-                      : static_cast<void*>(static_cast<uint16_t*>(a.Y) + t.row0 * a.ldy);
+    uint16_t* y = static_cast<uint16_t*>(a.Y) + t.row0 * a.ldy;
     if constexpr (PARTS > 1) {
         if (part) {
-            P::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
+            P::run(w, x, a.ldx, t.rows, y, a.ldy, n0, smem);
             return;
         }
         // an expert's last rows
         if (a.offsets && t.rows <= 64) {
-            Tile<T, 2, NT>::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
+            Tile<T, 2, NT>::run(w, x, a.ldx, t.rows, y, a.ldy, n0, smem);
             return;
         }
         if (a.offsets && t.rows <= 96) {
-            Tile<T, 3, NT>::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
+            Tile<T, 3, NT>::run(w, x, a.ldx, t.rows, y, a.ldy, n0, smem);
             return;
         }
     }
-    U::run(w, x, a.ldx, t.rows, y, a.ldy, a.y_f32, n0, smem);
+    U::run(w, x, a.ldx, t.rows, y, a.ldy, n0, smem);
 }
 
 template <typename T, int MT, int NT, int PARTS>
