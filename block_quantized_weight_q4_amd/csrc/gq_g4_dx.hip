@@ -31,8 +31,8 @@ struct Rows {
 };
 
 // Bound by forming the weights and by the wait at each stage, matrix cores busy 34% of
-// the time: 24,120 rows of 128 experts, 704 x 2816, in 147 to 151 us (640 TFLOP/s), 3015 x
-// 17408 x 5120 in 539 us (1.0 PFLOP/s, where there are 272 stages).  32 x 32 instructions,
+// the time: 24,120 rows of 128 experts, 704 x 2816, in 145 to 152 us (640 TFLOP/s), 3015 x
+// 17408 x 5120 in 522 to 539 us (1.0 PFLOP/s, where there are 272 stages).  32 x 32 instructions,
 // which gained a sixth in the product, would leave a lane two columns instead of four,
 // with twice the reads of LDS.
 //
@@ -372,7 +372,7 @@ hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
     using U = DxStream<MT, W, H, C>;
     const int64_t gm = a.offsets ? most_tiles(a.M, a.n_experts, U::BM) : (a.M + U::BM - 1) / U::BM;
     const int64_t gn = (w.K + U::BN - 1) / U::BN;
-    if (!grid_ok(gm * gn, 64 * W)) return hipErrorInvalidValue;  // (never: at most four times the groups counted below)
+    if (!grid_ok(gm * gn, 64 * W)) return hipErrorInvalidValue;  // (never: at most four times the groups below)
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_g4_dx_few<T, MT, W, H, C>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
     if (e != hipSuccess) return e;

@@ -72,14 +72,14 @@ __device__ __forceinline__ typename T::x8 weights8(uint32_t w, float s, float sz
 // to LDS as they are in memory: X in stages of 64 inputs, W in blocks of two stages
 // (64 bytes a row).
 //
-// Bound by the matrix cores and what they are fed with: 3015 x 17408 x 5120 takes 466 to
-// 484 us (1.11 to 1.15 PFLOP/s; a library's product of the same rows with expanded
+// Bound by the matrix cores and what they are fed with: 3015 x 17408 x 5120 takes 449 to
+// 484 us (1.11 to 1.20 PFLOP/s; a library's product of the same rows with expanded
 // weights 505, of 8192^3 1.13 to 1.33 PFLOP/s, depending on the card and its heat), with
 // the matrix cores busy 72% of the time and 60% of the issue cycles spent on expanding
 // (20 instructions for eight weights).  Two workgroups a CU hide each other's starts and
 // ends; eight wavefronts in one, 16 x 16 instructions (576 us) and two barriers a stage
 // (703 us) were slower.  Short sums are bound by those starts and by the stores: 24,120
-// rows of 128 experts, 2816 x 704 (11 stages a tile), 141 to 147 us, 650 to 680 TFLOP/s.
+// rows of 128 experts, 2816 x 704 (11 stages a tile), 136 to 147 us, 650 to 700 TFLOP/s.
 template <typename T, int MT, int NT>
 struct Tile {
     static constexpr int NW = 4, XS = 2;  // wavefronts, stages of X
@@ -450,10 +450,17 @@ hipError_t few(const G4Weights& w, const Rows& a, hipStream_t s) {
 // 92 us in tiles with 256 to 1024 rows, streamed 39 to 115, with 768 rows 95 and 92;
 // 17408 x 5120 with 64 rows 56 and 38, with 128 51 and 65, with 256 70 and 110; 4096 x
 // 4096 with 400 rows 41 and 42, with 600 42 and 58; 2816 x 2816 of 8 experts with 600 rows
-// 41 and 40, with 1000 41 and 58; 704 x 2816 of 128 with 1024 51 and 45, with 4096 57 and
-// 87.  Narrow matrices leave most of a tile's 256 columns empty.  (fp32 results carry no
-// rounded weights, and exact ones take the streamed form at any size: 3015 x 17408 x 5120
-// in 1.13 ms.)
+// 41 and 40, with 1000 41 and 58.  With many experts the two meet near 1.5 million results
+// too, whatever the rows of each, and near 0.7 million where sums are short: 704 x 2816 of
+// 128 with 1024 rows 51 and 41, with 2048 53 and 54, with 4096 58 and 81; 2816 x 704 of 128
+// with 128 rows 32 and 28, with 512 47 and 54 (the rule streams these), with 620 48 and 55,
+// with 1024 50 and 61, with 2048 53 and 80; 1408 x 2816 of 64 with 620 rows 51 and 42, with
+// 1024 53 and 51, with 2048 56 and 75; 14336 x 4096 of 8 with 64 rows 80 and 66, with 128
+// 81 and 84, with 256 88 and 128; 4096 x 14336 of 8 with 256 171 and 146, with 512 174 and
+// 222.  Narrow matrices leave most of a tile's
+// 256 columns empty.  (fp32 results carry no rounded weights, and exact ones take the
+// streamed form at any size: 3015 x 17408 x 5120 in 1.13 ms, 24,120 rows of 128 experts,
+// 2816 x 704, in 326 us.)
 template <typename X, typename T>
 hipError_t matmul(const G4Weights& w, const Rows& a, hipStream_t s) {
     if (a.y_f32 || w.N < 128 || a.M * w.N < 1700000) return w.zeros ? few<X, true>(w, a, s) : few<X, false>(w, a, s);

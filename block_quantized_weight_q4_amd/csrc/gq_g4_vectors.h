@@ -43,7 +43,9 @@ hipError_t vectors(const G4Weights& w, const void* x, int batch, void* y, int y_
 // Rows of W a workgroup and wavefronts: 32 rows read X half as often as 16 (34816 x
 // 5120, 16 bf16 vectors: 32 and 39 us), but below 4096 rows 16 make more workgroups
 // (2560 x 9728, 8 vectors: 7.1 and 10.1 us) and up to 4 vectors have little X to read
-// (19456 x 2560, 1 vector: 8.9 and 9.9 us).  Up to 8192 rows eight wavefronts a
+// (19456 x 2560, 1 vector: 8.9 and 9.9 us).  5120 rows, which 16 would spread over all
+// CUs, take 32 too (5120 x 17408, 8 vectors: 14.8 and 15.8 us, 16 vectors: 16.8 and 20.3;
+// from HBM alone 18.2 and 21.9 with 8).  Up to 8192 rows eight wavefronts a
 // workgroup (5120 x 17408, 8 vectors: 18.4 us, with four 19.3; 2560 x 9728, 1 vector:
 // 6.6, 9.1), above that four, each with more blocks (19456 x 2560, 16 vectors: 13 us,
 // with eight 18).

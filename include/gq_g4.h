@@ -62,7 +62,8 @@ gq_status gq_g4_matvec(const void* W, const void* scales, gq_dtype s_dtype, cons
  * rounded to that type first (by the number of rows), i.e. within half its eps
  * (bf16 2^-8, fp16 2^-11) times sum |w x| more, and 2^-25 |x| where a weight is
  * below fp16's normal numbers, 2^-125 |x| where one is below 2^-117 in bf16;
- * weights of 65520 and more are infinite then in fp16. */
+ * weights of 65520 and more are infinite then in fp16.  Who needs the weights as
+ * they are whatever the number of rows takes GQ_F32 results. */
 gq_status gq_g4_matmul(const void* W, const void* scales, gq_dtype s_dtype, const void* zeros, int32_t group,
                        int64_t N, int64_t K, const void* X, gq_dtype x_dtype, int64_t M, int64_t ldx, void* Y,
                        gq_dtype y_dtype, int64_t ldy, int32_t n_experts, const int32_t* offsets,

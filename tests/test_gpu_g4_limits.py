@@ -39,7 +39,8 @@ def ints(g, *shape, dt=BF):
 
 @pytest.mark.parametrize("M", [2 ** 30 + 77, 2 ** 30 + 64 * 2 ** 21 + 1])
 def test_dx_of_the_most_rows(gq, M):
-    """One matrix of 3 rows: 2^24 tiles of 64 rows and more, dX of 69 GB and more.  Sums of 3 * 2 * 15 halves have 7 bits."""
+    """One matrix of 3 rows: 2^24 tiles of 64 rows and more, dX of 69 GB and more.  Sums of 3 * 2 * 15 halves have
+    7 bits."""
     N, K = 3, 32
     g = gen(M)
     W = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=U8)
@@ -114,7 +115,8 @@ def test_product_of_experts_with_the_most_columns(gq):
 
 
 def inside(t, rows):
-    """t between `rows` rows (whole 16 bytes) of 7 (results) or NaN (operands) on each side: the whole, and the part that is t."""
+    """t between `rows` rows (whole 16 bytes) of 7 (results) or NaN (operands) on each side: the whole, and the part
+    that is t."""
     full = torch.full((t.shape[0] + 2 * rows, t.shape[1]), 7.0 if t.isnan().all() else float("nan"), dtype=t.dtype,
                       device="cuda")
     part = full[rows:rows + t.shape[0]]
