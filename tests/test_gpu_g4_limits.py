@@ -141,3 +141,47 @@ def test_offsets_that_are_none_of_many_rows(gq, grad, M, N, K, E):
         assert (full[:304] == 7.0).all() and (full[-304:] == 7.0).all() and full.isfinite().all(), i
         if i in (0, 4):  # no expert has rows
             assert (full == 7.0).all()
+
+
+MOST_ROWS = 2 ** 31 - 256
+
+
+def in_chunks(M, K, g):
+    x = torch.empty(M, K, dtype=BF, device="cuda")
+    for r in range(0, M, 1 << 25):
+        x[r:r + (1 << 25)] = ints(g, min(1 << 25, M - r), K)
+    return x
+
+
+def small_weights(g, lead, N, K):
+    W = torch.randint(0, 256, (*lead, N, K // 2), generator=g, device="cuda", dtype=U8)
+    w = 0.5 * (torch.stack([W & 15, W >> 4], -1).view(*lead, N, K).float() - 8)
+    return W, torch.full((*lead, N, 1), 0.5, dtype=BF, device="cuda"), w
+
+
+@pytest.mark.parametrize("N,ydt", [(1, F32), (17, BF)])
+def test_product_of_the_most_rows(gq, N, ydt):
+    K, g = 32, gen(N)
+    W, s, w = small_weights(g, (), N, K)
+    x = in_chunks(MOST_ROWS, K, g)
+    y = gq.gq_g4_matmul(W, s, x, poisoned(MOST_ROWS, N, dt=ydt), group=32)
+    for r in range(0, MOST_ROWS, 1 << 24):
+        assert torch.equal(y[r:r + (1 << 24)], (x[r:r + (1 << 24)].float() @ w.t()).to(ydt)), r
+
+
+@pytest.mark.parametrize("N,E", [(1, 1), (8, 128)])  # in tiles of 64 rows, of 128
+def test_dx_of_the_most_rows_there_can_be(gq, N, E):
+    K, g = 32, gen(N, E)
+    lead = () if E == 1 else (E,)
+    W, s, w = small_weights(g, lead, N, K)
+    dy = in_chunks(MOST_ROWS, N, g)
+    counts = [MOST_ROWS // E + (37 if e % 2 else -37) for e in range(E)] if E > 1 else [MOST_ROWS]
+    off = None if E == 1 else ends_of(counts, MOST_ROWS)
+    dx = gq.gq_g4_matmul_dx(W, s, dy, poisoned(MOST_ROWS, K, dt=BF), group=32, offsets=off)
+    r = 0
+    for e, n in enumerate(counts):
+        we = w if E == 1 else w[e]
+        for a in range(r, r + n, 1 << 24):
+            b = min(a + (1 << 24), r + n)
+            assert torch.equal(dx[a:b], (dy[a:b].float() @ we).to(BF)), (e, a)
+        r += n
